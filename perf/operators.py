@@ -1,0 +1,462 @@
+"""Measured cases of the gated linear recurrence and of the AdamW step.
+
+The recurrence solves the lower bidiagonal system (I - S diag(a)) h = b along
+a sequence, and its backward pass the transposed one:
+
+  linear    h_t = a_t h_{t-1} + x_t                     (gate = a)
+  sigmoid   h_t = a_t h_{t-1} + (1 - a_t) x_t           (a = sigma(gate))
+  backward  lambda_t = dL/dh_t + mu_{t+1},  mu_t = a_t lambda_t,
+            mu after the last step = dL/dh_last, dL/dh_0 = mu_1
+
+The AdamW step runs over many tensors at once,
+
+  m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g^2,
+  p' = p (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps),
+
+with m and v held in 32 bits, or in 8 bits per element with a 16-bit base per
+block of 256 (three mantissa bits, rounded stochastically by a hash of seed,
+step and element index).
+
+``own`` false: elementary torch operations in 32 bits, rounded once at the
+end; ``own`` true: the library's entry points.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda:0"
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+BYTES = {"f32": 4, "bf16": 2, "f16": 2}
+BLOCK = 256
+B1, B2, EPS, LR, WD = 0.9, 0.999, 1e-8, 1e-3, 0.01
+STEP, SEED = 1000, 20260
+
+
+# ----- cases -----
+
+def listed():
+    return [
+        # serving: one step of 16 sequences, the smallest call (latency)
+        rec("rec_step_bf16", "fwd", "bf16", "sigmoid", 16, 1, 4096, h0=True),
+        # odd everything, no initial state: a bidiagonal system per channel of a small field
+        rec("rec_odd_f32_train", "train", "f32", "linear", 3, 1001, 77, h0=False),
+        # prefill of four prompts from slices of one fused projection (strided inputs)
+        rec("rec_prefill_bf16", "fwd", "bf16", "sigmoid", 4, 4096, 4096, h0=False, fused=True),
+        # an ordinary training step
+        rec("rec_train_bf16", "train", "bf16", "sigmoid", 8, 2048, 2048, h0=True),
+        # packed documents of very different lengths, empty and one-step ones among them
+        rec("rec_packed_bf16_train", "train", "bf16", "sigmoid", 120, 100_003, 1024, h0=True,
+            packed=True),
+        # one long sequence of few channels in full precision: all the parallelism is in time
+        rec("rec_long_f32_train", "train", "f32", "linear", 1, 65_536, 512, h0=True),
+        # one very long sequence, forward
+        rec("rec_long_f16", "fwd", "f16", "sigmoid", 1, 262_144, 1024, h0=True),
+        # a small model: few small tensors (latency)
+        adam("adam_small_f32", "f32", "f32", 32, 24, 60_000),
+        # an ordinary model's many tensors, 32-bit states
+        adam("adam_f32", "f32", "f32", 32, 290, 120_000_000),
+        # bf16 gradients into f32 parameters, 8-bit states, and the states' values read back
+        adam("adam_8bit", "f32", "bf16", 8, 150, 60_000_000),
+        # bf16 parameters (stochastically rounded), 8-bit states, tensors packed without padding
+        adam("adam_8bit_bf16_packed", "bf16", "bf16", 8, 61, 9_000_001, pack=1),
+        # the largest step: 32-bit states
+        adam("adam_f32_bf16grad_large", "f32", "bf16", 32, 400, 400_000_000),
+    ]
+
+
+def rec(name, do, dtype, mode, seqs, steps, dim, h0=True, fused=False, packed=False):
+    c = {"op": "rec", "do": do, "dtype": dtype, "mode": mode, "seqs": seqs, "steps": steps,
+         "dim": dim, "h0": h0, "fused": fused, "packed": packed}
+    return dict(c, name=name) if name else c
+
+
+def adam(name, param, grad, bits, tensors, total, pack=BLOCK):
+    c = {"op": "adam", "param": param, "grad": grad, "bits": bits, "tensors": tensors,
+         "total": total, "pack": pack}
+    return dict(c, name=name) if name else c
+
+
+def log_int(rng, lo, hi):
+    return max(lo, min(hi, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    if rng.random() < 0.6:
+        do = rng.choice(["fwd", "train"])
+        elems = 268_435_456 if do == "fwd" else 67_108_864
+        dim = log_int(rng, 16, 8192)
+        if rng.random() < 0.6:
+            dim = max(8, dim // 8 * 8)
+        packed = rng.random() < 0.3
+        steps = log_int(rng, 1, min(262_144, elems // dim))
+        seqs = log_int(rng, 1, min(256, steps if packed else elems // dim // steps))
+        return rec(None, do, rng.choice(list(DTYPES)), rng.choice(["sigmoid", "linear"]), seqs,
+                   steps, dim, rng.random() < 0.6, rng.random() < 0.3, packed)
+    param, grad = rng.choice([("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+    total = log_int(rng, 2000, 100_000_000)
+    return adam(None, param, grad, rng.choice([32, 8]), log_int(rng, 1, min(300, total // 8)),
+                total, rng.choice([BLOCK, BLOCK, 1]))
+
+
+# ----- inputs -----
+
+def generator(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def lengths(case, seed):
+    """Packed sequences' lengths: from empty to many times the mean."""
+    r = np.random.RandomState(seed % (1 << 31))
+    w = r.exponential(1.0, case["seqs"]) ** 2
+    if case["seqs"] > 3:
+        w[1] = 0.0
+    n = np.floor(w / w.sum() * case["steps"]).astype(np.int64)
+    if case["seqs"] > 3:
+        n[2] = 1
+    n[int(np.argmax(n))] += case["steps"] - n.sum()
+    return n
+
+
+def rec_inputs(case, seed):
+    """Gate logits of mean 1.5 (or coefficients up to 0.98), unit inputs."""
+    g, dt = generator(seed), DTYPES[case["dtype"]]
+    lead = (case["steps"],) if case["packed"] else (case["seqs"], case["steps"])
+    d = case["dim"]
+    both = torch.randn(*lead, 2 * d, device=DEV, generator=g, dtype=torch.float32)
+    if case["mode"] == "sigmoid":
+        both[..., d:].mul_(1.5).add_(1.5)
+    else:
+        both[..., d:].sigmoid_().mul_(1.28).sub_(0.3)
+    both = both.to(dt)
+    x, gate = both[..., :d], both[..., d:]
+    if not case["fused"]:
+        x, gate = x.contiguous(), gate.contiguous()
+    s = {"case": case, "x": x, "gate": gate, "h0": None, "offsets": None, "dh": None,
+         "dlast": None}
+    if case["h0"]:
+        s["h0"] = torch.randn(case["seqs"], d, device=DEV, generator=g)
+    if case["packed"]:
+        n = lengths(case, seed)
+        s["offsets"] = torch.from_numpy(np.concatenate([[0], np.cumsum(n)])).to(DEV)
+        s["longest"] = int(n.max())
+    if case["do"] == "train":
+        s["dh"] = torch.randn(*lead, d, device=DEV, generator=g, dtype=torch.float32).to(dt)
+        s["dlast"] = torch.randn(case["seqs"], d, device=DEV, generator=g)
+    return s
+
+
+def sizes(case):
+    """Tensor sizes: a few large ones among many small, odd ones too."""
+    r = np.random.RandomState(case["total"] % 65_536 + case["tensors"])
+    w = r.lognormal(0.0, 2.0, case["tensors"])
+    n = np.maximum(1, np.floor(w / w.sum() * (case["total"] - case["tensors"]))).astype(np.int64)
+    n[n > 4096] &= ~7
+    n[int(np.argmax(n))] += case["total"] - n.sum()
+    return [int(v) for v in n]
+
+
+def starts(ns, pack):
+    at = np.concatenate([[0], np.cumsum([-(-n // pack) * pack for n in ns])])
+    return [int(v) for v in at]
+
+
+def adam_inputs(case, seed):
+    """A model in mid-training: heavy-tailed gradients, states near their running means."""
+    g, ns = generator(seed), sizes(case)
+    at, held = starts(ns, case["pack"]), starts(ns, BLOCK)
+    total, padded = at[-1], held[-1]
+    p = torch.randn(total, device=DEV, generator=g).mul_(0.02).to(DTYPES[case["param"]])
+    grad = torch.randn(total, device=DEV, generator=g).exp_().mul_(1e-3)
+    grad = grad.mul_(torch.randn(total, device=DEV, generator=g)).to(DTYPES[case["grad"]])
+    m = torch.randn(padded, device=DEV, generator=g).mul_(1e-3)
+    v = torch.randn(padded, device=DEV, generator=g).square_().mul_(2e-6)
+    real = torch.zeros(padded, dtype=torch.bool, device=DEV)
+    place = None
+    for n, h in zip(ns, held):
+        real[h:h + n] = True
+    if case["pack"] != BLOCK:
+        place = real.nonzero().flatten()
+    m.mul_(real)
+    v.mul_(real)
+    if case["bits"] == 8:  # values that the 8-bit form holds
+        m, v = level_down(m, 126), level_down(v, 254)
+    return {"case": case, "p": p, "grad": grad, "m": m, "v": v, "place": place, "ns": ns,
+            "at": at, "step": STEP}
+
+
+def level_down(x, top):
+    k = x.abs().view(torch.int32) >> 20
+    lowest = (k.view(-1, BLOCK).amax(1, keepdim=True) - top).clamp_(min=0)
+    k = torch.where(k.view(-1, BLOCK) > lowest, k.view(-1, BLOCK), 0).flatten()
+    return torch.copysign((k << 20).view(torch.float32), x)
+
+
+def prepare(case, seed):
+    if case["op"] == "rec":
+        return rec_inputs(case, seed)
+    s = adam_inputs(case, seed)
+    if own:
+        from preconditioned_cg_solver_amd import binding as B
+        pieces = [slice(a, a + n) for a, n in zip(s["at"], s["ns"])]
+        s["grads"] = [s["grad"][q] for q in pieces]
+        s["opt"] = B.sla_adamw_create([s["p"][q] for q in pieces], state_bits=case["bits"],
+                                      grad_dtype=DTYPES[case["grad"]])
+        B.sla_adamw_set_state(s["opt"], s["m"], s["v"])
+        s["m"] = s["v"] = None
+    return s
+
+
+# ----- one pass -----
+
+def run(state):
+    if state["case"]["op"] == "rec":
+        return rec_own(state) if own else rec_plain(state)
+    state["step"] += 1
+    return adam_own(state) if own else adam_plain(state)
+
+
+def rec_own(s):
+    from preconditioned_cg_solver_amd import binding as B
+    c = s["case"]
+    train = c["do"] == "train"
+    h, last, saved = B.sla_linrec_forward(s["x"], s["gate"], h0=s["h0"], offsets=s["offsets"],
+                                          mode=c["mode"], save=train)
+    if not train:
+        return {"h": h, "last": last}
+    dx, dgate, dh0 = B.sla_linrec_backward(s["x"], s["gate"], saved, s["dh"],
+                                           grad_last=s["dlast"], h0=s["h0"],
+                                           offsets=s["offsets"], mode=c["mode"])
+    return {"h": h, "last": last, "dx": dx, "dgate": dgate, "dh0": dh0}
+
+
+def scan(a, b, longest):
+    """b_t + a_t b_{t-1} + a_t a_{t-1} b_{t-2} + ... along dimension 1, by doubling."""
+    k = 1
+    while k < longest:
+        b = torch.cat([b[:, :k], b[:, k:] + a[:, k:] * b[:, :-k]], 1)
+        a = torch.cat([a[:, :k], a[:, k:] * a[:, :-k]], 1)
+        k *= 2
+    return b
+
+
+def rec_plain(s):
+    c, dt = s["case"], DTYPES[s["case"]["dtype"]]
+    x, gate = s["x"].float(), s["gate"].float()
+    if c["packed"]:
+        x, gate = x.unsqueeze(0), gate.unsqueeze(0)
+        off = s["offsets"]
+        some = off[1:] > off[:-1]
+        first, end, longest = off[:-1][some], off[1:][some] - 1, s["longest"]
+    else:
+        some, longest = slice(None), c["steps"]
+    h0 = s["h0"] if s["h0"] is not None else x.new_zeros(c["seqs"], c["dim"])
+    if c["mode"] == "sigmoid":
+        a, keep = torch.sigmoid(gate), torch.sigmoid(-gate)
+        b = keep * x
+    else:
+        a, b = gate.clone(), x.clone()
+    across = a.clone()  # the coefficient between t - 1 and t: none into a sequence's first step
+    if c["packed"]:
+        b[0, first] += a[0, first] * h0[some]
+        across[0, first] = 0
+    else:
+        b[:, 0] += a[:, 0] * h0
+        across[:, 0] = 0
+    h = scan(across, b, longest)
+    last = h0.clone()
+    last[some] = h[0, end] if c["packed"] else h[:, -1]
+    out = {"h": (h[0] if c["packed"] else h).to(dt), "last": last}
+    if c["do"] == "fwd":
+        return out
+    dh = s["dh"].float()
+    before = torch.cat([h[:, :1], h[:, :-1]], 1)
+    if c["packed"]:
+        dh = dh.unsqueeze(0).clone()
+        dh[0, end] += s["dlast"][some]
+        before[0, first] = h0[some]
+    else:
+        dh = dh.clone()
+        dh[:, -1] += s["dlast"]
+        before[:, 0] = h0
+    # lambda_t = dh_t + a_{t+1} lambda_{t+1}
+    back = torch.cat([across[:, 1:], across.new_zeros(across.shape[0], 1, c["dim"])], 1)
+    lam = scan(back.flip(1), dh.flip(1), longest).flip(1)
+    if c["mode"] == "sigmoid":
+        dx, dgate = lam * keep, lam * (before - x) * a * keep
+    else:
+        dx, dgate = lam, lam * before
+    dh0 = None
+    if s["h0"] is not None:
+        dh0 = s["dlast"].clone()
+        dh0[some] = (a[0, first] * lam[0, first]) if c["packed"] else a[:, 0] * lam[:, 0]
+    if c["packed"]:
+        dx, dgate = dx[0], dgate[0]
+    return dict(out, dx=dx.to(dt), dgate=dgate.to(dt), dh0=dh0)
+
+
+def adam_own(s):
+    from preconditioned_cg_solver_amd import binding as B
+    B.sla_adamw_step(s["opt"], s["grads"], step=s["step"], lr=LR, beta1=B1, beta2=B2, eps=EPS,
+                     weight_decay=WD, seed=SEED)
+    # 32-bit states are the handle's own buffers; 8-bit ones are returned as the values they stand for
+    m, v = B.sla_adamw_get_state(s["opt"])
+    return {"p": s["p"], "m": m, "v": v}
+
+
+def mix(x):
+    x = ((x ^ (x >> 16)) * 0x9E3779B1) & 0xFFFFFFFF
+    x = ((x ^ (x >> 15)) * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def noise(step, n):
+    """32 random bits for each of n elements (n < 2^32) at this step."""
+    key = mix((SEED & 0xFFFFFFFF) ^ mix((SEED >> 32) ^ mix(step & 0xFFFFFFFF)))
+    e = torch.arange(n, device=DEV, dtype=torch.int64)
+    return mix((e * 0x9E3779B1 + key) & 0xFFFFFFFF)
+
+
+def to_levels(x, bits, top):
+    """x rounded to the 8-bit form's levels: the float32 pattern kept to its
+    three leading mantissa bits, `top` levels from the block's largest down."""
+    k = (x.abs().view(torch.int32).long()).view(-1, BLOCK)
+    lowest = (((k.amax(1, keepdim=True) + 0xFFFFF) >> 20) - top).clamp_(min=0)
+    code = torch.where(k == 0, 0, ((k + bits.view(-1, BLOCK)) >> 20) - lowest)
+    code = code.clamp(1, top) if top == 254 else code.clamp(0, top)
+    code = torch.where(k == 0, 0, code)
+    level = torch.where(code == 0, 0, code + lowest) << 20
+    return torch.copysign(level.int().view(torch.float32).flatten(), x)
+
+
+def adam_plain(s):
+    c, t = s["case"], s["step"]
+    n = s["m"].numel()
+    place = s["place"]
+    p, g = s["p"].float(), s["grad"].float()
+    if place is not None:
+        p = torch.zeros(n, device=DEV).index_copy_(0, place, p)
+        g = torch.zeros(n, device=DEV).index_copy_(0, place, g)
+    m = s["m"] * B1 + g * (1 - B1)
+    v = s["v"] * B2 + (g * g) * (1 - B2)
+    root = v.sqrt() * (1 / math.sqrt(1 - B2 ** t)) + EPS
+    p = p * (1 - LR * WD) - (m / root) * (LR / (1 - B1 ** t))
+    rand = noise(t, n) if c["bits"] == 8 or c["param"] == "bf16" else None
+    if c["bits"] == 8:
+        m = to_levels(m, ((rand & 0xFFFF) << 4) + 8, 126)
+        v = to_levels(v, ((rand >> 16) << 4) + 8, 254)
+    if c["param"] == "bf16":  # a bf16 parameter is rounded up with the probability of its remainder
+        low = mix((rand + 0x6A09E667) & 0xFFFFFFFF) & 0xFFFF
+        p = ((p.view(torch.int32) + low.int()) & -65536).view(torch.float32)
+    s["m"], s["v"] = m, v
+    s["p"].copy_(p if place is None else p[place])
+    held = torch.bfloat16 if c["bits"] == 8 else torch.float32  # 8-bit values have 4 significant bits
+    return {"p": s["p"], "m": m.to(held), "v": v.to(held)}
+
+
+# ----- work -----
+
+def work(case):
+    if case["op"] == "rec":
+        e = BYTES[case["dtype"]]
+        n = case["seqs"] * case["steps"] * case["dim"] if not case["packed"] \
+            else case["steps"] * case["dim"]
+        state = 4 * case["seqs"] * case["dim"]
+        if case["do"] == "fwd":
+            return {"bytes": 3 * e * n + state * (2 if case["h0"] else 1), "flops": 10 * n}
+        # x, gate, dh in; h, dx, dgate out; the states and their gradients
+        return {"bytes": 6 * e * n + state * (4 if case["h0"] else 2), "flops": 30 * n}
+    n = case["total"]
+    each = 2 * BYTES[case["param"]] + BYTES[case["grad"]]
+    # 8-bit states: read, written, and read back as two-byte values
+    each += 16 if case["bits"] == 32 else 4 + 4 + 8 / BLOCK
+    return {"bytes": int(each * n), "flops": 16 * n}
+
+
+# ----- 64 bits -----
+
+def exact(case, seed):
+    return rec_exact(rec_inputs(case, seed)) if case["op"] == "rec" \
+        else adam_exact(adam_inputs(case, seed))
+
+
+def rec_exact(s):
+    """Step by step in 64 bits; packed sequences as one, cut where each begins."""
+    c = s["case"]
+    x, gate = s["x"].double(), s["gate"].double()
+    T = c["steps"]
+    h0 = s["h0"].double() if s["h0"] is not None else x.new_zeros(c["seqs"], c["dim"])
+    keep = 1 / (1 + gate.exp()) if c["mode"] == "sigmoid" else None
+    a = 1 / (1 + (-gate).exp()) if c["mode"] == "sigmoid" else gate
+    b = keep * x if c["mode"] == "sigmoid" else x.clone()
+    if c["packed"]:
+        off = s["offsets"].cpu().numpy()
+        seqs = [k for k in range(c["seqs"]) if off[k + 1] > off[k]]
+        first = torch.tensor([off[k] for k in seqs], device=DEV)
+        end = torch.tensor([off[k + 1] - 1 for k in seqs], device=DEV)
+        of = torch.tensor(seqs, device=DEV)
+    else:  # time first
+        x, a, b, gate = (u.transpose(0, 1) for u in (x, a, b, gate))
+        keep = keep.transpose(0, 1) if keep is not None else None
+        first, end, of = 0, T - 1, slice(None)
+    b, a_in = b.contiguous(), a.contiguous().clone()
+    b[first] += a[first] * h0[of]
+    a_in[first] = 0  # nothing crosses into a sequence's first step
+    h = torch.empty_like(b)
+    h[0] = b[0]
+    for t in range(1, T):
+        torch.addcmul(b[t], a_in[t], h[t - 1], out=h[t])
+    del b
+    last = h0.clone()
+    last[of] = h[end]
+    flat = (lambda u: u) if c["packed"] else (lambda u: u.transpose(0, 1))
+    out = {"h": flat(h), "last": last}
+    if c["do"] == "fwd":
+        return out
+    lam = s["dh"].double()
+    lam = lam.clone() if c["packed"] else lam.transpose(0, 1).contiguous()
+    lam[end] += s["dlast"].double()[of]
+    for t in range(T - 2, -1, -1):
+        lam[t].addcmul_(a_in[t + 1], lam[t + 1])
+    before = torch.cat([h[:1], h[:-1]])
+    before[first] = h0[of]
+    dx, dgate = (lam, lam * before) if keep is None else \
+        (lam * keep, lam * (before - x) * a * keep)
+    dh0 = None
+    if s["h0"] is not None:
+        dh0 = s["dlast"].double()
+        dh0[of] = a[first] * lam[first]
+    return dict(out, dx=flat(dx), dgate=flat(dgate), dh0=dh0)
+
+
+def level_exact(x, rand, top):
+    """Levels 2^e (1 + q / 8) of the 8-bit form, from frexp in 64 bits."""
+    mant, e = torch.frexp(x.abs())
+    place = (2 * mant - 1) * 8 + 8.0 * (e + 126).double()  # 8 (e' + 127) + 8 (m' - 1)
+    some = x != 0
+    place = torch.where(some, place, -1e9).view(-1, BLOCK)
+    lowest = (torch.ceil(place.amax(1, keepdim=True)) - top).clamp(min=0)
+    k = torch.floor(place + rand.view(-1, BLOCK).double() / 2 ** 20) - lowest
+    k = k.clamp(1, top) if top == 254 else torch.where(k < 1, -1e9, k.clamp(max=top))
+    full = torch.where(k < 0, 0.0, k + lowest).flatten()
+    value = torch.ldexp(1 + (full % 8) / 8, torch.floor(full / 8) - 127)
+    return torch.where(some & (full > 0), torch.copysign(value, x), 0.0)
+
+
+def adam_exact(s):
+    c, t = s["case"], s["step"] + 1
+    n = s["m"].numel()
+    p, g = s["p"].double(), s["grad"].double()
+    if s["place"] is not None:
+        p = torch.zeros(n, device=DEV, dtype=torch.float64).index_copy_(0, s["place"], p)
+        g = torch.zeros(n, device=DEV, dtype=torch.float64).index_copy_(0, s["place"], g)
+    m = B1 * s["m"].double() + (1 - B1) * g
+    v = B2 * s["v"].double() + (1 - B2) * g ** 2
+    p = p * (1 - LR * WD) - LR / (1 - B1 ** t) * m / ((v / (1 - B2 ** t)).sqrt() + EPS)
+    if c["bits"] == 8:
+        rand = noise(t, n)
+        m = level_exact(m, ((rand & 0xFFFF) << 4) + 8, 126)
+        v = level_exact(v, ((rand >> 16) << 4) + 8, 254)
+    return {"p": p if s["place"] is None else p[s["place"]], "m": m, "v": v}
