@@ -179,6 +179,9 @@ def adam_inputs(case, seed):
         real[h:h + n] = True
     if case["pack"] != BLOCK:
         place = real.nonzero().flatten()
+    else:  # nothing lies between the tensors
+        p.mul_(real)
+        grad.mul_(real)
     m.mul_(real)
     v.mul_(real)
     if case["bits"] == 8:  # values that the 8-bit form holds
