@@ -97,7 +97,13 @@ extern "C" {
 /* SLA_DTYPE_RANGE_ makes every non-negative int32 a value of the type, so a
  * caller's out-of-range dtype reaches the library's check (and is rejected
  * with SLA_ERR_INVALID_ARG) instead of being an invalid enum value. */
-typedef enum { SLA_F64 = 0, SLA_F32 = 1, SLA_DTYPE_RANGE_ = 0x7fffffff } sla_dtype;
+typedef enum {
+    SLA_F64 = 0,
+    SLA_F32 = 1,
+    SLA_BF16 = 2, /* recurrences and the AdamW step only: matrices are SLA_F64 or SLA_F32 */
+    SLA_F16 = 3,  /* recurrences only */
+    SLA_DTYPE_RANGE_ = 0x7fffffff
+} sla_dtype;
 
 typedef enum {
     SLA_OK = 0,
@@ -397,6 +403,174 @@ sla_status sla_init(void);
 sla_status sla_pcg_solve_noalloc(sla_mat_t A, sla_mat_t G, double eps, const void *d_b,
                                  void *d_x, double rtol, int32_t maxit, void *stream,
                                  sla_solve_info *info);
+
+/*
+ * Gated linear recurrences along a sequence, and their adjoint.
+ *
+ * Per sequence and channel this solves the lower bidiagonal system
+ * (I - S diag(a)) h = b (S shifts by one step) by forward substitution:
+ *   SLA_GATE_LINEAR   h_t = a_t h_{t-1} + x_t              a = gate
+ *   SLA_GATE_SIGMOID  h_t = a_t h_{t-1} + (1 - a_t) x_t    a = 1 / (1 + exp(-gate))
+ * for t = 1 .. T with h_0 given (zero if d_h0 is NULL), and the adjoint is
+ * the transposed solve ("torch-sla", Technical Summary, Methodology 2, on a
+ * bidiagonal pattern): with mu_{T+1} = dL/dh_last,
+ *   lambda_t = dL/dh_t + mu_{t+1},  mu_t = a_t lambda_t,  dL/dh_0 = mu_1,
+ *   linear:   dL/dx = lambda,          dL/dgate = lambda_t h_{t-1}
+ *   sigmoid:  dL/dx = lambda (1 - a),  dL/dgate = lambda_t (h_{t-1} - x_t) a_t (1 - a_t).
+ *
+ * Shapes.  Dense (d_offsets NULL): n_seq sequences of `steps` steps and `dim`
+ * channels.  Packed: `steps` is the total number of steps of n_seq sequences
+ * laid end to end, sequence s taking steps d_offsets[s] .. d_offsets[s+1]-1
+ * (device array of n_seq + 1, ascending from 0 to `steps`; sequences may be
+ * empty: their last state is their first).  The offsets are not checked on
+ * the host; whatever they hold, no access leaves the arrays.
+ *
+ * Element (s, t, c) of an input lies at s * seq_stride + t * step_stride + c
+ * (in elements; packed inputs ignore seq_stride), so inputs may be slices of
+ * a wider projection or repeat (stride 0).  d_h, d_grad_x and d_grad_gate
+ * are dense: (n_seq, steps, dim), or (steps, dim) when packed.  x, gate, h and
+ * their gradients have the shape's dtype; the states d_h0 and d_h_last and
+ * their gradients, (n_seq, dim), are fp32 (fp64 for SLA_F64), and so are all
+ * sums and products: only h, dx and dgate are rounded, once, when stored.
+ * Non-finite values propagate as in the formulas; a gate of -infinity
+ * (sigmoid) or 0 (linear) cuts the sequence there unless h_{t-1} is itself
+ * non-finite.
+ */
+typedef enum { SLA_GATE_LINEAR = 0, SLA_GATE_SIGMOID = 1, SLA_GATE_RANGE_ = 0x7fffffff } sla_gate;
+
+typedef struct {
+    int64_t n_seq;             /* sequences                                       */
+    int64_t steps;             /* steps of each (dense) or of all (packed)        */
+    int64_t dim;               /* channels                                        */
+    const int64_t *d_offsets;  /* NULL: dense                                     */
+    sla_dtype dtype;
+    sla_gate gate;
+} sla_linrec_shape;
+
+/* Bytes of d_saved (the states the backward pass starts its recomputation
+ * from, one per 64 steps) and of d_work for either direction (0: none needed).
+ * Errors: SLA_ERR_INVALID_ARG (NULL, negative size, unknown dtype or gate),
+ * SLA_ERR_UNSUPPORTED (a size beyond what one launch can index). */
+sla_status sla_linrec_sizes(const sla_linrec_shape *shape, size_t *saved_bytes,
+                            size_t *work_bytes);
+
+/*
+ * h and the last states.  d_h0 (NULL: zeros), d_h_last (NULL: not wanted; may
+ * be d_h0 for a state updated in place) and d_saved (NULL: no backward pass
+ * will follow) are optional.  One serving step is steps = 1.  d_h must not
+ * overlap the inputs.  Asynchronous on `stream`; allocates nothing, so it can be
+ * captured in a HIP graph.  SLA_ERR_INVALID_ARG on NULL arrays, negative
+ * strides, d_h equal to an input or a short workspace.
+ */
+sla_status sla_linrec_forward(const sla_linrec_shape *shape, const void *d_x,
+                              int64_t x_seq_stride, int64_t x_step_stride, const void *d_gate,
+                              int64_t gate_seq_stride, int64_t gate_step_stride,
+                              const void *d_h0, void *d_h, void *d_h_last, void *d_saved,
+                              void *d_work, size_t work_bytes, void *stream);
+
+/*
+ * Gradients.  d_saved is what the forward call on the same arguments wrote.
+ * d_grad_h (NULL: zeros; strided like an input), d_grad_last (NULL: zeros),
+ * d_grad_h0 (NULL: not wanted).  Asynchronous on `stream`, as the forward.
+ */
+sla_status sla_linrec_backward(const sla_linrec_shape *shape, const void *d_x,
+                               int64_t x_seq_stride, int64_t x_step_stride, const void *d_gate,
+                               int64_t gate_seq_stride, int64_t gate_step_stride,
+                               const void *d_h0, const void *d_saved, const void *d_grad_h,
+                               int64_t grad_seq_stride, int64_t grad_step_stride,
+                               const void *d_grad_last, void *d_grad_x, void *d_grad_gate,
+                               void *d_grad_h0, void *d_work, size_t work_bytes, void *stream);
+
+/*
+ * AdamW over many tensors at once:
+ *   g = grad * grad_scale
+ *   m' = beta1 m + (1 - beta1) g,    v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
+ * in fp32 (the update of an SLA_F64 parameter is added in fp64).
+ *
+ * The states m and v are the caller's, in one buffer.  Every tensor starts a
+ * new block of 256 elements; with `padded` = 256 * (sum of ceil(numel / 256))
+ * the buffer holds
+ *   32 bits: m, then v, fp32, `padded` each;
+ *    8 bits: the codes of m, then of v, one byte each, `padded` each, then
+ *            the bases of m, then of v, uint16, padded / 256 each.
+ * Zeros are the initial state.  In 8 bits an element is the fp32 number with
+ * the bit pattern (base + code) << 20, i.e. with three mantissa bits: v takes
+ * codes 1..254 (levels down to 2^-31 of the block's largest; smaller ones are
+ * held at the lowest level, so no divisor vanishes), m a sign bit and 1..126
+ * (down to 2^-15; smaller ones become 0).  Code 0 is 0 and the highest code
+ * (255; 127 for m) stands for a value that is not finite, which stays within
+ * its element.  The levels lie 6 to 12 % apart and one step moves v by as
+ * little as 0.1 %, so values are rounded stochastically (unbiased): with R
+ * the 32 random bits of the element, 16 * (R & 0xffff) + 8 is added to m's
+ * pattern and 16 * (R >> 16) + 8 to v's before the low 20 bits are dropped.
+ * An SLA_BF16 parameter is rounded the same way from the 16 low bits of
+ * mix(R + 0x6A09E667).  R = mix(e * 0x9E3779B1 + key) with e the
+ * element's place in the padded order (its high 32 bits folded into the key)
+ * and key = mix(lo32(seed) ^ mix(hi32(seed) ^ mix(lo32(step)))), where
+ * mix(x): x = (x ^ x >> 16) * 0x9E3779B1; x = (x ^ x >> 15) * 0xBB67AE85;
+ * x ^= x >> 16 (mod 2^32).  The same seed and step give the same bits.
+ */
+typedef struct sla_adamw *sla_adamw_t;
+
+typedef struct {
+    void *d_param;        /* SLA_F64, SLA_F32 or SLA_BF16, contiguous                 */
+    void *d_copy;         /* NULL, or a bf16 copy of an SLA_F32 parameter to keep up to date */
+    int64_t numel;
+    sla_dtype dtype;
+    sla_dtype grad_dtype; /* dtype, or SLA_BF16 for an SLA_F32 parameter              */
+} sla_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;         /* >= 1 */
+    uint64_t seed;        /* of the stochastic rounding */
+} sla_adamw_hyper;
+
+/* Bytes of the state buffer and of the device table (the tensors' pointers
+ * and the work list), and the padded element count. */
+sla_status sla_adamw_sizes(const sla_adamw_tensor *h_tensors, int32_t n_tensors,
+                           int32_t state_bits, size_t *state_bytes, size_t *table_bytes,
+                           int64_t *padded);
+
+/*
+ * A handle for stepping n_tensors parameters with states of state_bits (8 or 32).
+ * It BORROWS the parameters, d_state (256-byte aligned; its contents are the
+ * states, zeros at first) and d_table (256-byte aligned, written here), which
+ * must outlive the last queued step and every graph that holds one; the
+ * handle itself owns no device memory.  Synchronises `stream`.  Errors:
+ * SLA_ERR_INVALID_ARG (NULL or short buffers, negative sizes, misaligned
+ * pointers, unknown dtypes), SLA_ERR_UNSUPPORTED (a dtype pair or state_bits
+ * other than the above), SLA_ERR_OOM, SLA_ERR_HIP.
+ */
+sla_status sla_adamw_create(sla_adamw_t *out, const sla_adamw_tensor *h_tensors,
+                            int32_t n_tensors, int32_t state_bits, void *d_state,
+                            size_t state_bytes, void *d_table, size_t table_bytes, void *stream);
+sla_status sla_adamw_destroy(sla_adamw_t opt);
+
+/*
+ * One step.  h_grads[i] (host array of device pointers) is the gradient of
+ * tensor i, contiguous, in its grad_dtype; NULL leaves tensor i and its
+ * states as they are.  d_grad_scale (may be NULL) is a device fp32 number
+ * that multiplies every gradient; if it is not finite the step changes
+ * nothing.  Asynchronous on `stream`; allocates nothing and copies nothing,
+ * so it can be captured in a HIP graph (the gradients' addresses and the
+ * step number are then fixed).  SLA_ERR_INVALID_ARG on NULL arguments,
+ * misaligned gradients, lr or weight_decay or eps negative or not finite,
+ * betas outside [0, 1), step < 1.
+ */
+sla_status sla_adamw_step(sla_adamw_t opt, const void *const *h_grads,
+                          const sla_adamw_hyper *hyper, const float *d_grad_scale, void *stream);
+
+/* The states' values, `padded` each: bf16 (which holds them exactly) for 8-bit
+ * states, fp32 for 32-bit ones.  Asynchronous on `stream`. */
+sla_status sla_adamw_get_state(sla_adamw_t opt, void *d_m, void *d_v, void *stream);
+
+/* Sets the states from fp32 values, `padded` each with zeros in the padding;
+ * 8-bit states take the nearest level (a value that sla_adamw_get_state gave is
+ * kept exactly).  v must not be negative.  Asynchronous on `stream`. */
+sla_status sla_adamw_set_state(sla_adamw_t opt, const float *d_m, const float *d_v, void *stream);
 
 /* Human-readable name of a status, and the calling thread's last error text. */
 const char *sla_status_string(sla_status st);

@@ -9,6 +9,7 @@ no GPU is present, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -20,7 +21,8 @@ import torch  # noqa: F401  (must precede loading libsla.so, see above)
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libsla.so")
 
-SLA_F64, SLA_F32 = 0, 1
+SLA_F64, SLA_F32, SLA_BF16, SLA_F16 = 0, 1, 2, 3
+SLA_GATE_LINEAR, SLA_GATE_SIGMOID = 0, 1
 SLA_BUILD_TRANSPOSE, SLA_VALIDATE = 1, 2
 STATUS = {0: "SLA_OK", 1: "SLA_NOT_CONVERGED", -1: "SLA_ERR_INVALID_ARG", -2: "SLA_ERR_UNSUPPORTED",
           -3: "SLA_ERR_BREAKDOWN", -4: "SLA_ERR_NONFINITE", -5: "SLA_ERR_HIP", -6: "SLA_ERR_OOM"}
@@ -38,6 +40,22 @@ class SlaError(RuntimeError):
 class SolveInfo(ctypes.Structure):
     _fields_ = [("iterations", ctypes.c_int32), ("converged", ctypes.c_int32),
                 ("rel_residual", ctypes.c_double), ("bnorm", ctypes.c_double)]
+
+
+class LinrecShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int64), ("steps", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("d_offsets", ctypes.c_void_p), ("dtype", ctypes.c_int), ("gate", ctypes.c_int)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("d_param", ctypes.c_void_p), ("d_copy", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int)]
+
+
+class AdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
 
 
 _lib = None
@@ -101,6 +119,17 @@ def _declare(L):
         "sla_init": ([], st),
         "sla_pcg_solve_noalloc": ([vp, vp, dbl, vp, vp, dbl, i32, vp, ctypes.POINTER(SolveInfo)],
                                   st),
+        "sla_linrec_sizes": ([vp, ctypes.POINTER(sz), ctypes.POINTER(sz)], st),
+        "sla_linrec_forward": ([vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp], st),
+        "sla_linrec_backward": ([vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, i64, vp, vp, vp,
+                                 vp, vp, sz, vp], st),
+        "sla_adamw_sizes": ([vp, i32, i32, ctypes.POINTER(sz), ctypes.POINTER(sz),
+                             ctypes.POINTER(i64)], st),
+        "sla_adamw_create": ([ctypes.POINTER(vp), vp, i32, i32, vp, sz, vp, sz, vp], st),
+        "sla_adamw_destroy": ([vp], st),
+        "sla_adamw_step": ([vp, vp, vp, vp, vp], st),
+        "sla_adamw_get_state": ([vp, vp, vp, vp], st),
+        "sla_adamw_set_state": ([vp, vp, vp, vp], st),
         "sla_status_string": ([st], ctypes.c_char_p),
         "sla_last_error": ([], ctypes.c_char_p),
         "sla_set_profiling": ([i32], st),
@@ -600,3 +629,310 @@ def sla_get_profile(kernel_class) -> Tuple[int, float]:
 
 def sla_status_string(status: int) -> str:
     return lib().sla_status_string(int(status)).decode()
+
+
+# ----- recurrences along a sequence, and the AdamW step -----
+
+_DTYPES = {torch.float64: SLA_F64, torch.float32: SLA_F32, torch.bfloat16: SLA_BF16,
+           torch.float16: SLA_F16}
+_GATES = {"linear": SLA_GATE_LINEAR, "sigmoid": SLA_GATE_SIGMOID}
+
+
+def _device_of(named) -> torch.device:
+    """The one GPU that all the given (name, tensor) pairs live on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not getattr(t, "is_cuda", False):
+            raise ValueError(f"{name} must live on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, others on {dev}")
+    return dev
+
+
+def _enter(dev: torch.device, stream):
+    """(raw stream, context in which to allocate): results and scratch belong
+    to the stream that the kernels run on.  Kernels are launched on the
+    current device, which has to be the tensors'."""
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        raw = stream.value if isinstance(stream, ctypes.c_void_p) else stream
+        stream = torch.cuda.ExternalStream(raw or 0, device=dev)
+    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _raw(t) -> Optional[ctypes.c_void_p]:
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _linrec_shape(x, gate, offsets, mode) -> Tuple[LinrecShape, torch.dtype]:
+    if mode not in _GATES:
+        raise ValueError(f"mode must be one of {sorted(_GATES)}, got {mode!r}")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError("x must be (sequences, steps, channels), or give offsets")
+        n, t, d = x.shape
+    else:
+        if x.dim() != 2:
+            raise ValueError("packed x must be (steps, channels)")
+        if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1 \
+                or not offsets.is_contiguous():
+            raise ValueError("offsets must be a contiguous int64 vector of sequences + 1 entries")
+        n, (t, d) = offsets.numel() - 1, x.shape
+    if tuple(gate.shape) != tuple(x.shape) or gate.dtype != x.dtype:
+        raise ValueError("gate must have x's shape and dtype")
+    q = LinrecShape(n, t, d, None if offsets is None else offsets.data_ptr(), _DTYPES[x.dtype],
+                    _GATES[mode])
+    return q, torch.float64 if x.dtype == torch.float64 else torch.float32
+
+
+def _steps_in(t, name: str, x):
+    """(pointer, sequence stride, step stride) of an input shaped like x."""
+    if t is None:
+        return None, 0, 0
+    if tuple(t.shape) != tuple(x.shape) or t.dtype != x.dtype:
+        raise ValueError(f"{name} must have x's shape and dtype")
+    st = t.stride()
+    if t.shape[-1] > 1 and st[-1] != 1 and t.numel():
+        raise ValueError(f"{name}'s channels must be adjacent (last stride 1)")
+    return ctypes.c_void_p(t.data_ptr()), (st[0] if len(st) == 3 else 0), st[-2]
+
+
+def _states(t, name: str, q: LinrecShape, dtype):
+    if t is None:
+        return None
+    if tuple(t.shape) != (q.n_seq, q.dim) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous ({q.n_seq}, {q.dim}) tensor of {dtype}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def sla_linrec_sizes(x, gate, offsets=None, mode: str = "sigmoid") -> Tuple[int, int]:
+    """Bytes of (the states kept for the backward pass, the workspace)."""
+    q, _ = _linrec_shape(x, gate, offsets, mode)
+    return _linrec_sizes(q)
+
+
+def _linrec_sizes(q: LinrecShape) -> Tuple[int, int]:
+    saved, work = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().sla_linrec_sizes(ctypes.byref(q), ctypes.byref(saved), ctypes.byref(work)))
+    return saved.value, work.value
+
+
+def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                       offsets: Optional[torch.Tensor] = None, mode: str = "sigmoid",
+                       save: bool = False, h_last: Optional[torch.Tensor] = None, stream=None):
+    """h_t = a_t h_{t-1} + b_t along each sequence: a = gate, b = x ("linear"),
+    or a = sigmoid(gate), b = (1 - a) x ("sigmoid").
+
+    x and gate: (sequences, steps, channels), or (steps, channels) with
+    `offsets` (int64, on the device) marking where each of the packed
+    sequences begins; slices of a wider tensor and expanded ones are taken as
+    they are.  h0 and h_last: (sequences, channels) float32 (float64 for
+    float64); h_last may be given, h0 itself included, to be overwritten.
+    Returns (h, h_last, saved); `saved` (None unless save) is what the
+    backward pass needs."""
+    q, sdt = _linrec_shape(x, gate, offsets, mode)
+    px, pg = _steps_in(x, "x", x), _steps_in(gate, "gate", x)
+    p0, pl = _states(h0, "h0", q, sdt), _states(h_last, "h_last", q, sdt)
+    dev = _device_of((("x", x), ("gate", gate), ("h0", h0), ("offsets", offsets),
+                      ("h_last", h_last)))
+    raw, ctx = _enter(dev, stream)
+    n_saved, n_work = _linrec_sizes(q)
+    with ctx:
+        h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if h_last is None:
+            h_last = torch.empty((q.n_seq, q.dim), dtype=sdt, device=dev)
+            pl = _raw(h_last)
+        saved = torch.empty(n_saved // sdt.itemsize, dtype=sdt, device=dev) if save else None
+        work = torch.empty(n_work, dtype=torch.uint8, device=dev) if n_work else None
+    _check(lib().sla_linrec_forward(ctypes.byref(q), *px, *pg, p0, _raw(h), pl, _raw(saved),
+                                    _raw(work), n_work, raw))
+    return h, h_last, saved
+
+
+def sla_linrec_backward(x: torch.Tensor, gate: torch.Tensor, saved: torch.Tensor,
+                        grad_h: Optional[torch.Tensor],
+                        grad_last: Optional[torch.Tensor] = None,
+                        h0: Optional[torch.Tensor] = None,
+                        offsets: Optional[torch.Tensor] = None, mode: str = "sigmoid",
+                        stream=None):
+    """Gradients (of x, of gate, of h0 or None) from those of h and h_last
+    (None: zero); the other arguments are the forward call's."""
+    q, sdt = _linrec_shape(x, gate, offsets, mode)
+    px, pg = _steps_in(x, "x", x), _steps_in(gate, "gate", x)
+    pd = _steps_in(grad_h, "grad_h", x)
+    p0, pl = _states(h0, "h0", q, sdt), _states(grad_last, "grad_last", q, sdt)
+    dev = _device_of((("x", x), ("gate", gate), ("saved", saved), ("grad_h", grad_h),
+                      ("grad_last", grad_last), ("h0", h0), ("offsets", offsets)))
+    n_saved, n_work = _linrec_sizes(q)
+    if saved.dtype != sdt or not saved.is_contiguous() or \
+            saved.numel() * sdt.itemsize != n_saved:
+        raise ValueError("saved must be the forward call's")
+    raw, ctx = _enter(dev, stream)
+    with ctx:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dg = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dh0 = torch.empty((q.n_seq, q.dim), dtype=sdt, device=dev) if h0 is not None else None
+        work = torch.empty(n_work, dtype=torch.uint8, device=dev) if n_work else None
+    _check(lib().sla_linrec_backward(ctypes.byref(q), *px, *pg, p0, _raw(saved), *pd, pl,
+                                     _raw(dx), _raw(dg), _raw(dh0), _raw(work), n_work, raw))
+    return dx, dg, dh0
+
+
+class Adamw:
+    """A handle of the AdamW step; keeps what it borrows alive.  `state` holds
+    the states as bytes (see include/sla.h for the layout): copy it to save a
+    run, copy it back to resume."""
+
+    def __init__(self, handle, params, copies, grad_dtypes, state_bits, state, table, padded):
+        self.handle = handle
+        self.params, self.copies, self.grad_dtypes = params, copies, grad_dtypes
+        self.state_bits, self.state, self._table, self.padded = state_bits, state, table, padded
+        self.starts, at = [], 0
+        for p in params:
+            self.starts.append(at)
+            at += -(-p.numel() // 256) * 256
+        self._want = [(p.numel(), dt) for p, dt in zip(params, grad_dtypes)]
+        self._ptrs = (ctypes.c_void_p * max(len(params), 1))()
+
+    @property
+    def device(self):
+        return self.state.device
+
+    def views(self, flat: torch.Tensor):
+        """The parts of a padded array that belong to each parameter, in its shape."""
+        return [flat[a:a + p.numel()].view(p.shape) for a, p in zip(self.starts, self.params)]
+
+    def destroy(self):
+        if self.handle:
+            lib().sla_adamw_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def _adamw_list(params, grad_dtype, copies):
+    n = len(params)
+    gd = list(grad_dtype) if isinstance(grad_dtype, (list, tuple)) else \
+        [grad_dtype or p.dtype for p in params]
+    copies = list(copies) if copies is not None else [None] * n
+    if len(gd) != n or len(copies) != n:
+        raise ValueError("grad_dtype and copies must have one entry per parameter")
+    ts = (AdamwTensor * max(n, 1))()
+    for i, (p, g, c) in enumerate(zip(params, gd, copies)):
+        if p.dtype not in _DTYPES or g not in _DTYPES:
+            raise ValueError(f"unsupported dtypes {p.dtype}, {g}")
+        if not p.is_contiguous():
+            raise ValueError(f"parameter {i} must be contiguous")
+        if c is not None and (c.dtype != torch.bfloat16 or not c.is_contiguous()
+                              or tuple(c.shape) != tuple(p.shape)):
+            raise ValueError(f"copy {i} must be a contiguous bfloat16 tensor of its "
+                             "parameter's shape")
+        ts[i] = AdamwTensor(p.data_ptr(), None if c is None else c.data_ptr(), p.numel(),
+                            _DTYPES[p.dtype], _DTYPES[g])
+    return ts, gd, copies
+
+
+def sla_adamw_sizes(params, state_bits: int = 32, grad_dtype=None, copies=None):
+    """(state bytes, table bytes, padded elements) of a handle for `params`."""
+    params = list(params)
+    return _adamw_sizes(_adamw_list(params, grad_dtype, copies)[0], len(params), state_bits)
+
+
+def _adamw_sizes(ts, n, state_bits):
+    sb, tb, padded = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_int64()
+    _check(lib().sla_adamw_sizes(ts, n, int(state_bits), ctypes.byref(sb), ctypes.byref(tb),
+                                 ctypes.byref(padded)))
+    return sb.value, tb.value, padded.value
+
+
+def sla_adamw_create(params, state_bits: int = 32, grad_dtype=None, copies=None,
+                     stream=None) -> Adamw:
+    """A handle that steps all of `params` (float64, float32 or bfloat16, in
+    place) with zero states of 32 or 8 bits.  grad_dtype: one dtype or one per
+    parameter (default: the parameter's; bfloat16 is taken for float32
+    parameters too).  copies: per parameter None or a bfloat16 tensor that
+    each step rewrites from a float32 parameter."""
+    params = [p.detach() for p in params]
+    ts, gd, copies = _adamw_list(params, grad_dtype, copies)
+    sb, tb, padded = _adamw_sizes(ts, len(params), state_bits)
+    dev = _device_of([("a parameter", p) for p in params] + [("a copy", c) for c in copies])
+    if dev is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    raw, ctx = _enter(dev, stream)
+    with ctx:
+        state = torch.zeros(sb, dtype=torch.uint8, device=dev)
+        table = torch.empty(tb, dtype=torch.uint8, device=dev)
+    h = ctypes.c_void_p()
+    _check(lib().sla_adamw_create(ctypes.byref(h), ts, len(params), int(state_bits), _raw(state),
+                                  sb, _raw(table), tb, raw))
+    return Adamw(h, params, copies, gd, int(state_bits), state, table, padded)
+
+
+def sla_adamw_destroy(opt: Adamw) -> None:
+    opt.destroy()
+
+
+def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
+                   beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
+                   grad_scale: Optional[torch.Tensor] = None, seed: int = 0, stream=None) -> None:
+    """One step (number `step`, from 1) of every parameter from its gradient
+    (None leaves a parameter and its states alone).  grad_scale: a float32
+    device number that multiplies the gradients; one that is not finite makes
+    the step change nothing.  seed: of the stochastic rounding."""
+    if len(grads) != len(opt.params):
+        raise ValueError(f"{len(grads)} gradients for {len(opt.params)} parameters")
+    dev, ptrs = opt.device, opt._ptrs
+    for i, (g, (n, dt)) in enumerate(zip(grads, opt._want)):
+        if g is None:
+            ptrs[i] = None
+            continue
+        if g.dtype != dt or g.numel() != n or g.device != dev or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be a contiguous {dt} tensor of {n} elements "
+                             f"on {dev}")
+        ptrs[i] = g.data_ptr()
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
+                                   or grad_scale.device != dev):
+        raise ValueError("grad_scale must be one float32 number on the parameters' device")
+    hyper = AdamwHyper(lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFFFFFFFFFF)
+    raw, _ = _enter(dev, stream)
+    _check(lib().sla_adamw_step(opt.handle, ptrs, ctypes.byref(hyper), _raw(grad_scale), raw))
+
+
+def sla_adamw_get_state(opt: Adamw, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The values of m and v over the padded elements (see Adamw.views): the
+    handle's own buffers for 32-bit states, bfloat16 arrays (exact) for 8-bit."""
+    if opt.state_bits == 32:
+        f = opt.state.view(torch.float32)
+        return f[:opt.padded], f[opt.padded:]
+    raw, ctx = _enter(opt.device, stream)
+    with ctx:
+        m = torch.empty(opt.padded, dtype=torch.bfloat16, device=opt.device)
+        v = torch.empty(opt.padded, dtype=torch.bfloat16, device=opt.device)
+    _check(lib().sla_adamw_get_state(opt.handle, _raw(m), _raw(v), raw))
+    return m, v
+
+
+def sla_adamw_set_state(opt: Adamw, m: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Set the states from float32 values over the padded elements (zeros in
+    the padding); 8-bit states take the nearest level."""
+    for name, t in (("m", m), ("v", v)):
+        if t.dtype != torch.float32 or t.numel() != opt.padded or not t.is_contiguous() \
+                or t.device != opt.device:
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {opt.padded} "
+                             f"elements on {opt.device}")
+    raw, _ = _enter(opt.device, stream)
+    _check(lib().sla_adamw_set_state(opt.handle, _raw(m), _raw(v), raw))

@@ -16,8 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsla.so")
 LIB_DEBUG = os.path.join(PKG, "libsla_debug.so")
-SOURCES = ["setup.hip", "solver.hip", "multi.hip", "noalloc.hip", "host_util.cpp", "spectrum.cpp",
-           "trace.cpp", "api.cpp"]
+SOURCES = ["setup.hip", "solver.hip", "multi.hip", "noalloc.hip", "linrec.hip", "adamw.hip",
+           "host_util.cpp", "spectrum.cpp", "trace.cpp", "api.cpp"]
 ARCH = os.environ.get("SLA_OFFLOAD_ARCH", "gfx950")
 
 

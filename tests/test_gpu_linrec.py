@@ -1,0 +1,320 @@
+"""Gated linear recurrences along a sequence against a plain 64-bit
+computation, element by element, within bounds derived from the number of
+roundings (seq_util.recurrence)."""
+import numpy as np
+import pytest
+import torch
+
+from preconditioned_cg_solver_amd import autograd as AG
+from preconditioned_cg_solver_amd import binding as B
+from gpu_util import DEV, say
+import seq_util as S
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f64": torch.float64, "f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def state_dtype(dt):
+    return torch.float64 if dt == "f64" else torch.float32
+
+
+def make(dt, mode, lead, d, n, seed, h0=True):
+    """Inputs already rounded to the storage type, on the host in fp64."""
+    r = np.random.default_rng([7, seed, *lead, d])
+
+    def host(a, to):
+        return torch.from_numpy(np.asarray(a)).to(to).double().numpy()
+
+    x = host(r.standard_normal((*lead, d)), DT[dt])
+    g = r.standard_normal((*lead, d))
+    g = host(1.5 * g + 1.5 if mode == "sigmoid" else S.sigmoid(g) * 1.28 - 0.3, DT[dt])
+    dh = host(r.standard_normal((*lead, d)), DT[dt])
+    st, dl = (host(r.standard_normal((n, d)), state_dtype(dt)) for _ in range(2))
+    return x, g, (st if h0 else None), dh, dl
+
+
+def dev(a, to):
+    return None if a is None else torch.from_numpy(a).to(to).to(DEV)
+
+
+def check(got, want, what):
+    for name, t in got.items():
+        v, e = want[name]
+        off = np.abs(t.detach().double().cpu().numpy() - v)
+        worst = float(np.max(off / np.maximum(e, 1e-300), initial=0.0))
+        assert np.all(off <= e), (what, name, "error over bound", worst)
+
+
+def run(dt, mode, x, g, h0, offsets, dh, dl, xt=None, gt=None, dht=None, stream=None):
+    xt = dev(x, DT[dt]) if xt is None else xt
+    gt = dev(g, DT[dt]) if gt is None else gt
+    dht = dev(dh, DT[dt]) if dht is None else dht
+    sd = state_dtype(dt)
+    h0t, dlt = dev(h0, sd), dev(dl, sd)
+    off = None if offsets is None else torch.tensor(offsets, device=DEV, dtype=torch.int64)
+    h, last, saved = B.sla_linrec_forward(xt, gt, h0=h0t, offsets=off, mode=mode, save=True)
+    dx, dg, dh0 = B.sla_linrec_backward(xt, gt, saved, dht, grad_last=dlt, h0=h0t, offsets=off,
+                                        mode=mode)
+    torch.cuda.synchronize()
+    out = {"h": h, "last": last, "dx": dx, "dgate": dg}
+    if h0 is not None:
+        out["dh0"] = dh0
+    return out
+
+
+def reference(dt, mode, x, g, h0, offsets, dh, dl):
+    return S.recurrence(x, g, h0, offsets, mode, dh, dl, S.U64 if dt == "f64" else S.U32, dt)
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f64", "f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,steps,d", [(1, 1, 1), (3, 1, 200), (2, 15, 65), (2, 16, 64),
+                                       (1, 17, 7), (1, 63, 130), (2, 64, 8), (2, 65, 256),
+                                       (1, 128, 77), (3, 129, 40), (2, 1000, 33),
+                                       (1, 4097, 16), (5, 300, 260)])
+def test_dense(dt, mode, n, steps, d):
+    say("recurrence dense", dt, mode, n, steps, d)
+    x, g, h0, dh, dl = make(dt, mode, (n, steps), d, n, 1, h0=steps != 128)
+    got = run(dt, mode, x, g, h0, None, dh, dl)
+    check(got, reference(dt, mode, x, g, h0, None, dh, dl), (dt, mode, n, steps, d))
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f64", "f32", "bf16"])
+@pytest.mark.parametrize("lens,d", [([5], 3), ([1, 1, 1, 1], 65), ([0, 0, 3, 0], 8),
+                                    ([64, 64], 16), ([63, 1, 65, 0, 127, 2], 72),
+                                    ([700, 0, 1, 33, 500, 64], 24), ([1] * 150 + [200], 64),
+                                    ([0, 0], 8)])
+def test_packed(dt, mode, lens, d):
+    """Empty and one-step sequences, ends inside, at and one past a chunk."""
+    say("recurrence packed", dt, mode, lens[:6], d)
+    offsets = np.concatenate([[0], np.cumsum(lens)])
+    x, g, h0, dh, dl = make(dt, mode, (int(offsets[-1]),), d, len(lens), 2)
+    got = run(dt, mode, x, g, h0, offsets, dh, dl)
+    check(got, reference(dt, mode, x, g, h0, offsets, dh, dl), (dt, mode, lens, d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_slices_of_a_wider_tensor(dt, shift):
+    """x, the gate and the gradient as slices, aligned and not."""
+    say("recurrence slices", dt, shift)
+    n, steps, d = 2, 150, 72
+    x, g, h0, dh, dl = make(dt, "sigmoid", (n, steps), d, n, 3)
+    wide = torch.zeros(n, steps, 4 * d + 8, dtype=DT[dt], device=DEV)
+    xt, gt, dht = (wide[..., shift + k * (d + 1):shift + k * (d + 1) + d] for k in range(3))
+    for t, a in ((xt, x), (gt, g), (dht, dh)):
+        t.copy_(torch.from_numpy(a))
+    got = run(dt, "sigmoid", x, g, h0, None, dh, dl, xt, gt, dht)
+    check(got, reference(dt, "sigmoid", x, g, h0, None, dh, dl), (dt, shift))
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+def test_broadcast_inputs(mode):
+    """One gate for all sequences and steps, one x for all sequences; the
+    gradients through autograd are the sums over what was broadcast."""
+    n, steps, d = 3, 131, 20
+    x, g, h0, dh, dl = make("f64", mode, (n, steps), d, n, 4)
+    say("recurrence broadcast", mode)
+    x[:], g[:] = x[:1], g[:1, :1]
+    xt = dev(x[0], torch.float64).requires_grad_()
+    gt = dev(g[0, 0], torch.float64).requires_grad_()
+    h, last = AG.linear_recurrence(xt.expand(n, steps, d), gt.expand(n, steps, d),
+                                   dev(h0, torch.float64), mode=mode)
+    (h * dev(dh, torch.float64)).sum().add((last * dev(dl, torch.float64)).sum()).backward()
+    want = reference("f64", mode, x, g, h0, None, dh, dl)
+    check({"h": h, "last": last}, want, mode)
+    for t, name, axes in ((xt, "dx", 0), (gt, "dgate", (0, 1))):
+        v, e = want[name]
+        # the sum itself: one rounding per term
+        slack = np.abs(v).sum(axes) * 2 * S.U64 * v.size
+        assert np.all(np.abs(t.grad.cpu().numpy() - v.sum(axes)) <= e.sum(axes) + slack)
+
+
+def test_missing_gradients_are_zeros():
+    n, steps, d = 2, 70, 12
+    x, g, h0, dh, dl = make("f64", "sigmoid", (n, steps), d, n, 5)
+    say("recurrence: gradient of the last state alone, of h alone")
+    for use_h, use_last in ((True, False), (False, True)):
+        xt, gt, ht = (dev(a, torch.float64).requires_grad_() for a in (x, g, h0))
+        h, last = AG.linear_recurrence(xt, gt, ht)
+        loss = (h * dev(dh, torch.float64)).sum() if use_h else \
+            (last * dev(dl, torch.float64)).sum()
+        loss.backward()
+        want = reference("f64", "sigmoid", x, g, h0, None, dh * use_h, dl * use_last)
+        check({"dx": xt.grad, "dgate": gt.grad, "dh0": ht.grad}, want, (use_h, use_last))
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("offsets", [None, [0, 4, 4, 5, 75]])
+def test_gradients_against_differences(mode, offsets):
+    """Central differences of the whole map (torch's gradcheck, fp64)."""
+    say("recurrence gradcheck", mode, offsets)
+    lead, n = ((2, 66), 2) if offsets is None else ((75,), 4)
+    x, g, h0, _, _ = make("f64", mode, lead, 2, n, 6)
+    off = None if offsets is None else torch.tensor(offsets, device=DEV)
+    args = [dev(a, torch.float64).requires_grad_() for a in (x, g, h0)]
+    assert torch.autograd.gradcheck(
+        lambda a, b, c: AG.linear_recurrence(a, b, c, off, mode), args, eps=1e-6, atol=1e-7,
+        rtol=1e-6)
+
+
+def test_serving_steps_equal_one_pass():
+    """Single steps with the state updated in place follow the whole pass."""
+    n, steps, d = 4, 70, 100
+    x, g, h0, dh, dl = make("bf16", "sigmoid", (n, steps), d, n, 8)
+    say("recurrence serving steps")
+    want = reference("bf16", "sigmoid", x, g, h0, None, dh, dl)
+    xt, gt = dev(x, torch.bfloat16), dev(g, torch.bfloat16)
+    state = dev(h0, torch.float32)
+    for t in range(steps):
+        h, last, _ = B.sla_linrec_forward(xt[:, t:t + 1], gt[:, t:t + 1], h0=state, h_last=state)
+        assert last is state
+        v, e = want["h"]
+        assert np.all(np.abs(h[:, 0].double().cpu().numpy() - v[:, t]) <= e[:, t]), t
+    check({"last": state}, want, "last")
+
+
+def test_long_state_in_place():
+    """h_last may be h0 itself also where the sequence spans many chunks."""
+    x, g, h0, dh, dl = make("f32", "sigmoid", (2, 1500), 70, 2, 9)
+    say("recurrence in place, long")
+    state = dev(h0, torch.float32)
+    h, _, _ = B.sla_linrec_forward(dev(x, torch.float32), dev(g, torch.float32), h0=state,
+                                   h_last=state)
+    want = reference("f32", "sigmoid", x, g, h0, None, dh, dl)
+    check({"h": h, "last": state}, want, "in place")
+
+
+@pytest.mark.parametrize("lead,n,offsets", [((2, 0), 2, None), ((0, 5), 0, None),
+                                            ((0,), 3, [0, 0, 0, 0])])
+def test_nothing_to_do(lead, n, offsets):
+    say("recurrence: no steps", lead)
+    x, g, h0, dh, dl = make("f32", "linear", lead, 4, n, 10)
+    got = run("f32", "linear", x, g, h0, offsets, dh, dl)
+    assert torch.equal(got["last"].cpu(), torch.from_numpy(h0).float())
+    assert torch.equal(got["dh0"].cpu(), torch.from_numpy(dl).float())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_non_finite_values_stay_where_they_belong(dt):
+    """A NaN or an infinity reaches the later steps of its own sequence and
+    channel only, and a gate of -infinity shuts what came before out."""
+    say("recurrence non-finite", dt)
+    n, steps, d = 2, 200, 9
+    x, g, h0, dh, dl = make(dt, "sigmoid", (n, steps), d, n, 11)
+    want = reference(dt, "sigmoid", x, g, h0, None, dh, dl)["h"]
+    xb, gb = x.copy(), g.copy()
+    xb[0, 70, 3] = np.nan
+    xb[1, 20, 5] = np.inf
+    gb[0, 100, 7] = -np.inf          # a cut
+    gb[0, 101, 8] = np.inf           # x has no weight, the state passes unchanged
+    h, _, _ = B.sla_linrec_forward(dev(xb, DT[dt]), dev(gb, DT[dt]), h0=dev(h0, torch.float32))
+    h = h.double().cpu().numpy()
+    assert np.all(np.isnan(h[0, 70:, 3])) and np.all(np.isfinite(h[0, :70, 3]))
+    assert np.all(h[1, 20:, 5] == np.inf) and np.all(np.isfinite(h[1, :20, 5]))
+    assert h[0, 100, 7] == x[0, 100, 7]
+    assert h[0, 101, 8] == h[0, 100, 8]
+    same = np.ones_like(h, dtype=bool)
+    same[0, 70:, 3] = same[1, 20:, 5] = same[0, 100:, 7] = same[0, 101:, 8] = False
+    assert np.all(np.abs(h - want[0])[same] <= want[1][same])
+    # the cut sequence goes on as one that begins there
+    again = reference(dt, "sigmoid", xb[:1, 100:, 7:8], gb[:1, 100:, 7:8], None, None,
+                      dh[:1, 100:, 7:8], dl[:1, 7:8])["h"]
+    assert np.all(np.abs(h[:1, 100:, 7:8] - again[0]) <= again[1])
+
+
+@pytest.mark.parametrize("shape,offsets", [((2, 3000, 96), None), ((3000, 96), [0, 10, 10, 2900,
+                                                                                3000])])
+def test_same_bits_every_time(shape, offsets):
+    """Nothing depends on the order in which workgroups finish."""
+    say("recurrence determinism", shape)
+    n = shape[0] if offsets is None else 4
+    x, g, h0, dh, dl = make("f32", "sigmoid", shape[:-1], shape[-1], n, 12)
+    first = run("f32", "sigmoid", x, g, h0, offsets, dh, dl)
+    for _ in range(5):
+        again = run("f32", "sigmoid", x, g, h0, offsets, dh, dl)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_on_another_stream():
+    """Inputs produced on a side stream, the whole call on that stream."""
+    say("recurrence on a side stream")
+    n, steps, d = 2, 900, 64
+    x, g, h0, dh, dl = make("f32", "sigmoid", (n, steps), d, n, 13)
+    xt, gt, h0t, dht, dlt = (dev(a, torch.float32) for a in (x, g, h0, dh, dl))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        big = torch.ones(1 << 26, device=DEV)
+        for _ in range(20):
+            big.mul_(1.0)  # keeps the stream busy
+        x2 = xt * big[0]
+    h, last, saved = B.sla_linrec_forward(x2, gt, h0=h0t, save=True, stream=s)
+    dx, dg, dh0 = B.sla_linrec_backward(x2, gt, saved, dht, grad_last=dlt, h0=h0t,
+                                        stream=s.cuda_stream)
+    s.synchronize()
+    want = reference("f32", "sigmoid", x, g, h0, None, dh, dl)
+    check({"h": h, "last": last, "dx": dx, "dgate": dg, "dh0": dh0}, want, "stream")
+
+
+def test_captured_in_a_graph():
+    """Replays, with other work between them, give the eager results on the
+    inputs of each replay."""
+    say("recurrence in a graph")
+    n, steps, d = 2, 700, 64
+    sets = [make("f32", "sigmoid", (n, steps), d, n, 20 + k) for k in range(3)]
+    xt, gt, h0t, dht, dlt = (dev(a, torch.float32) for a in sets[0])
+
+    def both():
+        h, last, saved = B.sla_linrec_forward(xt, gt, h0=h0t, save=True)
+        dx, dg, dh0 = B.sla_linrec_backward(xt, gt, saved, dht, grad_last=dlt, h0=h0t)
+        return h, last, dx, dg, dh0
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for k in (0, 1, 2, 1):
+        for t, a in zip((xt, gt, h0t, dht, dlt), sets[k]):
+            t.copy_(torch.from_numpy(a))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager)), k
+
+
+def test_more_than_2_31_elements():
+    """The end of an array that 32-bit offsets would not reach, from the last
+    part alone (gates of at most one half: nothing older reaches it)."""
+    steps, d, tail = 2_100_000, 1040, 300
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    say("recurrence beyond 2^31 elements", steps * d)
+    x = torch.empty(1, steps, d, dtype=torch.bfloat16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    for a in range(0, steps, 300_000):
+        x[:, a:a + 300_000].normal_(generator=gen)
+    gate = torch.empty_like(x).copy_(x).neg_().abs_().neg_()
+    h, last, saved = B.sla_linrec_forward(x, gate, save=True)
+    xs, gs = x[:, -tail:].clone(), gate[:, -tail:].clone()
+    dh = torch.zeros_like(x)
+    dh[:, -tail:] = xs
+    dx, dg, _ = B.sla_linrec_backward(x, gate, saved, dh)
+    torch.cuda.synchronize()
+    cut = [a.double().cpu().numpy() for a in (xs, gs)]
+    want = reference("bf16", "sigmoid", cut[0], cut[1], None, None, cut[0],
+                     np.zeros((1, d)))
+    half = tail // 2  # a start from zero is forgotten by then: 2^-150
+    for t, name in ((h, "h"), (dx, "dx"), (dg, "dgate")):
+        v, e = want[name]
+        off = np.abs(t[:, -half:].double().cpu().numpy() - v[:, -half:])
+        assert np.all(off <= e[:, -half:] + 2.0 ** -130), name
+    v, e = want["last"]
+    assert np.all(np.abs(last.double().cpu().numpy() - v) <= e + 2.0 ** -130)
