@@ -433,8 +433,8 @@ sla_status sla_pcg_solve_noalloc(sla_mat_t A, sla_mat_t G, double eps, const voi
  * their gradients, (n_seq, dim), are fp32 (fp64 for SLA_F64), and so are all
  * sums and products: only h, dx and dgate are rounded, once, when stored.
  * Non-finite values propagate as in the formulas; a gate of -infinity
- * (sigmoid) or 0 (linear) cuts the sequence there unless h_{t-1} is itself
- * non-finite.
+ * (sigmoid: then a <= 2^-125, 0 in fp64) or 0 (linear) cuts the sequence there
+ * unless h_{t-1} is itself non-finite.
  */
 typedef enum { SLA_GATE_LINEAR = 0, SLA_GATE_SIGMOID = 1, SLA_GATE_RANGE_ = 0x7fffffff } sla_gate;
 
@@ -448,7 +448,7 @@ typedef struct {
 } sla_linrec_shape;
 
 /* Bytes of d_saved (the states the backward pass starts its recomputation
- * from, one per 128 steps) and of d_work for either direction (0: none needed).
+ * from, one every 32 to 256 steps) and of d_work for either direction (0: none needed).
  * Errors: SLA_ERR_INVALID_ARG (NULL, negative size, unknown dtype or gate),
  * SLA_ERR_UNSUPPORTED (a size beyond what one launch can index). */
 sla_status sla_linrec_sizes(const sla_linrec_shape *shape, size_t *saved_bytes,

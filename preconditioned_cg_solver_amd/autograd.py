@@ -9,7 +9,7 @@ Only x is saved between forward and backward.
 
 linear_recurrence does the same for the lower bidiagonal system of a gated
 recurrence along a sequence: forward substitution, and the transposed solve
-for the gradients; besides the inputs it saves one state per 128 steps.
+for the gradients; besides the inputs it saves a state every 32 to 256 steps.
 """
 from __future__ import annotations
 

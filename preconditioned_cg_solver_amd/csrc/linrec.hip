@@ -17,47 +17,55 @@
 namespace sla {
 namespace {
 
-// A workgroup takes kChunk consecutive steps of 64 V channels: each of its
-// kWaves waves kSub steps, a lane V channels of them.
-constexpr int kSub = 32;
-constexpr int kChunk = kWaves * kSub;
-
-// The coefficient and the weight of x at one step, 1 / (1 + e^-g) and
-// 1 / (1 + e^g), from e = exp(-|g|) so that neither is a difference of
-// nearly equal numbers and neither overflows.  `small` is the smaller one;
-// the other is 1 - small to half a unit in the last place.
-__device__ __forceinline__ float small_of(float g) {
-  const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
-  const float d = 1.0f + e;
-  float r = __builtin_amdgcn_rcpf(d);
-  r = fmaf(fmaf(-d, r, 1.0f), r, r);
-  return e * r;
+// A workgroup takes a chunk: W channels of as many steps as its registers
+// hold.  A thread has V neighbouring channels of consecutive steps.  The
+// backward pass holds more per element and spreads a chunk over twice the
+// threads; a chunk of the forward pass is one or more of the backward's.
+constexpr int kForward = 512, kBackward = 1024;
+// Many channels: wide rows, which memory serves faster.  Few: long chunks,
+// for then the time goes into joining one to the next.
+constexpr int kManyForward = 128, kManyBackward = 256, kNarrow = 64;
+// Whether the forward pass keeps the coefficients between its two passes over
+// a chunk, or the rows as they were loaded, which take half the registers
+// in 16 bits and allow a chunk of twice the steps.
+constexpr bool keeps(size_t size, int width) { return size > 2 || width != kNarrow; }
+constexpr int chunk_of(size_t size, int width, bool backward) {
+  return (size == 8 ? 8192 : backward || keeps(size, width) ? 16384 : 32768) / width;
 }
-__device__ __forceinline__ double small_of(double g) {
-  const double e = exp(-fabs(g));
-  return e / (1.0 + e);
+template <typename T, int W, bool BACKWARD>
+constexpr int chunk_steps() {
+  return chunk_of(sizeof(T), W, BACKWARD);
+}
+// Rows that are kept as loaded but not in pairs take a register an element.
+template <typename T, int W, int V>
+constexpr int forward_threads() {
+  return !keeps(sizeof(T), W) && V == 1 ? 2 * kForward : kForward;
 }
 
-// A step's coefficient and weight in one number: the smaller of the two,
-// negative where that is the weight (g >= 0).
+// 1 / (1 + e^-g), the coefficient, and 1 / (1 + e^g), the weight of x, neither
+// as a difference of nearly equal numbers.
+__device__ __forceinline__ void sigmoid2(float g, float& a, float& keep) {
+  const float e = __builtin_amdgcn_exp2f(-1.44269504f * g);
+  a = __builtin_amdgcn_rcpf(1.0f + e);
+  keep = e > 0x1p60f ? 1.0f : e * a;  // e may be infinite, and then a is 0
+}
+__device__ __forceinline__ void sigmoid2(double g, double& a, double& keep) {
+  const double e = exp(-fabs(g)), big = 1.0 / (1.0 + e), small = e * big;
+  a = g >= 0.0 ? big : small;
+  keep = g >= 0.0 ? small : big;
+}
+// Both in one number: the smaller, negative where that is the weight; the
+// larger is 1 less it, to half a unit in the last place.
+template <typename C>
+__device__ __forceinline__ C fold(C a, C keep) {
+  return a > keep ? -keep : a;
+}
 template <typename C>
 __device__ __forceinline__ void unfold(C s, C& a, C& keep) {
   const C m = fabs(s), big = C(1) - m;
   const bool neg = signbit(s);
   a = neg ? big : m;
   keep = neg ? m : big;
-}
-
-template <int GATE, typename C>
-__device__ __forceinline__ void coefficients(C g, C x, C& a, C& b) {
-  if constexpr (GATE == SLA_GATE_SIGMOID) {
-    C keep;
-    unfold(copysign(small_of(g), -g), a, keep);
-    b = keep * x;
-  } else {
-    a = g;
-    b = x;
-  }
 }
 
 template <typename T>
@@ -70,7 +78,7 @@ struct Args {
   const C* grad_last;
   T* h;
   C* h_last;
-  C* saved;      // the state after each chunk
+  C* saved;      // the state after each chunk of the backward pass
   T* grad_x;
   T* grad_gate;
   C* grad_h0;
@@ -78,40 +86,53 @@ struct Args {
   int64_t x_seq, x_step, g_seq, g_step, d_seq, d_step;
   int64_t n_seq, steps, dim;
   int chunks;        // dense: of each sequence
+  int chains, links, counters;  // chains of chunks, chunks of each, counters of tickets
   int blocks;        // channel blocks
   int64_t rows;      // rows of `saved`
   // joining the chunks of a sequence
   int* ticket;
-  C* sums;           // [row][channel][2]: a chunk's product of a and its sum from a zero start
+  int* progress;     // [chain][64 channels of it][link]
+  C* sums;           // [row][2][channel]: a chunk's product of a and its sum from a zero start
   C* ends;           // [row][channel]: what leaves the chunk (forward: h; backward: mu)
   const int* row_seq;  // packed: the sequence of a row
 };
 
-// A packed sequence's first row.  Rows offset / kChunk + s are distinct and
-// leave each sequence at least ceil(length / kChunk) of them, without any sum
+// A packed sequence's first row.  Rows offset / chunk + s are distinct and
+// leave each sequence at least ceil(length / chunk) of them, without any sum
 // over the lengths.
-__device__ __forceinline__ int64_t first_row(const int64_t* offsets, int64_t steps, int64_t s) {
-  return min(max(offsets[s], (int64_t)0), steps) / kChunk + s;
+__device__ __forceinline__ int64_t first_row(const int64_t* offsets, int64_t steps, int chunk,
+                                             int64_t s) {
+  return min(max(offsets[s], (int64_t)0), steps) / chunk + s;
 }
 
 // A chunk: its sequence, place and length.
 struct Where {
   int64_t s, row;
+  int64_t first;         // packed: the sequence's first step
   int64_t x, g, d, out;  // element offsets of the sequence's first step
   int64_t len;           // of the sequence
   int64_t c, after;      // chunks before and after it
+  int64_t mark;          // its place in `progress`
 };
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 // Chunk `row` of a packed sequence or of the dense sequence s.  Whatever the
 // offsets hold, the steps lie in [0, p.steps) and 0 <= c.
-template <typename T>
+template <int kChunk, typename T>
 __device__ __forceinline__ Where locate(const Args<T>& p, int64_t s, int64_t row) {
   Where w;
   w.s = s;
   w.row = row;
   if (p.offsets) {
-    const int64_t o0 = min(max(p.offsets[s], (int64_t)0), p.steps);
-    const int64_t o1 = min(max(p.offsets[s + 1], o0), p.steps);
+    const int64_t o0 = min(max(uniform(p.offsets[s]), (int64_t)0), p.steps);
+    const int64_t o1 = min(max(uniform(p.offsets[s + 1]), o0), p.steps);
+    w.first = o0;
     w.len = o1 - o0;
     w.c = p.row_seq ? max(row - (o0 / kChunk + s), (int64_t)0) : 0;
     w.x = o0 * p.x_step;
@@ -139,434 +160,582 @@ template <typename C>
 __device__ __forceinline__ bool written(C v) {
   return __builtin_bit_cast(Word<C>, v) != ~Word<C>(0);
 }
+// Addresses are a uniform array and a lane's byte offset within it.
 template <typename C>
-__device__ __forceinline__ void publish(C* to, C v) {
+__device__ __forceinline__ C* lane_ptr(C* base, uint32_t bytes) {
+  return (C*)((char*)base + bytes);
+}
+template <typename C>
+__device__ __forceinline__ const C* lane_ptr(const C* base, uint32_t bytes) {
+  return (const C*)((const char*)base + bytes);
+}
+template <typename C>
+__device__ __forceinline__ void publish(C* base, uint32_t bytes, C v) {
   Word<C> u = __builtin_bit_cast(Word<C>, v);
   if (u == ~Word<C>(0)) u = __builtin_bit_cast(Word<C>, C(NAN));
-  __hip_atomic_store((Word<C>*)to, u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store((Word<C>*)lane_ptr(base, bytes), u, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
 }
 template <typename C>
-__device__ __forceinline__ C look(const C* at) {
-  return __builtin_bit_cast(
-      C, __hip_atomic_load((const Word<C>*)at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+__device__ __forceinline__ C look(const C* base, uint32_t bytes) {
+  return __builtin_bit_cast(C, __hip_atomic_load((const Word<C>*)lane_ptr(base, bytes),
+                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
+// How far a chunk is, per 64 of its channels: a hint of which words are worth
+// reading, so that waiting costs one cache line per look.
+enum Progress { kNothing = 0, kSums = 1, kEnd = 2 };
+
 // What enters a chunk, from the chunks before it (forward: STEP = -1) or
-// after it (backward: STEP = 1), `have` of them in the sequence: the nearest
-// one whose end is known, carried over the sums of those between.  The sums
-// are applied one by one from the far end, as each chunk's own end is
-// computed, so the bits do not depend on how far the look went.  K ends are
-// tried at once, in one trip to memory.
-template <int K, int V, int STEP, typename C>
-__device__ __forceinline__ bool try_carry(const C* ends, const C* sums, int64_t dim, int have,
-                                          C (&carry)[V]) {
-  C e[K][V], a[K][V], m[K][V];
+// after it (backward: STEP = 1), `have` of them in the sequence, channel by
+// lane: the end of the nearest one whose end is known, carried over the sums
+// of those between.  The sums are applied one by one from the far end, as
+// each chunk's own end is computed, so the bits do not depend on how far the
+// look went.  progress, ends and sums point at the nearest chunk's.
+
+// The nearest K, in one trip to memory.
+template <int K, int STEP, typename C>
+__device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_t bytes,
+                                           int64_t dim, int have, C& carry) {
+  C e[K], a[K], m[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (j < have) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        e[j][v] = look(ends + STEP * j * dim + v);
-        if (j + 1 < K) {
-          a[j][v] = look(sums + 2 * (STEP * j * dim + v));
-          m[j][v] = look(sums + 2 * (STEP * j * dim + v) + 1);
-        }
-      }
+    const int64_t off = STEP * min(j, have - 1) * dim;
+    e[j] = look(ends + off, bytes);
+    if (j + 1 < K) {
+      a[j] = look(sums + 2 * off, bytes);
+      m[j] = look(sums + 2 * off + dim, bytes);
     }
   }
-  bool found = false, open = true;  // open: the sums so far are all known
+  int at = -1;
+  bool open = true;  // the sums so far are all known
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (j < have && open && !found) {
-      bool known = true, sum = true;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        known = known && written(e[j][v]);
-        if (j + 1 < K) sum = sum && written(a[j][v]) && written(m[j][v]);
-      }
-      if (__all(known)) {
-        found = true;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          C h = e[j][v];
-#pragma unroll
-          for (int q = j - 1; q >= 0; --q) h = a[q][v] * h + m[q][v];
-          carry[v] = h;
-        }
-      } else if (!__all(sum)) {
-        open = false;
-      }
-    }
+    if (open && at < 0 && j < have && __all(written(e[j]))) at = j;
+    if (j + 1 < K) open = open && __all(written(a[j]) && written(m[j]));
   }
-  return found;
+  if (at < 0) return false;
+  carry = e[0];
+#pragma unroll
+  for (int j = K - 1; j >= 0; --j) {
+    if (j == at) carry = e[j];
+    if (j + 1 < K && j < at) carry = a[j] * carry + m[j];
+  }
+  return true;
 }
 
 // Every chunk publishes its sums before it waits for anything, and a chunk
 // waits only for chunks whose tickets were drawn before its own, by
 // workgroups that therefore run already: the wait ends.
-template <int V, int STEP, typename C>
-__device__ __forceinline__ void wait_carry(const C* ends, const C* sums, int64_t dim, int have,
-                                           C (&carry)[V]) {
-  if (try_carry<2, V, STEP>(ends, sums, dim, have, carry)) return;
-  while (!try_carry<8, V, STEP>(ends, sums, dim, have, carry)) __builtin_amdgcn_s_sleep(1);
+constexpr int kReach = 32, kBatch = 8;
+template <int NEAR, int STEP, typename C>
+__device__ __forceinline__ C wait_carry(const int* progress, const C* ends, const C* sums,
+                                        uint32_t bytes, int64_t dim, int64_t have) {
+  const int n = (int)min(have, (int64_t)kReach), lane = threadIdx.x & 63;
+  C near = C(0);
+  if (near_carry<NEAR, STEP>(ends, sums, bytes, dim, n, near)) return near;
+  for (;; __builtin_amdgcn_s_sleep(1)) {
+    int f = kNothing;
+    if (lane < n)
+      f = __hip_atomic_load(progress + STEP * lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint64_t done = __ballot(f >= kEnd), some = __ballot(f >= kSums);
+    if (done == 0) continue;
+    const int j = __builtin_ctzll(done);
+    const uint64_t between = (1ull << j) - 1;
+    if ((some & between) != between) continue;
+    C h = look(ends + STEP * j * dim, bytes);
+    bool ok = true;
+    for (int top = j; top > 0; top -= kBatch) {
+      C a[kBatch], m[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int64_t off = STEP * max(top - 1 - q, 0) * 2 * dim;
+        a[q] = look(sums + off, bytes);
+        m[q] = look(sums + off + dim, bytes);
+      }
+      if (top == j) ok = written(h);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (top - 1 - q >= 0) {
+          ok = ok && written(a[q]) && written(m[q]);
+          h = a[q] * h + m[q];
+        }
+      }
+    }
+    if (j == 0) ok = written(h);
+    if (__all(ok)) return h;
+  }
 }
+__device__ __forceinline__ void tell(int* progress, Progress v) {
+  if ((threadIdx.x & 63) == 0)
+    __hip_atomic_store(progress, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Tickets are drawn from kCounters counters at most, kTicketStep bytes apart:
+// one for all would serve its atomics one after the other.
+constexpr int kCounters = 64, kTicketStep = 64;
 
 // Marks every word as not written, zeroes the ticket and finds each row's
 // sequence: the last one that begins at or before it.
 template <typename C>
 __global__ __launch_bounds__(kWG) void rec_begin(Word<C>* sums, int64_t n_sums, Word<C>* ends,
-                                                 int64_t n_ends, int* ticket, int* row_seq,
+                                                 int64_t n_ends, int* ticket, int* progress,
+                                                 int64_t n_progress, int* row_seq,
                                                  int64_t rows, const int64_t* offsets,
-                                                 int64_t n_seq, int64_t steps) {
+                                                 int64_t n_seq, int64_t steps, int chunk) {
   const int64_t i0 = (int64_t)blockIdx.x * kWG + threadIdx.x, n = (int64_t)gridDim.x * kWG;
-  if (i0 == 0) *ticket = 0;
+  if (i0 < kCounters) ticket[i0 * (kTicketStep / sizeof(int))] = 0;
   for (int64_t i = i0; i < n_sums; i += n) sums[i] = ~Word<C>(0);
   for (int64_t i = i0; i < n_ends; i += n) ends[i] = ~Word<C>(0);
+  for (int64_t i = i0; i < n_progress; i += n) progress[i] = kNothing;
   if (!row_seq) return;
   for (int64_t r = i0; r < rows; r += n) {
     int64_t lo = 0, hi = n_seq;  // first_row(lo) <= r < first_row(hi)
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;
-      if (first_row(offsets, steps, mid) <= r) lo = mid;
+      if (first_row(offsets, steps, chunk, mid) <= r) lo = mid;
       else hi = mid;
     }
     row_seq[r] = (int)lo;
   }
 }
 
-// This workgroup's chunk and channel block.  CHAIN: by ticket, so that the
-// chunks it waits for are under way, all sequences' first chunks first
-// (packed: in the order of rows); REVERSE: from the last chunk on.
-template <bool CHAIN, bool REVERSE, typename T>
-__device__ __forceinline__ Where my_chunk(const Args<T>& p, int& block) {
+// This workgroup's chunk and channel block; false if there is none for it.
+// CHAIN: the chunks of a sequence and channel block (packed: of a channel
+// block) form a chain, each handed out by ticket before those that wait for
+// it (REVERSE: from the last chunk on); a counter serves every
+// p.counters-th chain.
+template <int W, bool CHAIN, bool REVERSE, typename T>
+__device__ __forceinline__ bool my_chunk(const Args<T>& p, Where& w, int& block) {
   if constexpr (!CHAIN) {
     const int64_t s = blockIdx.x / (unsigned)p.blocks;
     block = blockIdx.x % (unsigned)p.blocks;
-    return locate(p, s, p.offsets ? 0 : s * p.chunks);
+    w = locate<chunk_steps<T, W, REVERSE>()>(p, s, p.offsets ? 0 : s * p.chunks);
+    return true;
   } else {
     __shared__ int drawn;
+    const unsigned J = p.counters, j = blockIdx.x % J;
     if (threadIdx.x == 0)
-      drawn = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      drawn = __hip_atomic_fetch_add(p.ticket + j * (kTicketStep / sizeof(int)), 1,
+                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     const unsigned k = __builtin_amdgcn_readfirstlane(drawn);
-    block = k % (unsigned)p.blocks;
-    unsigned r = k / (unsigned)p.blocks;
-    if (p.offsets) {
-      const int64_t row = REVERSE ? p.rows - 1 - r : r;
-      return locate(p, p.row_seq[row], row);
-    }
-    unsigned c = r / (unsigned)p.n_seq;
-    const int64_t s = r % (unsigned)p.n_seq;
-    if (REVERSE) c = p.chunks - 1 - c;
-    return locate(p, s, s * p.chunks + c);
+    const unsigned chains = (p.chains - j + J - 1) / J;  // of this counter
+    unsigned c = k / chains;
+    const unsigned chain = j + k % chains * J;
+    if (c >= (unsigned)p.links) return false;
+    if (REVERSE) c = p.links - 1 - c;
+    block = chain % (unsigned)p.blocks;
+    const int64_t s = p.offsets ? __builtin_amdgcn_readfirstlane(p.row_seq[c])
+                                : chain / (unsigned)p.blocks;
+    w = locate<chunk_steps<T, W, REVERSE>()>(p, s, p.offsets ? (int64_t)c : s * p.chunks + c);
+    w.mark = (int64_t)chain * (W / 64) * p.links + c;
+    return true;
   }
 }
 
-// Rows [0, nv) of kSub, V channels each; rows from nv on are the last one
-// again.  `base` is uniform, so the row addresses are scalar.
-template <int V, typename T>
-__device__ __forceinline__ void load_rows(const T* base, int64_t step, unsigned lane_at, int nv,
-                                          Pack<T, V> (&r)[kSub]) {
-  if (nv == kSub) {
+// A thread's part of a chunk: V channels of S steps.
+template <typename T, int W, int V, int N, bool BACKWARD>
+struct Part {
+  static constexpr int kChunk = chunk_steps<T, W, BACKWARD>();
+  static constexpr int kWidth = W, kPer = V;
+  static constexpr int kLanes = W / V;         // per row
+  static constexpr int kSubs = N / kLanes;         // parts along the steps
+  static constexpr int S = kChunk / kSubs;
+  int sub, c0;       // its place among them, its first channel within the block
+  bool act;          // it has channels
+  int64_t at;        // the first one (0 where it has none)
+  int64_t t0;        // first step
+  int nv;            // steps
+  bool full;         // the whole chunk has all its steps
+};
+template <typename P, typename T>
+__device__ __forceinline__ P my_part(const Args<T>& p, const Where& w, int block) {
+  constexpr int kChunk = P::kChunk;
+  P r;
+  r.sub = threadIdx.x / P::kLanes;
+  r.c0 = threadIdx.x % P::kLanes * P::kPer;
+  const int64_t ch = (int64_t)block * P::kWidth + r.c0;
+  r.act = ch < p.dim;
+  r.at = r.act ? ch : 0;
+  r.full = w.len - w.c * kChunk >= kChunk;
+  r.t0 = w.c * kChunk + r.sub * P::S;
+  r.nv = (int)min(max(w.len - r.t0, (int64_t)0), (int64_t)P::S);
+  return r;
+}
+
+// A thread's rows of an input; steps past the sequence's end hold `none`.
+template <int S, int V, typename T>
+__device__ __forceinline__ void load_part(const T* first, int64_t step, int64_t t0, int nv,
+                                          bool full, T none, Pack<T, V> (&r)[S]) {
+  const T* row = first + t0 * step;
+  if (full) {
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) r[i] = *(const Pack<T, V>*)(base + i * step + lane_at);
+    for (int i = 0; i < S; ++i) r[i] = *(const Pack<T, V>*)(row + i * step);
   } else {
 #pragma unroll
-    for (int i = 0; i < kSub; ++i)
-      r[i] = *(const Pack<T, V>*)(base + min(i, nv - 1) * step + lane_at);
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[i].v[v] = none;
+      if (i < nv) r[i] = *(const Pack<T, V>*)row;
+      row += step;
+    }
+  }
+}
+// The gate of a step that does nothing (with x = 0): coefficient 1, weight 0.
+template <int GATE, typename T>
+__device__ __forceinline__ T idle_gate() {
+  return (T)(GATE == SLA_GATE_SIGMOID ? INFINITY : 1.0f);
+}
+
+// Keeps the compiler from carrying over what it derived from these elements.
+template <typename T, int V>
+__device__ __forceinline__ void forget(Pack<T, V>& p) {
+  if constexpr (sizeof(p) < 4) {
+    uint16_t u;
+    __builtin_memcpy(&u, &p, 2);
+    asm volatile("" : "+v"(u));
+    __builtin_memcpy(&p, &u, 2);
+  } else {
+    uint32_t u[sizeof(p) / 4];
+    __builtin_memcpy(u, &p, sizeof(p));
+#pragma unroll
+    for (size_t k = 0; k < sizeof(p) / 4; ++k) asm volatile("" : "+v"(u[k]));
+    __builtin_memcpy(&p, u, sizeof(p));
   }
 }
 
-// WAVES: waves along the steps of a chunk (kWaves, or 1 where the whole
-// sequence fits one wave's rows; then each wave has its own channels).
-template <typename T, int GATE, int V, int WAVES, bool CHAIN>
-__global__ __launch_bounds__(kWG, 2) void rec_forward(Args<T> p) {
+// Keeps a pass over the rows in their order, four elements at a time: taken
+// together, the rows' intermediate values would not fit the registers.
+template <int V>
+__device__ __forceinline__ void row_fence(int i) {
+  if ((i + 1) * V % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+}
+
+// One chunk of a sequence.  CHAIN: sequences may have several, joined by the
+// look-back; otherwise each has one.
+template <typename T, int GATE, int W, int V, bool CHAIN>
+__global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(Args<T> p) {
   using C = typename Compute<T>::type;
-  constexpr int kWidth = 64 * V;
-  __shared__ C s_a[WAVES][kWidth], s_m[WAVES][kWidth], s_in[kWidth];
+  using P = Part<T, W, V, forward_threads<T, W, V>(), false>;
+  constexpr int SAVE = chunk_steps<T, W == kNarrow ? kNarrow : kManyBackward, true>();
+  constexpr bool kSig = GATE == SLA_GATE_SIGMOID;
+  constexpr int S = P::S, kSubs = P::kSubs;
+  __shared__ C s_a[kSubs][W], s_m[kSubs][W];
   int block;
-  const Where w = my_chunk<CHAIN, false>(p, block);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = WAVES == 1 ? 0 : wave;
-  const int64_t ch = ((int64_t)block * (kWaves / WAVES) + (WAVES == 1 ? wave : 0)) * kWidth +
-                     lane * V;
-  const bool act = ch < p.dim;
-  const int64_t at = act ? ch : 0;
-  const int64_t t0 = w.c * kChunk + part * kSub;
-  const int nv = (int)min(max(w.len - t0, (int64_t)0), (int64_t)kSub);
+  Where w;
+  if (!my_chunk<W, CHAIN, false>(p, w, block)) return;
+  const P r = my_part<P>(p, w, block);
 
-  C a[kSub][V], b[kSub][V];
-  if (nv > 0) {
-    Pack<T, V> x[kSub], g[kSub];
-    load_rows<V>(p.gate + w.g + t0 * p.g_step, p.g_step, (unsigned)at, nv, g);
-    load_rows<V>(p.x + w.x + t0 * p.x_step, p.x_step, (unsigned)at, nv, x);
+  // The rows as loaded or, where they fit, the coefficients they give; else
+  // each of the two passes over them works those out.
+  constexpr bool kKeep = keeps(sizeof(T), W);
+  Pack<T, V> x[S], g[S];
+  C ka[kKeep ? S : 1][V], kb[kKeep ? S : 1][V];
+  load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, idle_gate<GATE, T>(), g);
+  load_part<S, V>(p.x + w.x + r.at, p.x_step, r.t0, r.nv, r.full, (T)0.0f, x);
+  auto coefficients = [&](int i, int v, C& a, C& b) {
+    b = (C)x[i].v[v];
+    a = (C)g[i].v[v];
+    if constexpr (kSig) {
+      C keep;
+      sigmoid2((C)g[i].v[v], a, keep);
+      b *= keep;
+    }
+  };
+  {
+    C pa[V], pm[V];
 #pragma unroll
-    for (int i = 0; i < kSub; ++i)
+    for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        coefficients<GATE, C>((C)g[i].v[v], (C)x[i].v[v], a[i][v], b[i][v]);
-        if (i >= nv) a[i][v] = C(1), b[i][v] = C(0);
+        C a, b;
+        coefficients(i, v, a, b);
+        if constexpr (kKeep) ka[i][v] = a, kb[i][v] = b;
+        pm[v] = a * pm[v] + b;
+        pa[v] *= a;
       }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kSub; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) a[i][v] = C(1), b[i][v] = C(0);
-  }
-
-  C h[V];
-  if constexpr (WAVES > 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      C pa = C(1), pm = C(0);
-#pragma unroll
-      for (int i = 0; i < kSub; ++i) {
-        pm = a[i][v] * pm + b[i][v];
-        pa *= a[i][v];
-      }
-      s_a[wave][lane * V + v] = pa;
-      s_m[wave][lane * V + v] = pm;
+      row_fence<V>(i);
     }
-    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_a[r.sub][r.c0 + v] = pa[v], s_m[r.sub][r.c0 + v] = pm[v];
   }
-  if (wave == 0 || WAVES == 1) {
-    const int64_t row_at = w.row * p.dim + at;
-    C ca[V], cm[V];
-    if constexpr (CHAIN) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        ca[v] = C(1), cm[v] = C(0);
-#pragma unroll
-        for (int q = 0; q < WAVES; ++q) {
-          cm[v] = s_a[q][lane * V + v] * cm[v] + s_m[q][lane * V + v];
-          ca[v] *= s_a[q][lane * V + v];
-        }
-        if (act) {
-          publish(p.sums + 2 * (row_at + v), ca[v]);
-          publish(p.sums + 2 * (row_at + v) + 1, cm[v]);
-        }
-      }
+  __syncthreads();
+  // From here a lane has a channel, in the first W / 64 waves.
+  const int64_t ch0 = (int64_t)block * W, row0 = w.row * p.dim + ch0;
+  const int channels = (int)min((int64_t)W, p.dim - ch0);
+  const bool join = threadIdx.x < W, act = (int)threadIdx.x < channels;
+  const uint32_t at = act ? threadIdx.x * (uint32_t)sizeof(C) : 0;
+  C *ends = p.ends + row0, *sums = p.sums + row0 + w.row * p.dim;
+  int* mark = p.progress + w.mark + (int64_t)(threadIdx.x >> 6) * p.links;
+  C ca = C(1), cm = C(0), h = C(0);
+  if (CHAIN && join) {
+#pragma unroll 4
+    for (int q = 0; q < kSubs; ++q) {
+      const C pa = s_a[q][threadIdx.x];
+      cm = pa * cm + s_m[q][threadIdx.x];
+      ca *= pa;
     }
-    if (!CHAIN || w.c == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = p.h0 ? p.h0[w.s * p.dim + at + v] : C(0);
-    } else {
-      wait_carry<V, -1>(p.ends + row_at - p.dim, p.sums + 2 * (row_at - p.dim), p.dim,
-                        (int)min(w.c, (int64_t)64), h);
+    if (act) {
+      publish(sums, at, ca);
+      publish(sums + p.dim, at, cm);
+    }
+    tell(mark, kSums);
+  }
+  if (join) {
+    if (w.c == 0) {
+      if (p.h0) h = *lane_ptr(p.h0 + w.s * p.dim + ch0, at);
+    } else if constexpr (CHAIN) {
+      h = wait_carry<4, -1>(mark - 1, ends - p.dim, sums - 2 * p.dim, at, p.dim, w.c);
     }
     if constexpr (CHAIN) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (act) publish(p.ends + row_at + v, ca[v] * h[v] + cm[v]);
+      if (act) publish(ends, at, ca * h + cm);
+      tell(mark, kEnd);
     }
-    if (w.len == 0 && w.c == 0 && act && p.h_last) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.h_last[w.s * p.dim + at + v] = h[v];
-    }
-    if constexpr (WAVES > 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_in[lane * V + v] = h[v];
-    }
-  }
-  if constexpr (WAVES > 1) {
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = s_in[lane * V + v];
-      for (int q = 0; q < wave; ++q)
-        h[v] = s_a[q][lane * V + v] * h[v] + s_m[q][lane * V + v];
+    if (w.len == 0 && w.c == 0 && act && p.h_last)
+      *lane_ptr(p.h_last + w.s * p.dim + ch0, at) = h;
+    // what enters each part, in the place of its sum
+#pragma unroll 4
+    for (int q = 0; q < kSubs; ++q) {
+      const C next = s_a[q][threadIdx.x] * h + s_m[q][threadIdx.x];
+      s_m[q][threadIdx.x] = h;
+      h = next;
+      // the state where a chunk of the backward pass ends and another follows
+      const int64_t t = w.c * P::kChunk + (q + 1) * S;
+      if (p.saved && (q + 1) * S % SAVE == 0 && t < w.len && act) {
+        const int64_t first = p.offsets ? w.first / SAVE + w.s : w.s * ((p.steps + SAVE - 1) / SAVE);
+        *lane_ptr(p.saved + (first + t / SAVE - 1) * p.dim + ch0, at) = h;
+      }
     }
   }
-  if (nv == 0 || !act) return;
-  T* out = p.h + w.out + t0 * p.dim;
+  __syncthreads();
+  if (r.nv == 0 || !r.act) return;
+  if constexpr (!kKeep) {
 #pragma unroll
-  for (int i = 0; i < kSub; ++i) {
+    for (int i = 0; i < S; ++i) forget(x[i]), forget(g[i]);
+  }
+  C hv[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) hv[v] = s_m[r.sub][r.c0 + v];
+  T* out = p.h + w.out + r.t0 * p.dim + r.at;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
     Pack<T, V> o;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = a[i][v] * h[v] + b[i][v];
-      o.v[v] = (T)h[v];
+      C a, b;
+      if constexpr (kKeep) a = ka[i][v], b = kb[i][v];
+      else coefficients(i, v, a, b);
+      hv[v] = a * hv[v] + b;
+      o.v[v] = (T)hv[v];
     }
-    if (i < nv) *(Pack<T, V>*)(out + i * p.dim + (unsigned)at) = o;
+    if (i < r.nv) *(Pack<T, V>*)(out + i * p.dim) = o;
+    row_fence<V>(i);
   }
-  // rows past the end leave h as it was
-  if (t0 + nv == w.len && p.h_last) {
+  if (r.t0 + r.nv == w.len && p.h_last) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.h_last[w.s * p.dim + at + v] = h[v];
+    for (int v = 0; v < V; ++v) p.h_last[w.s * p.dim + r.at + v] = hv[v];
   }
 }
 
-template <typename T, int GATE, int V, int WAVES, bool CHAIN>
-__global__ __launch_bounds__(kWG, 2) void rec_backward(Args<T> p) {
+template <typename T, int GATE, int W, int V, bool CHAIN>
+__global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backward(Args<T> p) {
   using C = typename Compute<T>::type;
-  constexpr int kWidth = 64 * V;
+  using P = Part<T, W, V, kBackward, true>;
   constexpr bool kSig = GATE == SLA_GATE_SIGMOID;
-  __shared__ C s_a[WAVES][kWidth], s_m[WAVES][kWidth], s_u[WAVES][kWidth], s_in[kWidth],
-      s_mu[kWidth];
+  constexpr int S = P::S, kSubs = P::kSubs;
+  __shared__ C s_a[kSubs][W], s_m[kSubs][W], s_u[kSubs][W];
+  __shared__ Pack<T, V> s_d[S][kBackward];
   int block;
-  const Where w = my_chunk<CHAIN, true>(p, block);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = WAVES == 1 ? 0 : wave;
-  const int64_t ch = ((int64_t)block * (kWaves / WAVES) + (WAVES == 1 ? wave : 0)) * kWidth +
-                     lane * V;
-  const bool act = ch < p.dim;
-  const int64_t at = act ? ch : 0;
-  const int64_t t0 = w.c * kChunk + part * kSub;
-  const int nv = (int)min(max(w.len - t0, (int64_t)0), (int64_t)kSub);
+  Where w;
+  if (!my_chunk<W, CHAIN, true>(p, w, block)) return;
+  const P r = my_part<P>(p, w, block);
 
-  // f: linear the coefficient, sigmoid coefficient and weight folded into one
-  // number.  z: x, later h_{t-1} - x (linear: h_{t-1}).
-  C f[kSub][V], z[kSub][V];
-  Pack<T, V> d[kSub];
-  if (nv > 0) {
-    Pack<T, V> x[kSub], g[kSub];
-    load_rows<V>(p.gate + w.g + t0 * p.g_step, p.g_step, (unsigned)at, nv, g);
-    load_rows<V>(p.x + w.x + t0 * p.x_step, p.x_step, (unsigned)at, nv, x);
-    if (p.grad_h) load_rows<V>(p.grad_h + w.d + t0 * p.d_step, p.d_step, (unsigned)at, nv, d);
-#pragma unroll
-    for (int i = 0; i < kSub; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const C gv = (C)g[i].v[v];
-        f[i][v] = kSig ? copysign(small_of(gv), -gv) : gv;
-        z[i][v] = (C)x[i].v[v];
-        if (i >= nv) f[i][v] = kSig ? C(-0.0) : C(1), z[i][v] = C(0);
-        if (i >= nv || !p.grad_h) d[i].v[v] = (T)0.0f;
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kSub; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        f[i][v] = kSig ? C(-0.0) : C(1), z[i][v] = C(0), d[i].v[v] = (T)0.0f;
-  }
-  // Each pass over the steps unfolds f again: held unfolded, the two arrays
-  // would not fit the registers, so the compiler is kept from reusing them.
-  auto step = [&](C& fv, C& a, C& keep) {
+  // f: the coefficient, for the sigmoid folded with the weight of x: held
+  // apart, the two would not fit the registers, so the compiler is kept from
+  // carrying them over from pass to pass.  dL/dh waits in LDS.
+  C f[S][V];
+  Pack<T, V> x[S];
+  auto step = [&](int i, int v, C& a, C& keep) {
     if constexpr (kSig) {
-      asm volatile("" : "+v"(fv));
-      unfold(fv, a, keep);
+      asm volatile("" : "+v"(f[i][v]));
+      unfold(f[i][v], a, keep);
     } else {
-      a = fv, keep = C(1);
+      a = f[i][v], keep = C(1);
     }
   };
-
-  C h[V], mu[V];
-  if constexpr (WAVES > 1) {
+  {
+    C pa[V], pm[V], pu[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      C pa = C(1), pm = C(0), pu = C(0), a, keep;
+    for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0), pu[v] = C(0);
+    Pack<T, V> g[S], d[S];
+    load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, idle_gate<GATE, T>(), g);
+    load_part<S, V>(p.x + w.x + r.at, p.x_step, r.t0, r.nv, r.full, (T)0.0f, x);
+    load_part<S, V>(p.grad_h + w.d + r.at, p.d_step, r.t0, p.grad_h ? r.nv : 0,
+                    r.full && p.grad_h, (T)0.0f, d);
 #pragma unroll
-      for (int i = 0; i < kSub; ++i) {
-        step(f[i][v], a, keep);
-        pm = a * pm + (kSig ? keep * z[i][v] : z[i][v]);
-        pa *= a;
-      }
-#pragma unroll
-      for (int i = kSub - 1; i >= 0; --i) {
-        step(f[i][v], a, keep);
-        pu = a * ((C)d[i].v[v] + pu);
-      }
-      s_a[wave][lane * V + v] = pa;
-      s_m[wave][lane * V + v] = pm;
-      s_u[wave][lane * V + v] = pu;
-    }
-    __syncthreads();
-  }
-  if (wave == 0 || WAVES == 1) {
-    const int64_t row_at = w.row * p.dim + at;
-    C ca[V], cu[V];
-    if constexpr (CHAIN) {
+    for (int i = 0; i < S; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        ca[v] = C(1), cu[v] = C(0);
-#pragma unroll
-        for (int q = WAVES - 1; q >= 0; --q) {
-          cu[v] = s_a[q][lane * V + v] * cu[v] + s_u[q][lane * V + v];
-          ca[v] *= s_a[q][lane * V + v];
+        C a = (C)g[i].v[v], keep, b = (C)x[i].v[v];
+        f[i][v] = a;
+        if constexpr (kSig) {
+          sigmoid2((C)g[i].v[v], a, keep);
+          f[i][v] = fold(a, keep);
+          b *= keep;
         }
-        if (act) {
-          publish(p.sums + 2 * (row_at + v), ca[v]);
-          publish(p.sums + 2 * (row_at + v) + 1, cu[v]);
-        }
+        pm[v] = a * pm[v] + b;
+        pa[v] *= a;
+        pu[v] = pa[v] * (C)d[i].v[v] + pu[v];  // mu leaving the part, from a zero start
       }
+      s_d[i][threadIdx.x] = d[i];
+      forget(x[i]);
+      row_fence<V>(i);
     }
-    if (w.c == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = p.h0 ? p.h0[w.s * p.dim + at + v] : C(0);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = p.saved[row_at - p.dim + v];
+    for (int v = 0; v < V; ++v) {
+      s_a[r.sub][r.c0 + v] = pa[v];
+      s_m[r.sub][r.c0 + v] = pm[v];
+      s_u[r.sub][r.c0 + v] = pu[v];
     }
-    if (!CHAIN || w.after == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) mu[v] = p.grad_last ? p.grad_last[w.s * p.dim + at + v] : C(0);
-    } else {
-      wait_carry<V, 1>(p.ends + row_at + p.dim, p.sums + 2 * (row_at + p.dim), p.dim,
-                       (int)min(w.after, (int64_t)64), mu);
+  }
+  __syncthreads();
+  const int64_t ch0 = (int64_t)block * W, row0 = w.row * p.dim + ch0;
+  const int64_t state0 = w.s * p.dim + ch0;
+  const int channels = (int)min((int64_t)W, p.dim - ch0);
+  const bool join = threadIdx.x < W, act = (int)threadIdx.x < channels;
+  const uint32_t at = act ? threadIdx.x * (uint32_t)sizeof(C) : 0;
+  C *ends = p.ends + row0, *sums = p.sums + row0 + w.row * p.dim;
+  int* mark = p.progress + w.mark + (int64_t)(threadIdx.x >> 6) * p.links;
+  C ca = C(1), cu = C(0), mu = C(0);
+  if (join) {
+    if constexpr (CHAIN) {
+#pragma unroll 4
+      for (int q = kSubs - 1; q >= 0; --q) {
+        const C pa = s_a[q][threadIdx.x];
+        cu = pa * cu + s_u[q][threadIdx.x];
+        ca *= pa;
+      }
+      if (act) {
+        publish(sums, at, ca);
+        publish(sums + p.dim, at, cu);
+      }
+      tell(mark, kSums);
+    }
+    C h = C(0);
+    if (w.c > 0) h = *lane_ptr(p.saved + row0 - p.dim, at);
+    else if (p.h0) h = *lane_ptr(p.h0 + state0, at);
+    // what enters each part from before, in the place of its sum
+#pragma unroll 4
+    for (int q = 0; q < kSubs; ++q) {
+      const C next = s_a[q][threadIdx.x] * h + s_m[q][threadIdx.x];
+      s_m[q][threadIdx.x] = h;
+      h = next;
+    }
+    if (w.after == 0) {
+      if (p.grad_last) mu = *lane_ptr(p.grad_last + state0, at);
+    } else if constexpr (CHAIN) {
+      mu = wait_carry<2, 1>(mark + 1, ends + p.dim, sums + 2 * p.dim, at, p.dim, w.after);
     }
     if constexpr (CHAIN) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (act) publish(p.ends + row_at + v, ca[v] * mu[v] + cu[v]);
+      if (act) publish(ends, at, ca * mu + cu);
+      tell(mark, kEnd);
     }
-    if (w.len == 0 && w.c == 0 && act && p.grad_h0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.grad_h0[w.s * p.dim + at + v] = mu[v];
-    }
-    if constexpr (WAVES > 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_in[lane * V + v] = h[v], s_mu[lane * V + v] = mu[v];
+    if (w.len == 0 && w.c == 0 && act && p.grad_h0) *lane_ptr(p.grad_h0 + state0, at) = mu;
+#pragma unroll 4
+    for (int q = kSubs - 1; q >= 0; --q) {
+      const C next = s_a[q][threadIdx.x] * mu + s_u[q][threadIdx.x];
+      s_u[q][threadIdx.x] = mu;
+      mu = next;
     }
   }
-  if constexpr (WAVES > 1) {
-    __syncthreads();
+  __syncthreads();
+  if (r.nv == 0 || !r.act) return;
+  C h[V], mv[V], z[S][V];  // z: h_{t-1} - x (linear: h_{t-1})
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = s_in[lane * V + v];
-      for (int q = 0; q < wave; ++q)
-        h[v] = s_a[q][lane * V + v] * h[v] + s_m[q][lane * V + v];
-      mu[v] = s_mu[lane * V + v];
-      for (int q = WAVES - 1; q > wave; --q)
-        mu[v] = s_a[q][lane * V + v] * mu[v] + s_u[q][lane * V + v];
-    }
-  }
-  if (nv == 0 || !act) return;
+  for (int v = 0; v < V; ++v) h[v] = s_m[r.sub][r.c0 + v], mv[v] = s_u[r.sub][r.c0 + v];
 #pragma unroll
-  for (int i = 0; i < kSub; ++i)
+  for (int i = 0; i < S; ++i) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       C a, keep;
-      step(f[i][v], a, keep);
-      const C before = h[v], x = z[i][v];
-      h[v] = a * h[v] + (kSig ? keep * x : x);
-      z[i][v] = kSig ? before - x : before;
+      step(i, v, a, keep);
+      const C xv = (C)x[i].v[v];
+      z[i][v] = kSig ? h[v] - xv : h[v];
+      h[v] = a * h[v] + (kSig ? keep * xv : xv);
     }
-  T* ox = p.grad_x + w.out + t0 * p.dim;
-  T* og = p.grad_gate + w.out + t0 * p.dim;
+    row_fence<V>(i);
+  }
+  T* ox = p.grad_x + w.out + r.t0 * p.dim + r.at;
+  T* og = p.grad_gate + w.out + r.t0 * p.dim + r.at;
 #pragma unroll
-  for (int i = kSub - 1; i >= 0; --i) {
+  for (int i = S - 1; i >= 0; --i) {
     Pack<T, V> rx, rg;
+    const Pack<T, V> d = s_d[i][threadIdx.x];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       C a, keep;
-      step(f[i][v], a, keep);
-      const C lam = (C)d[i].v[v] + mu[v];
-      mu[v] = a * lam;
+      step(i, v, a, keep);
+      const C lam = (C)d.v[v] + mv[v];
+      mv[v] = a * lam;
       rx.v[v] = (T)(kSig ? lam * keep : lam);
-      rg.v[v] = (T)(kSig ? mu[v] * z[i][v] * keep : lam * z[i][v]);
+      rg.v[v] = (T)(kSig ? mv[v] * z[i][v] * keep : lam * z[i][v]);
     }
-    if (i < nv) {
-      *(Pack<T, V>*)(ox + i * p.dim + (unsigned)at) = rx;
-      *(Pack<T, V>*)(og + i * p.dim + (unsigned)at) = rg;
+    if (i < r.nv) {
+      *(Pack<T, V>*)(ox + i * p.dim) = rx;
+      *(Pack<T, V>*)(og + i * p.dim) = rg;
     }
+    row_fence<V>(i);
   }
   // mu has passed the first step
-  if (t0 == 0 && p.grad_h0) {
+  if (r.t0 == 0 && p.grad_h0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.grad_h0[w.s * p.dim + at + v] = mu[v];
+    for (int v = 0; v < V; ++v) p.grad_h0[w.s * p.dim + r.at + v] = mv[v];
+  }
+}
+
+// Sequences of a few steps, a serving step above all: a thread takes V
+// channels from the first step to the last.
+constexpr int kFew = 8;
+template <typename T, int GATE, int V>
+__global__ __launch_bounds__(kWG) void few_forward(Args<T> p) {
+  using C = typename Compute<T>::type;
+  const int64_t k = (int64_t)blockIdx.x * kWG + threadIdx.x, per = p.dim / V;
+  if (k >= p.n_seq * per) return;
+  const int64_t s = k / per, at = k % per * V;
+  int64_t first = 0, len = p.steps;
+  if (p.offsets) {
+    first = min(max(p.offsets[s], (int64_t)0), p.steps);
+    len = min(max(p.offsets[s + 1], first), p.steps) - first;
+  }
+  const int64_t out = p.offsets ? first : s * p.steps;
+  const T* g0 = p.gate + s * p.g_seq + first * p.g_step + at;
+  const T* x0 = p.x + s * p.x_seq + first * p.x_step + at;
+  C h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = p.h0 ? p.h0[s * p.dim + at + v] : C(0);
+  for (int64_t t = 0; t < len; ++t) {
+    const auto g = *(const Pack<T, V>*)(g0 + t * p.g_step);
+    const auto x = *(const Pack<T, V>*)(x0 + t * p.x_step);
+    Pack<T, V> o;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      C a = (C)g.v[v], b = (C)x.v[v];
+      if constexpr (GATE == SLA_GATE_SIGMOID) {
+        C keep;
+        sigmoid2((C)g.v[v], a, keep);
+        b *= keep;
+      }
+      h[v] = a * h[v] + b;
+      o.v[v] = (T)h[v];
+    }
+    *(Pack<T, V>*)(p.h + (out + t) * p.dim + at) = o;
+  }
+  if (p.h_last) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.h_last[s * p.dim + at + v] = h[v];
   }
 }
 
@@ -579,10 +748,20 @@ sla_status refuse(const char* msg) {
   return SLA_ERR_INVALID_ARG;
 }
 
-// Rows of kept states (see span_of).
-int64_t saved_rows(const sla_linrec_shape& q) {
-  if (q.d_offsets) return q.steps / kChunk + q.n_seq;
-  return q.n_seq * ((q.steps + kChunk - 1) / kChunk);
+// Channels of a chunk.  Sequences side by side join their chunks side by side.
+int width_of(const sla_linrec_shape& q, bool backward) {
+  const int64_t side = (q.d_offsets ? 1 : q.n_seq) * q.dim;
+  return side < 8192 ? kNarrow : backward ? kManyBackward : kManyForward;
+}
+int chunk_of(const sla_linrec_shape& q, bool backward) {
+  return chunk_of(dtype_bytes(q.dtype), width_of(q, backward), backward);
+}
+
+// Rows of chunks (see first_row).
+int64_t rows_of(const sla_linrec_shape& q, bool backward) {
+  const int chunk = chunk_of(q, backward);
+  if (q.d_offsets) return q.steps / chunk + q.n_seq;
+  return q.n_seq * ((q.steps + chunk - 1) / chunk);
 }
 
 bool empty(const sla_linrec_shape& q) { return q.n_seq == 0 || q.dim == 0; }
@@ -595,10 +774,10 @@ sla_status check_shape(const sla_linrec_shape* q) {
     return refuse("unknown dtype");
   if (q->gate != SLA_GATE_LINEAR && q->gate != SLA_GATE_SIGMOID) return refuse("unknown gate");
   const int64_t seqs = q->d_offsets ? 1 : q->n_seq;
-  if (q->n_seq >= INT32_MAX || q->dim >= INT32_MAX || q->steps >= ((int64_t)1 << 40) ||
-      (__int128)(q->steps / kChunk + 1) * q->n_seq >= ((__int128)1 << 60) || (__int128)seqs * q->steps * q->dim >= ((__int128)1 << 60) ||
+  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 28) || q->steps >= ((int64_t)1 << 40) ||
+      (__int128)(q->steps / 64 + 1) * q->n_seq >= ((__int128)1 << 60) || (__int128)seqs * q->steps * q->dim >= ((__int128)1 << 60) ||
       (__int128)q->n_seq * q->dim >= ((__int128)1 << 60) ||
-      (__int128)(saved_rows(*q) + q->n_seq) * ((q->dim + 63) / 64) >= INT32_MAX) {
+      (__int128)(rows_of(*q, true) + 2 * q->n_seq + 64) * (q->dim / 64 + 64) >= INT32_MAX) {
     set_error("sizes beyond what one launch can index");
     return SLA_ERR_UNSUPPORTED;
   }
@@ -624,35 +803,44 @@ sla_status with_types(const sla_linrec_shape& q, F&& f) {
 }
 
 // Whether no sequence has more than one chunk, whatever the offsets.
-bool one_chunk(const sla_linrec_shape& q) { return q.steps <= kChunk; }
+bool one_chunk(const sla_linrec_shape& q, bool backward) {
+  return q.steps <= chunk_of(q, backward);
+}
 
-// The workspace of a call that joins chunks: the ticket, the rows'
-// sequences, the chunks' sums and (always, though the forward call has them
-// in d_saved when that is given) their ends.
+// One per 64 channels of each chunk.
+int64_t progress_words(const sla_linrec_shape& q, bool backward) {
+  const int width = width_of(q, backward);
+  return rows_of(q, backward) * ((q.dim + width - 1) / width) * (width / 64);
+}
+
+// The workspace of a call that joins chunks: the tickets, the progress, the
+// rows' sequences, the chunks' sums and ends; enough for either direction.
 struct Work {
-  size_t rows_at = 0, sums_at = 0, ends_at = 0, bytes = 0;
+  size_t progress_at = 0, rows_at = 0, sums_at = 0, ends_at = 0, bytes = 0;
 };
 Work work_of(const sla_linrec_shape& q) {
   Work w;
-  if (no_steps(q) || one_chunk(q)) return w;
-  const size_t words = (size_t)saved_rows(q) * q.dim * state_bytes(q);
-  w.rows_at = align_up(sizeof(int));
-  w.sums_at = w.rows_at + (q.d_offsets ? align_up((size_t)saved_rows(q) * sizeof(int)) : 0);
+  if (no_steps(q) || (one_chunk(q, false) && one_chunk(q, true))) return w;
+  const size_t rows = (size_t)std::max(rows_of(q, false), rows_of(q, true));
+  const size_t marks = (size_t)std::max(progress_words(q, false), progress_words(q, true));
+  const size_t words = rows * q.dim * state_bytes(q);
+  w.progress_at = kCounters * kTicketStep;
+  w.rows_at = w.progress_at + align_up(marks * sizeof(int));
+  w.sums_at = w.rows_at + (q.d_offsets ? align_up(rows * sizeof(int)) : 0);
   w.ends_at = w.sums_at + align_up(2 * words);
   w.bytes = w.ends_at + align_up(words);
   return w;
 }
 
-// Whether two neighbouring 16-bit channels can be moved as one word anywhere.
-bool even(int64_t v) { return (v & 1) == 0; }
-bool paired(const sla_linrec_shape& q, const void* p, int64_t seq, int64_t step) {
-  return ((uintptr_t)p & 3) == 0 && (even(seq) || q.d_offsets || q.n_seq == 1) &&
-         (even(step) || q.steps == 1);
+// Whether an array's rows allow access by `v` channels at a time, anywhere.
+bool packs(const sla_linrec_shape& q, const void* p, int64_t seq, int64_t step, int v) {
+  return (uintptr_t)p % (v * dtype_bytes(q.dtype)) == 0 &&
+         (seq % v == 0 || q.d_offsets || q.n_seq == 1) && (step % v == 0 || q.steps == 1);
 }
 
 template <typename T>
 Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_t xt,
-                    const void* g, int64_t gs, int64_t gt, const void* h0) {
+                    const void* g, int64_t gs, int64_t gt, const void* h0, bool backward) {
   using C = typename Compute<T>::type;
   Args<T> p{};
   p.x = (const T*)x;
@@ -666,53 +854,67 @@ Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_
   p.n_seq = q.n_seq;
   p.steps = q.steps;
   p.dim = q.dim;
-  p.chunks = (int)std::max<int64_t>(1, (q.steps + kChunk - 1) / kChunk);
-  p.rows = saved_rows(q);
+  const int chunk = chunk_of(q, backward);
+  p.chunks = (int)std::max<int64_t>(1, (q.steps + chunk - 1) / chunk);
+  p.rows = rows_of(q, backward);
   return p;
 }
 
-// Sets up the chunks' joining and calls launch(integral V, integral WAVES,
-// integral CHAIN, grid).
-template <typename T, typename F>
-sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool pairs, void* work, bool own_ends,
-                      hipStream_t s, F&& launch) {
+// Channels per thread, where every array's rows allow it: what 8 bytes hold
+// forward, 4 bytes backward.
+template <typename T>
+constexpr int most_v(bool backward) {
+  return std::max(1, (backward ? 4 : 8) / (int)sizeof(T));
+}
+
+// Sets up the chunks' joining and calls launch(W, V, CHAIN, grid), the first
+// three as types.
+template <int M, typename T, typename F>
+sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool packed_v, void* work,
+                      bool backward, hipStream_t s, F&& launch) {
   using C = typename Compute<T>::type;
-  const bool chain = !no_steps(q) && !one_chunk(q);
+  const bool chain = !no_steps(q) && !one_chunk(q, backward);
+  const int width = width_of(q, backward);
+  p.blocks = (int)((q.dim + width - 1) / width);
+  int64_t grid = q.n_seq * p.blocks;
   if (chain) {
+    p.chains = (int)(q.d_offsets ? p.blocks : q.n_seq * p.blocks);
+    p.links = (int)(q.d_offsets ? p.rows : p.chunks);
+    // the number of counters that leaves the fewest workgroups without work
+    p.counters = 1;
+    int64_t least = INT64_MAX;
+    for (int j = 1; j <= kCounters; ++j) {
+      const int64_t n = (int64_t)((p.chains + j - 1) / j) * j;
+      if (n <= least) least = n, p.counters = j;
+    }
+    grid = least * p.links;
     const Work w = work_of(q);
     char* base = (char*)work;
     p.ticket = (int*)base;
+    p.progress = (int*)(base + w.progress_at);
     int* row_seq = q.d_offsets ? (int*)(base + w.rows_at) : nullptr;
     p.row_seq = row_seq;
     p.sums = (C*)(base + w.sums_at);
-    if (own_ends) p.ends = (C*)(base + w.ends_at);
+    p.ends = (C*)(base + w.ends_at);
     const int64_t words = p.rows * p.dim;
     const int64_t want = (2 * words / 4 + kWG - 1) / kWG;
     rec_begin<C><<<dim3((unsigned)std::min<int64_t>(std::max<int64_t>(want, 1), 2048)), kWG, 0, s>>>(
-        (Word<C>*)p.sums, 2 * words, (Word<C>*)p.ends, words, p.ticket, row_seq, p.rows,
-        q.d_offsets, q.n_seq, q.steps);
+        (Word<C>*)p.sums, 2 * words, (Word<C>*)p.ends, words, p.ticket, p.progress,
+        progress_words(q, backward), row_seq, p.rows, q.d_offsets, q.n_seq, q.steps,
+        chunk_of(q, backward));
     SLA_HIP(hipGetLastError());
   }
-  const bool narrow = !chain && q.steps <= kSub;
-  auto with_v = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    const int64_t per = 64 * V * (narrow ? kWaves : 1);
-    p.blocks = (int)((q.dim + per - 1) / per);
-    const int64_t rows = !chain ? q.n_seq : q.d_offsets ? p.rows : q.n_seq * p.chunks;
-    const dim3 grid((unsigned)(rows * p.blocks));
-    using I1 = std::integral_constant<int, 1>;
-    using I4 = std::integral_constant<int, kWaves>;
-    if (chain) launch(v, I4{}, std::true_type{}, grid);
-    else if (narrow) launch(v, I1{}, std::false_type{}, grid);
-    else launch(v, I4{}, std::false_type{}, grid);
+  auto with_v = [&](auto w, auto v) {
+    if (chain) launch(w, v, std::true_type{}, dim3((unsigned)grid));
+    else launch(w, v, std::false_type{}, dim3((unsigned)grid));
   };
-  if constexpr (sizeof(T) == 2) {
-    if (pairs) with_v(std::integral_constant<int, 2>{});
-    else with_v(std::integral_constant<int, 1>{});
-  } else {
-    (void)pairs;
-    with_v(std::integral_constant<int, 1>{});
-  }
+  auto with_w = [&](auto w) {
+    if (packed_v) with_v(w, std::integral_constant<int, M>{});
+    else with_v(w, std::integral_constant<int, 1>{});
+  };
+  if (width == kNarrow) with_w(std::integral_constant<int, kNarrow>{});
+  else if (backward) with_w(std::integral_constant<int, kManyBackward>{});
+  else with_w(std::integral_constant<int, kManyForward>{});
   SLA_HIP(hipGetLastError());
   return SLA_OK;
 }
@@ -736,7 +938,7 @@ sla_status sla_linrec_sizes(const sla_linrec_shape* shape, size_t* saved_bytes,
   const sla_status st = check_shape(shape);
   if (st != SLA_OK) return st;
   if (!saved_bytes || !work_bytes) return refuse("NULL result");
-  *saved_bytes = no_steps(*shape) ? 0 : (size_t)saved_rows(*shape) * shape->dim * state_bytes(*shape);
+  *saved_bytes = no_steps(*shape) ? 0 : (size_t)rows_of(*shape, true) * shape->dim * state_bytes(*shape);
   *work_bytes = work_of(*shape).bytes;
   return SLA_OK;
 }
@@ -757,23 +959,32 @@ sla_status sla_linrec_forward(const sla_linrec_shape* shape, const void* d_x,
   const sla_linrec_shape& q = *shape;
   if ((st = check_work(q, d_work, work_bytes)) != SLA_OK) return st;
   TraceRange tr("sla_linrec_forward");
-  const bool pairs = even(q.dim) && paired(q, d_x, x_seq_stride, x_step_stride) &&
-                     paired(q, d_gate, gate_seq_stride, gate_step_stride) && paired(q, d_h, 0, 0);
   return with_types(q, [&](auto t, auto gate) {
     using T = decltype(t);
     using C = typename Compute<T>::type;
-    constexpr int GATE = decltype(gate)::value;
+    constexpr int GATE = decltype(gate)::value, M = most_v<T>(false);
+    const bool wide = q.dim % M == 0 && packs(q, d_x, x_seq_stride, x_step_stride, M) &&
+                      packs(q, d_gate, gate_seq_stride, gate_step_stride, M) &&
+                      packs(q, d_h, 0, 0, M);
+    const hipStream_t s = (hipStream_t)stream;
     Args<T> p = common_args<T>(q, d_x, x_seq_stride, x_step_stride, d_gate, gate_seq_stride,
-                               gate_step_stride, d_h0);
+                               gate_step_stride, d_h0, false);
     p.h = (T*)d_h;
     p.h_last = (C*)d_h_last;
-    p.ends = (C*)d_saved;
-    return run_chunks<T>(q, p, pairs, d_work, !d_saved, (hipStream_t)stream,
-                         [&](auto v, auto waves, auto chain, dim3 grid) {
-                           rec_forward<T, GATE, decltype(v)::value, decltype(waves)::value,
-                                       decltype(chain)::value>
-                               <<<grid, kWG, 0, (hipStream_t)stream>>>(p);
-                         });
+    p.saved = (C*)d_saved;
+    if (q.steps <= kFew) {
+      const int64_t n = q.n_seq * (q.dim / (wide ? M : 1));
+      const dim3 grid((unsigned)((n + kWG - 1) / kWG));
+      if (wide) few_forward<T, GATE, M><<<grid, kWG, 0, s>>>(p);
+      else few_forward<T, GATE, 1><<<grid, kWG, 0, s>>>(p);
+      SLA_HIP(hipGetLastError());
+      return SLA_OK;
+    }
+    return run_chunks<M>(q, p, wide, d_work, false, s, [&](auto w, auto v, auto chain, dim3 grid) {
+      if constexpr (decltype(w)::value == kNarrow || decltype(w)::value == kManyForward)
+      rec_forward<T, GATE, decltype(w)::value, decltype(v)::value, decltype(chain)::value>
+          <<<grid, forward_threads<T, decltype(w)::value, decltype(v)::value>(), 0, s>>>(p);
+    });
   });
 }
 
@@ -801,16 +1012,17 @@ sla_status sla_linrec_backward(const sla_linrec_shape* shape, const void* d_x,
   const sla_linrec_shape& q = *shape;
   if ((st = check_work(q, d_work, work_bytes)) != SLA_OK) return st;
   TraceRange tr("sla_linrec_backward");
-  const bool pairs = even(q.dim) && paired(q, d_x, x_seq_stride, x_step_stride) &&
-                     paired(q, d_gate, gate_seq_stride, gate_step_stride) &&
-                     paired(q, d_grad_h, grad_seq_stride, grad_step_stride) &&
-                     paired(q, d_grad_x, 0, 0) && paired(q, d_grad_gate, 0, 0);
   return with_types(q, [&](auto t, auto gate) {
     using T = decltype(t);
     using C = typename Compute<T>::type;
-    constexpr int GATE = decltype(gate)::value;
+    constexpr int GATE = decltype(gate)::value, M = most_v<T>(true);
+    const bool wide = q.dim % M == 0 && packs(q, d_x, x_seq_stride, x_step_stride, M) &&
+                      packs(q, d_gate, gate_seq_stride, gate_step_stride, M) &&
+                      packs(q, d_grad_h, grad_seq_stride, grad_step_stride, M) &&
+                      packs(q, d_grad_x, 0, 0, M) && packs(q, d_grad_gate, 0, 0, M);
+    const hipStream_t s = (hipStream_t)stream;
     Args<T> p = common_args<T>(q, d_x, x_seq_stride, x_step_stride, d_gate, gate_seq_stride,
-                               gate_step_stride, d_h0);
+                               gate_step_stride, d_h0, true);
     p.grad_h = (const T*)d_grad_h;
     p.d_seq = q.d_offsets ? 0 : grad_seq_stride;
     p.d_step = grad_step_stride;
@@ -819,12 +1031,11 @@ sla_status sla_linrec_backward(const sla_linrec_shape* shape, const void* d_x,
     p.grad_x = (T*)d_grad_x;
     p.grad_gate = (T*)d_grad_gate;
     p.grad_h0 = (C*)d_grad_h0;
-    return run_chunks<T>(q, p, pairs, d_work, true, (hipStream_t)stream,
-                         [&](auto v, auto waves, auto chain, dim3 grid) {
-                           rec_backward<T, GATE, decltype(v)::value, decltype(waves)::value,
-                                        decltype(chain)::value>
-                               <<<grid, kWG, 0, (hipStream_t)stream>>>(p);
-                         });
+    return run_chunks<M>(q, p, wide, d_work, true, s, [&](auto w, auto v, auto chain, dim3 grid) {
+      if constexpr (decltype(w)::value == kNarrow || decltype(w)::value == kManyBackward)
+      rec_backward<T, GATE, decltype(w)::value, decltype(v)::value, decltype(chain)::value>
+          <<<grid, kBackward, 0, s>>>(p);
+    });
   });
 }
 
