@@ -896,11 +896,12 @@ def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
     if len(grads) != len(opt.params):
         raise ValueError(f"{len(grads)} gradients for {len(opt.params)} parameters")
     dev, ptrs = opt.device, opt._ptrs
+    on = dev.index
     for i, (g, (n, dt)) in enumerate(zip(grads, opt._want)):
         if g is None:
             ptrs[i] = None
             continue
-        if g.dtype != dt or g.numel() != n or g.device != dev or not g.is_contiguous():
+        if g.dtype is not dt or g.numel() != n or g.get_device() != on or not g.is_contiguous():
             raise ValueError(f"gradient {i} must be a contiguous {dt} tensor of {n} elements "
                              f"on {dev}")
         ptrs[i] = g.data_ptr()

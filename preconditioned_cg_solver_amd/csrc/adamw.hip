@@ -12,8 +12,10 @@
 #include <cstring>
 #include <new>
 #include <string>
+#include <type_traits>
 #include <vector>
 
+#include "device_util.h"
 #include "elem.h"
 #include "internal.h"
 
@@ -22,10 +24,15 @@ namespace {
 
 constexpr int kBlock = 256;          // elements per block
 constexpr int kPerLane = kBlock / 64;
-constexpr int kChunkBlocks = 16;     // blocks per workgroup
+constexpr int kWaveBlocks = 2;       // blocks per wave
+constexpr int kChunkBlocks = kWaves * kWaveBlocks;  // per workgroup
 // Gradient addresses per launch: with the other arguments they stay within
 // the 4 KB that a launch can carry.
 constexpr int kGrads = 448;
+// Bytes of a step above which it goes past the caches (the last-level cache
+// has 256 MB): 120M fp32 elements 640 -> 588 us, 60M with 8-bit states 231 -> 218 us;
+// 9M with 8-bit states (90 MB) 42.2 us past them, 40.9 us through them.
+constexpr int64_t kCacheBytes = 256 << 20;
 constexpr int kTopM = 126, kTopV = 254;      // highest finite codes
 constexpr int kBadM = 127, kBadV = 255;      // not finite
 
@@ -71,16 +78,29 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
   x = (x ^ (x >> 15)) * 0xBB67AE85u;
   return x ^ (x >> 16);
 }
-// 32 random bits of element e (place in the padded order).
-__device__ __forceinline__ uint32_t noise(uint32_t key, uint64_t e) {
-  const uint32_t hi = (uint32_t)(e >> 32);
-  return mix((uint32_t)e * 0x9E3779B1u + (key ^ mix(hi) * (hi != 0)));
+// 32 random bits of elements e, e + 1, ... e + kPerLane - 1 (places in the
+// padded order; e is a multiple of kPerLane).
+__device__ __forceinline__ void noise(uint32_t key, uint64_t e, uint32_t (&r)[kPerLane]) {
+  const uint32_t hi = (uint32_t)(e >> 32), k = hi ? key ^ mix(hi) : key;
+#pragma unroll
+  for (uint32_t j = 0; j < kPerLane; ++j) r[j] = mix((uint32_t)e * 0x9E3779B1u + (j * 0x9E3779B1u + k));
 }
 
+// Largest over the 64 lanes, in every lane: within 16-lane rows by DPP moves,
+// across rows and halves by the lane swaps.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+  v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
+  v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
+  v = dpp_max<0x141>(v);  // row_half_mirror
+  v = dpp_max<0x140>(v);  // row_mirror
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max((uint32_t)r[0], (uint32_t)r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max((uint32_t)h[0], (uint32_t)h[1]);
 }
 
 // The 8-bit form (see sla.h): patterns of finite magnitudes are below this.
@@ -140,6 +160,15 @@ struct Types<K_F64> {
   using G = double;
 };
 
+// rate m / (root sqrt(v) + eps), by the hardware's root and reciprocal (each
+// within a unit in the last place; the full-precision sequences would make
+// the 8-bit step wait for its arithmetic).  They take no subnormal numbers:
+// v counts as 2^-126 at least.
+__device__ __forceinline__ float update(const Step& q, float m, float v) {
+  const float s = __builtin_amdgcn_sqrtf(fmaxf(v, 0x1p-126f));
+  return m * __builtin_amdgcn_rcpf(s * q.root + q.eps) * q.rate;
+}
+
 // A bf16 parameter's new value, rounded up with the probability of its
 // remainder (16 random bits).
 __device__ __forceinline__ bf16_t round_bf16(float x, uint32_t r16) {
@@ -158,87 +187,165 @@ __device__ __forceinline__ void moments(const Step& q, float g, float& m, float&
   v = v * q.b2 + (g * g) * q.b2c;
 }
 
+// A pointer from the table, known to be to global memory.
+template <typename T>
+__device__ __forceinline__ T* global(const void* p) {
+  return (T*)(__attribute__((address_space(1))) T*)(uintptr_t)p;
+}
+
+// Four elements of a lane, at any address that is a multiple of their size.
+// NT: past the caches, for a step that moves more than they hold.
+template <typename T>
+using Quad4 = unsigned __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T))));
+template <bool NT, typename T>
+__device__ __forceinline__ void load4(const T* from, T (&to)[kPerLane]) {
+  const Quad4<T> w = ld_stream<NT>((const Quad4<T>*)from);
+  __builtin_memcpy(to, &w, sizeof to);
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void store4(T* to, const T (&from)[kPerLane]) {
+  Quad4<T> w;
+  __builtin_memcpy(&w, from, sizeof w);
+  if constexpr (NT) __builtin_nontemporal_store(w, (Quad4<T>*)to);
+  else *(Quad4<T>*)to = w;
+}
+
+// A lane's part of a block: as read, and after the step.
 template <int KIND, int BITS>
-__global__ __launch_bounds__(kWG) void adamw_step(Step q, Grads grads) {
+struct Quad {
   using P = typename Types<KIND>::P;
   using G = typename Types<KIND>::G;
+  using S = std::conditional_t<BITS == 32, float, uint8_t>;
+  P p[kPerLane];
+  G g[kPerLane];
+  Pack<S, kPerLane> m, v;
+  uint32_t bm, bv;
+};
+
+// PART: the block ends with the tensor, after `left` elements of this lane.
+template <int KIND, int BITS, bool NT, bool PART>
+__device__ __forceinline__ void read_quad(const Step& q, const Tensor& t,
+                                          const typename Types<KIND>::G* gr, int64_t blk,
+                                          Quad<KIND, BITS>& d) {
+  using Q = Quad<KIND, BITS>;
+  const int64_t i = blk * kBlock + kPerLane * (threadIdx.x & 63);
+  const int64_t at = t.block0 * kBlock + i;  // in the states
+  const auto* p = global<const typename Q::P>(t.p);
+  if constexpr (PART) {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      d.p[j] = i + j < t.numel ? p[i + j] : (typename Q::P)0.0f;
+      d.g[j] = i + j < t.numel ? gr[i + j] : (typename Q::G)0.0f;
+    }
+  } else {
+    load4<NT>(p + i, d.p);
+    load4<NT>(gr + i, d.g);
+  }
+  if constexpr (BITS == 32) {
+    load4<NT>(q.st.m32 + at, d.m.v);
+    load4<NT>(q.st.v32 + at, d.v.v);
+  } else {
+    load4<NT>(q.st.m8 + at, d.m.v);
+    load4<NT>(q.st.v8 + at, d.v.v);
+    d.bm = q.st.mbase[t.block0 + blk];
+    d.bv = q.st.vbase[t.block0 + blk];
+  }
+}
+
+template <int KIND, int BITS, bool NT, bool PART>
+__device__ __forceinline__ void step_quad(const Step& q, const Tensor& t, float scale,
+                                          int64_t blk, Quad<KIND, BITS>& d) {
+  using Q = Quad<KIND, BITS>;
+  const int lane = threadIdx.x & 63;
+  const int64_t i = blk * kBlock + kPerLane * lane, at = t.block0 * kBlock + i;
+  float m[kPerLane], v[kPerLane];
+  uint32_t rnd[kPerLane] = {}, mb[kPerLane], vb[kPerLane];
+  bf16_t low[kPerLane];
+  if (BITS == 8 || KIND == K_BF16) noise(q.key, (uint64_t)at, rnd);
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) {
+    const bool in = !PART || i + j < t.numel;
+    if constexpr (BITS == 32) m[j] = d.m.v[j], v[j] = d.v.v[j];
+    else m[j] = decode_m(d.m.v[j], d.bm), v[j] = decode_v(d.v.v[j], d.bv);
+    float g;
+    if constexpr (KIND == K_F64) g = (float)(q.scale ? d.g[j] * (double)scale : d.g[j]);
+    else g = q.scale ? (float)d.g[j] * scale : (float)d.g[j];
+    moments(q, g, m[j], v[j]);
+    if (!in) m[j] = v[j] = 0.0f;
+    const float up = update(q, m[j], v[j]);
+    if constexpr (KIND == K_F64) {
+      d.p[j] = d.p[j] * q.decay64 - (double)up;
+    } else if constexpr (KIND == K_BF16) {
+      d.p[j] = round_bf16((float)d.p[j] * q.decay - up, mix(rnd[j] + 0x6A09E667u) & 0xffff);
+    } else {
+      d.p[j] = d.p[j] * q.decay - up;
+      low[j] = (bf16_t)d.p[j];
+    }
+    mb[j] = magnitude(m[j]);
+    vb[j] = magnitude(v[j]);
+  }
+  auto* p = global<typename Q::P>(t.p);
+  bf16_t* copy = t.copy ? global<bf16_t>(t.copy) : nullptr;
+  if constexpr (PART) {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      if (i + j < t.numel) {
+        p[i + j] = d.p[j];
+        if ((KIND == K_F32 || KIND == K_F32_BF16) && copy) copy[i + j] = low[j];
+      }
+    }
+  } else {
+    store4<NT>(p + i, d.p);
+    if ((KIND == K_F32 || KIND == K_F32_BF16) && copy) store4<false>(copy + i, low);
+  }
+  if constexpr (BITS == 32) {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) d.m.v[j] = m[j], d.v.v[j] = v[j];
+    store4<NT>(q.st.m32 + at, d.m.v);
+    store4<NT>(q.st.v32 + at, d.v.v);
+  } else {
+    const uint32_t bm = base_of(mb, kTopM, 0xfffff), bv = base_of(vb, kTopV, 0xfffff);
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const uint32_t cm = encode_m(mb[j], ((rnd[j] & 0xffff) << 4) + 8, bm);
+      d.m.v[j] = (uint8_t)(cm | (m[j] < 0.0f ? 128u : 0u));
+      d.v.v[j] = (uint8_t)encode_v(vb[j], ((rnd[j] >> 16) << 4) + 8, bv);
+    }
+    store4<NT>(q.st.m8 + at, d.m.v);
+    store4<NT>(q.st.v8 + at, d.v.v);
+    if (lane == 0) {
+      q.st.mbase[t.block0 + blk] = (uint16_t)bm;
+      q.st.vbase[t.block0 + blk] = (uint16_t)bv;
+    }
+  }
+}
+
+template <int KIND, int BITS, bool NT>
+__global__ __launch_bounds__(kWG) void adamw_step(Step q, Grads grads) {
   const float scale = q.scale ? *q.scale : 1.0f;
   if (!(fabsf(scale) < INFINITY)) return;
   const Chunk ch = q.chunks[blockIdx.x];
-  const G* gr = (const G*)grads.g[ch.tensor - q.tensor0];
-  if (!gr) return;
-  const Tensor t = q.tensors[ch.tensor];
-  P* p = (P*)t.p;
-  bf16_t* copy = (bf16_t*)t.copy;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int b = wave; b < kChunkBlocks; b += kWaves) {
-    const int64_t blk = (int64_t)ch.first * kChunkBlocks + b;
-    const int64_t e0 = blk * kBlock;
-    if (e0 >= t.numel) break;
-    const int64_t at = (t.block0 + blk) * kBlock + kPerLane * lane;  // in the states
-    float m[kPerLane], v[kPerLane];
-    if constexpr (BITS == 32) {
-      const auto pm = *(const Pack<float, 4>*)(q.st.m32 + at);
-      const auto pv = *(const Pack<float, 4>*)(q.st.v32 + at);
+  const int tensor = __builtin_amdgcn_readfirstlane(ch.tensor);
+  const void* grad = grads.g[tensor - q.tensor0];
+  if (!grad) return;
+  const auto* gr = global<const typename Types<KIND>::G>(grad);
+  const Tensor t = q.tensors[tensor];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t b0 = (int64_t)__builtin_amdgcn_readfirstlane(ch.first) * kChunkBlocks +
+                     wave * kWaveBlocks;
+  if ((b0 + kWaveBlocks) * kBlock <= t.numel) {
+    // all of a wave's blocks are read before the first is stepped
+    Quad<KIND, BITS> d[kWaveBlocks];
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) m[j] = pm.v[j], v[j] = pv.v[j];
-    } else {
-      const auto pm = *(const Pack<uint8_t, 4>*)(q.st.m8 + at);
-      const auto pv = *(const Pack<uint8_t, 4>*)(q.st.v8 + at);
-      const uint32_t bm = q.st.mbase[t.block0 + blk], bv = q.st.vbase[t.block0 + blk];
+    for (int b = 0; b < kWaveBlocks; ++b) read_quad<KIND, BITS, NT, false>(q, t, gr, b0 + b, d[b]);
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) m[j] = decode_m(pm.v[j], bm), v[j] = decode_v(pv.v[j], bv);
-    }
-    uint32_t rnd[kPerLane] = {};
-    uint32_t mb[kPerLane], vb[kPerLane];
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int64_t i = e0 + kPerLane * lane + j;
-      const bool in = i < t.numel;
-      if (BITS == 8 || KIND == K_BF16) rnd[j] = noise(q.key, (uint64_t)(at + j));
-      float g = 0.0f;
-      if (in) {
-        if constexpr (KIND == K_F64) g = (float)(q.scale ? gr[i] * (double)scale : gr[i]);
-        else g = q.scale ? (float)gr[i] * scale : (float)gr[i];
-      }
-      moments(q, g, m[j], v[j]);
-      if (!in) m[j] = v[j] = 0.0f;
-      if (in) {
-        const float up = m[j] / (sqrtf(v[j]) * q.root + q.eps) * q.rate;
-        if constexpr (KIND == K_F64) {
-          p[i] = p[i] * q.decay64 - (double)up;
-        } else if constexpr (KIND == K_BF16) {
-          p[i] = round_bf16((float)p[i] * q.decay - up, mix(rnd[j] + 0x6A09E667u) & 0xffff);
-        } else {
-          const float np = p[i] * q.decay - up;
-          p[i] = np;
-          if (copy) copy[i] = (bf16_t)np;
-        }
-      }
-      mb[j] = magnitude(m[j]);
-      vb[j] = magnitude(v[j]);
-    }
-    if constexpr (BITS == 32) {
-      Pack<float, 4> pm, pv;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) pm.v[j] = m[j], pv.v[j] = v[j];
-      *(Pack<float, 4>*)(q.st.m32 + at) = pm;
-      *(Pack<float, 4>*)(q.st.v32 + at) = pv;
-    } else {
-      const uint32_t bm = base_of(mb, kTopM, 0xfffff), bv = base_of(vb, kTopV, 0xfffff);
-      Pack<uint8_t, 4> pm, pv;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) {
-        const uint32_t cm = encode_m(mb[j], ((rnd[j] & 0xffff) << 4) + 8, bm);
-        pm.v[j] = (uint8_t)(cm | (m[j] < 0.0f ? 128u : 0u));
-        pv.v[j] = (uint8_t)encode_v(vb[j], ((rnd[j] >> 16) << 4) + 8, bv);
-      }
-      *(Pack<uint8_t, 4>*)(q.st.m8 + at) = pm;
-      *(Pack<uint8_t, 4>*)(q.st.v8 + at) = pv;
-      if (lane == 0) {
-        q.st.mbase[t.block0 + blk] = (uint16_t)bm;
-        q.st.vbase[t.block0 + blk] = (uint16_t)bv;
-      }
+    for (int b = 0; b < kWaveBlocks; ++b) step_quad<KIND, BITS, NT, false>(q, t, scale, b0 + b, d[b]);
+  } else {
+    for (int b = 0; b < kWaveBlocks; ++b) {
+      if ((b0 + b) * kBlock >= t.numel) break;
+      Quad<KIND, BITS> d;
+      read_quad<KIND, BITS, NT, true>(q, t, gr, b0 + b, d);
+      step_quad<KIND, BITS, NT, true>(q, t, scale, b0 + b, d);
     }
   }
 }
@@ -363,6 +470,7 @@ struct Launch {
 struct sla_adamw {
   int32_t n = 0, bits = 32;
   int64_t blocks = 0;
+  bool streams = false;                    // a step moves more than the caches hold
   const sla::Tensor* d_tensors = nullptr;  // sorted by kind
   const sla::Chunk* d_chunks = nullptr;
   sla::State st = {};
@@ -382,12 +490,15 @@ sla_status build(sla_adamw* o, const sla_adamw_tensor* ts, void* d_state, void* 
   Tensor* ht = (Tensor*)table.data();
   Chunk* hc = (Chunk*)(table.data() + tbytes);
   std::vector<int64_t> block0((size_t)o->n);
-  int64_t blocks = 0;
+  int64_t blocks = 0, bytes = 0;
   for (int32_t i = 0; i < o->n; ++i) {
     block0[i] = blocks;
     blocks += (ts[i].numel + kBlock - 1) / kBlock;
+    bytes += ts[i].numel * (int64_t)(2 * dtype_bytes(ts[i].dtype) + dtype_bytes(ts[i].grad_dtype) +
+                                     (o->bits == 32 ? 16 : 4));
   }
   o->blocks = blocks;
+  o->streams = bytes > kCacheBytes;
   int64_t nc = 0;
   for (int kind = 0; kind < K_KINDS; ++kind) {
     o->kind0[kind] = (int32_t)o->order.size();
@@ -423,14 +534,14 @@ sla_status build(sla_adamw* o, const sla_adamw_tensor* ts, void* d_state, void* 
   return SLA_OK;
 }
 
-template <int BITS>
+template <int BITS, bool NT>
 void launch(const Launch& l, const Step& q, const Grads& g, hipStream_t s) {
   const dim3 grid((unsigned)l.chunks);
   switch (l.kind) {
-    case K_F32: adamw_step<K_F32, BITS><<<grid, kWG, 0, s>>>(q, g); break;
-    case K_F32_BF16: adamw_step<K_F32_BF16, BITS><<<grid, kWG, 0, s>>>(q, g); break;
-    case K_BF16: adamw_step<K_BF16, BITS><<<grid, kWG, 0, s>>>(q, g); break;
-    default: adamw_step<K_F64, BITS><<<grid, kWG, 0, s>>>(q, g); break;
+    case K_F32: adamw_step<K_F32, BITS, NT><<<grid, kWG, 0, s>>>(q, g); break;
+    case K_F32_BF16: adamw_step<K_F32_BF16, BITS, NT><<<grid, kWG, 0, s>>>(q, g); break;
+    case K_BF16: adamw_step<K_BF16, BITS, NT><<<grid, kWG, 0, s>>>(q, g); break;
+    default: adamw_step<K_F64, BITS, NT><<<grid, kWG, 0, s>>>(q, g); break;
   }
 }
 
@@ -528,8 +639,9 @@ sla_status sla_adamw_step(sla_adamw_t opt, const void* const* h_grads,
     q.tensors = opt->d_tensors + opt->kind0[l.kind];
     q.chunks = opt->d_chunks + l.chunk0;
     q.tensor0 = l.tensor0;
-    if (opt->bits == 32) launch<32>(l, q, g, (hipStream_t)stream);
-    else launch<8>(l, q, g, (hipStream_t)stream);
+    const hipStream_t s = (hipStream_t)stream;
+    if (opt->bits == 32) opt->streams ? launch<32, true>(l, q, g, s) : launch<32, false>(l, q, g, s);
+    else opt->streams ? launch<8, true>(l, q, g, s) : launch<8, false>(l, q, g, s);
     SLA_HIP(hipGetLastError());
   }
   return SLA_OK;
