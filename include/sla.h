@@ -487,7 +487,8 @@ sla_status sla_linrec_backward(const sla_linrec_shape *shape, const void *d_x,
  *   m' = beta1 m + (1 - beta1) g,    v' = beta2 v + (1 - beta2) g^2
  *   p' = p (1 - lr weight_decay)
  *        - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
- * in fp32 (the update of an SLA_F64 parameter is added in fp64).
+ * in fp32 (gradients of SLA_F64 parameters are rounded to it, the update is
+ * added in fp64); under the root v' counts as 2^-126 at least.
  *
  * The states m and v are the caller's, in one buffer.  Every tensor starts a
  * new block of 256 elements; with `padded` = 256 * (sum of ceil(numel / 256))
