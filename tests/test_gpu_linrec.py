@@ -81,6 +81,48 @@ def test_dense(dt, mode, n, steps, d):
 
 
 @pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f64", "f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,steps,d", [(8, 300, 1040), (3, 333, 2731), (1, 130, 8200),
+                                       (5, 129, 1700), (1, 20_000, 20), (2, 9000, 35)])
+def test_chunk_shapes(dt, mode, n, steps, d):
+    """Many channels (wide, short chunks), channel counts that end within a
+    block or cannot be read by pairs, and chains of many more chunks than one
+    look takes in."""
+    say("recurrence chunk shapes", dt, mode, n, steps, d)
+    x, g, h0, dh, dl = make(dt, mode, (n, steps), d, n, 14)
+    got = run(dt, mode, x, g, h0, None, dh, dl)
+    check(got, reference(dt, mode, x, g, h0, None, dh, dl), (dt, mode, n, steps, d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [8192, 8195, 33])
+def test_packed_chunk_shapes(dt, d):
+    lens = [200, 0, 1, 129, 128, 64, 300, 255, 257]
+    offsets = np.concatenate([[0], np.cumsum(lens)])
+    say("recurrence packed chunk shapes", dt, d)
+    x, g, h0, dh, dl = make(dt, "sigmoid", (int(offsets[-1]),), d, len(lens), 15, h0=d != 33)
+    got = run(dt, "sigmoid", x, g, h0, offsets, dh, dl)
+    check(got, reference(dt, "sigmoid", x, g, h0, offsets, dh, dl), (dt, d))
+
+
+def test_past_the_caches():
+    """More than 256 MB of rows: the same bits as a part of the channels alone,
+    which goes through the caches."""
+    say("recurrence streams")
+    n, steps, d = 2, 1500, 16_384
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x, gate, dh = (torch.randn(n, steps, d, device=DEV, generator=gen) for _ in range(3))
+    h, last, saved = B.sla_linrec_forward(x, gate, save=True)
+    dx, dg, _ = B.sla_linrec_backward(x, gate, saved, dh)
+    part = slice(4096, 8192 + 64)  # as many channels: the same chunks
+    xs, gs, ds = (t[..., part].contiguous() for t in (x, gate, dh))
+    hp, lp, sp = B.sla_linrec_forward(xs, gs, save=True)
+    dxp, dgp, _ = B.sla_linrec_backward(xs, gs, sp, ds)
+    for a, b in ((h, hp), (last, lp), (dx, dxp), (dg, dgp)):
+        assert torch.equal(a[..., part], b)
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
 @pytest.mark.parametrize("dt", ["f64", "f32", "bf16"])
 @pytest.mark.parametrize("lens,d", [([5], 3), ([1, 1, 1, 1], 65), ([0, 0, 3, 0], 8),
                                     ([64, 64], 16), ([63, 1, 65, 0, 127, 2], 72),
