@@ -21,9 +21,20 @@
   which shows the library's phases (handle creation, the ordering, the
   solves, the pattern gradient) around their kernels.
 
-Usage: ``python -m preconditioned_cg_solver_amd.studies jacobi|quality|trace
-[--configs 0,1,2,3] [--rows N]``.  jacobi and quality print one JSON line per
-configuration.
+* ``learn``: coefficients of a model learnt through the solver (the inverse
+  problem of "torch-sla", applications: an optimiser's loop through the
+  solve).  Sources on the nodes of a 64 x 64 grid relax towards a driving
+  signal, h_t = a h_{t-1} + (1 - a) s u_t with a rate a = sigmoid(g) and a
+  strength s per node; some of the fields that they cause over a short time
+  by diffusion, A x_t = h_t with A = I + dt L / h^2, are observed.  g and s are learnt from the observations: the recurrence along time
+  (autograd.linear_recurrence), the solves of all observed times at once,
+  their adjoint, the recurrence's adjoint and an AdamW step over both
+  parameters, with states of ``--bits`` bits.
+
+Usage: ``python -m preconditioned_cg_solver_amd.studies
+jacobi|quality|trace|learn [--configs 0,1,2,3] [--rows N] [--iters N]
+[--bits 8|32]``.  jacobi and quality print one JSON line per configuration,
+learn one for the run.
 """
 from __future__ import annotations
 
@@ -34,6 +45,7 @@ import time
 import numpy as np
 import torch
 
+from . import autograd as AG
 from . import binding as B
 from . import inputs as I
 
@@ -138,17 +150,88 @@ def trace_run(rows: int):
           flush=True)
 
 
+class _SolveColumns(torch.autograd.Function):
+    """X = A^-1 B for the columns of B, with the adjoint solves as its gradient."""
+
+    @staticmethod
+    def forward(ctx, rhs, A, G, eps, rtol, maxit):
+        ctx.args = (A, G, eps, rtol, maxit)
+        return B.sla_pcg_solve_multi(A, G, eps, rhs.contiguous(), rtol=rtol, maxit=maxit)[0]
+
+    @staticmethod
+    def backward(ctx, grad):
+        A, G, eps, rtol, maxit = ctx.args
+        # A does not depend on the parameters: of its adjoint only dL/dB is used
+        x = torch.zeros_like(grad)
+        out = B.sla_pcg_adjoint_multi(A, G, eps, x, grad.contiguous(), rtol=rtol, maxit=maxit)
+        return out[0], None, None, None, None, None
+
+
+def learn(iters: int = 300, bits: int = 32, steps: int = 256, snapshots: int = 16, lr: float = 0.05,
+          seed: int = 0):
+    """Learn relaxation rates and source strengths from observed fields."""
+    rng = np.random.default_rng([21, seed])
+    M = I.heat2d(64, dt=1e-4)
+    A, G = _handle(M), _handle(I.spai_factor(M, rng), transpose=True)
+    n = M.n
+    drive = _dev(np.cumsum(rng.standard_normal(steps)) / 4.0)
+    seen = _dev(np.linspace(steps // 8, steps - 1, snapshots).astype(np.int64))
+    true_g = _dev(3.0 + 0.5 * rng.standard_normal(n))
+    true_s = _dev(1.0 + 0.3 * rng.standard_normal(n))
+
+    def fields(g, s):
+        x = drive[None, :, None] * s
+        h, _ = AG.linear_recurrence(x, g.expand(1, steps, n))
+        return _SolveColumns.apply(h[0, seen].t(), A, G, 3e-3, 1e-10, 500)
+
+    with torch.no_grad():
+        observed = fields(true_g, true_s)
+    scale = float(observed.square().mean())
+    g = torch.full_like(true_g, 3.0, requires_grad=True)
+    s = torch.ones_like(true_s, requires_grad=True)
+    opt = B.sla_adamw_create([g, s], state_bits=bits)
+    losses, t0 = [], None
+    for t in range(1, iters + 1):
+        if t == 2:
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+        loss = (fields(g, s) - observed).square().mean() / scale
+        grads = torch.autograd.grad(loss, [g, s])
+        B.sla_adamw_step(opt, grads, step=t, lr=lr * (1 - (t - 1) / iters), weight_decay=0.0,
+                         seed=seed)
+        losses.append(loss.detach())
+    torch.cuda.synchronize()
+    each = (time.perf_counter() - t0) / max(iters - 1, 1) if t0 else None
+    losses = torch.stack(losses).cpu().numpy()
+
+    def off(a, b, start):
+        return float((a - b).norm() / (b - start).norm())
+
+    out = {"grid": "64x64", "n": n, "steps": steps, "snapshots": snapshots, "bits": bits,
+           "iterations": iters, "loss_first": float(losses[0]), "loss_last": float(losses[-1]),
+           "rate_error": off(g.detach(), true_g, 3.0), "strength_error": off(s.detach(), true_s, 1.0),
+           "ms_per_iteration": None if each is None else round(each * 1e3, 3)}
+    for h in (A, G):
+        h.destroy()
+    opt.destroy()
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("study", choices=["jacobi", "quality", "trace"])
+    ap.add_argument("study", choices=["jacobi", "quality", "trace", "learn"])
     ap.add_argument("--configs", default="0,1,2,3")
     ap.add_argument("--rows", type=int, default=20000)
+    ap.add_argument("--iters", type=int, default=300)
+    ap.add_argument("--bits", type=int, default=32, choices=[8, 32])
     args = ap.parse_args()
     configs = [int(c) for c in args.configs.split(",")]
     if args.study == "jacobi":
         jacobi(configs)
     elif args.study == "quality":
         quality(configs)
+    elif args.study == "learn":
+        print(json.dumps(learn(args.iters, args.bits)), flush=True)
     else:
         trace_run(args.rows)
 
