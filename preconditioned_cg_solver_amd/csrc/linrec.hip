@@ -79,6 +79,8 @@ struct Args {
   T* h;
   C* h_last;
   C* saved;      // the state after each chunk of the backward pass
+  int save_log;  // log2 of those chunks' steps
+  int64_t saves;     // dense: of each sequence
   T* grad_x;
   T* grad_gate;
   C* grad_h0;
@@ -194,16 +196,18 @@ enum Progress { kNothing = 0, kSums = 1, kEnd = 2 };
 // each chunk's own end is computed, so the bits do not depend on how far the
 // look went.  progress, ends and sums point at the nearest chunk's.
 
-// The nearest K, in one trip to memory.
-template <int K, int STEP, typename C>
+// The nearest two, in one trip to memory (the backward pass with four: 8 x 4096 x
+// 1024 bf16 104 -> 124 us, for what is read in vain; forward 45.8 -> 47.6 us).
+constexpr int kNear = 2;
+template <int STEP, typename C>
 __device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_t bytes,
                                            int64_t dim, int have, C& carry) {
-  C e[K], a[K], m[K];
+  C e[kNear], a[kNear], m[kNear];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
+  for (int j = 0; j < kNear; ++j) {
     const int64_t off = STEP * min(j, have - 1) * dim;
     e[j] = look(ends + off, bytes);
-    if (j + 1 < K) {
+    if (j + 1 < kNear) {
       a[j] = look(sums + 2 * off, bytes);
       m[j] = look(sums + 2 * off + dim, bytes);
     }
@@ -211,16 +215,16 @@ __device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_
   int at = -1;
   bool open = true;  // the sums so far are all known
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
+  for (int j = 0; j < kNear; ++j) {
     if (open && at < 0 && j < have && __all(written(e[j]))) at = j;
-    if (j + 1 < K) open = open && __all(written(a[j]) && written(m[j]));
+    if (j + 1 < kNear) open = open && __all(written(a[j]) && written(m[j]));
   }
   if (at < 0) return false;
   carry = e[0];
 #pragma unroll
-  for (int j = K - 1; j >= 0; --j) {
+  for (int j = kNear - 1; j >= 0; --j) {
     if (j == at) carry = e[j];
-    if (j + 1 < K && j < at) carry = a[j] * carry + m[j];
+    if (j + 1 < kNear && j < at) carry = a[j] * carry + m[j];
   }
   return true;
 }
@@ -229,12 +233,12 @@ __device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_
 // waits only for chunks whose tickets were drawn before its own, by
 // workgroups that therefore run already: the wait ends.
 constexpr int kReach = 32, kBatch = 8;
-template <int NEAR, int STEP, typename C>
+template <int STEP, typename C>
 __device__ __forceinline__ C wait_carry(const int* progress, const C* ends, const C* sums,
                                         uint32_t bytes, int64_t dim, int64_t have) {
   const int n = (int)min(have, (int64_t)kReach), lane = threadIdx.x & 63;
   C near = C(0);
-  if (near_carry<NEAR, STEP>(ends, sums, bytes, dim, n, near)) return near;
+  if (near_carry<STEP>(ends, sums, bytes, dim, n, near)) return near;
   for (;; __builtin_amdgcn_s_sleep(1)) {
     int f = kNothing;
     if (lane < n)
@@ -272,9 +276,12 @@ __device__ __forceinline__ void tell(int* progress, Progress v) {
     __hip_atomic_store(progress, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Tickets are drawn from kCounters counters at most, kTicketStep bytes apart:
-// one for all would serve its atomics one after the other.
-constexpr int kCounters = 64, kTicketStep = 64;
+// Tickets are drawn from two counters, kTicketStep bytes apart.  One serves
+// its atomics one after the other (forward, 4 x 4096 x 1024 bf16: 38.1 us
+// against 35.8), but keeps all chains at the same step, whose row is one piece of
+// memory; with many they drift apart (65536 x 512 fp32, counters 1, 2, 8, 64:
+// 89.8, 89.6, 109, 109 us; backward, 131072 x 2048 bf16: 551, 576, 647, 649 us).
+constexpr int kCounters = 2, kTicketStep = 64;
 
 // Marks every word as not written, zeroes the ticket and finds each row's
 // sequence: the last one that begins at or before it.
@@ -333,6 +340,21 @@ __device__ __forceinline__ bool my_chunk(const Args<T>& p, Where& w, int& block)
     w.mark = (int64_t)chain * (W / 64) * p.links + c;
     return true;
   }
+}
+
+// A row past its packed sequence's end: none of valid offsets waits for it,
+// and the end it publishes keeps those of any others from waiting for ever.
+template <int W, int kChunk, typename T>
+__device__ __forceinline__ bool unused_row(const Args<T>& p, const Where& w, int block) {
+  using C = typename Compute<T>::type;
+  if (!p.offsets || w.c == 0 || w.c * kChunk < w.len) return false;
+  const int64_t ch0 = (int64_t)block * W;
+  if (threadIdx.x < W) {
+    if (ch0 + threadIdx.x < p.dim)
+      publish(p.ends + w.row * p.dim + ch0, threadIdx.x * (uint32_t)sizeof(C), C(0));
+    tell(p.progress + w.mark + (int64_t)(threadIdx.x >> 6) * p.links, kEnd);
+  }
+  return true;
 }
 
 // A thread's part of a chunk: V channels of S steps.
@@ -447,13 +469,14 @@ template <typename T, int GATE, int W, int V, bool CHAIN>
 __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(Args<T> p) {
   using C = typename Compute<T>::type;
   using P = Part<T, W, V, forward_threads<T, W, V>(), false>;
-  constexpr int SAVE = chunk_steps<T, W == kNarrow ? kNarrow : kManyBackward, true>();
   constexpr bool kSig = GATE == SLA_GATE_SIGMOID;
   constexpr int S = P::S, kSubs = P::kSubs;
   __shared__ C s_a[kSubs][W], s_m[kSubs][W];
   int block;
   Where w;
   if (!my_chunk<W, CHAIN, false>(p, w, block)) return;
+  if (CHAIN && unused_row<W, P::kChunk>(p, w, block)) return;
+  static_assert(chunk_steps<T, kManyBackward, true>() % S == 0, "saved states fall between parts");
   const P r = my_part<P>(p, w, block);
 
   // The rows as loaded or, where they fit, the coefficients they give; else
@@ -517,7 +540,7 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
     if (w.c == 0) {
       if (p.h0) h = *lane_ptr(p.h0 + w.s * p.dim + ch0, at);
     } else if constexpr (CHAIN) {
-      h = wait_carry<4, -1>(mark - 1, ends - p.dim, sums - 2 * p.dim, at, p.dim, w.c);
+      h = wait_carry<-1>(mark - 1, ends - p.dim, sums - 2 * p.dim, at, p.dim, w.c);
     }
     if constexpr (CHAIN) {
       if (act) publish(ends, at, ca * h + cm);
@@ -532,10 +555,10 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
       s_m[q][threadIdx.x] = h;
       h = next;
       // the state where a chunk of the backward pass ends and another follows
-      const int64_t t = w.c * P::kChunk + (q + 1) * S;
-      if (p.saved && (q + 1) * S % SAVE == 0 && t < w.len && act) {
-        const int64_t first = p.offsets ? w.first / SAVE + w.s : w.s * ((p.steps + SAVE - 1) / SAVE);
-        *lane_ptr(p.saved + (first + t / SAVE - 1) * p.dim + ch0, at) = h;
+      const int64_t t = w.c * P::kChunk + (q + 1) * S, k = t >> p.save_log;
+      if (p.saved && k << p.save_log == t && t < w.len && act) {
+        const int64_t row = p.offsets ? (w.first >> p.save_log) + w.s : w.s * p.saves;
+        *lane_ptr(p.saved + (row + k - 1) * p.dim + ch0, at) = h;
       }
     }
   }
@@ -580,6 +603,7 @@ __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backwar
   int block;
   Where w;
   if (!my_chunk<W, CHAIN, true>(p, w, block)) return;
+  if (CHAIN && unused_row<W, P::kChunk>(p, w, block)) return;
   const P r = my_part<P>(p, w, block);
 
   // f: the coefficient, for the sigmoid folded with the weight of x: held
@@ -666,7 +690,7 @@ __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backwar
     if (w.after == 0) {
       if (p.grad_last) mu = *lane_ptr(p.grad_last + state0, at);
     } else if constexpr (CHAIN) {
-      mu = wait_carry<2, 1>(mark + 1, ends + p.dim, sums + 2 * p.dim, at, p.dim, w.after);
+      mu = wait_carry<1>(mark + 1, ends + p.dim, sums + 2 * p.dim, at, p.dim, w.after);
     }
     if constexpr (CHAIN) {
       if (act) publish(ends, at, ca * mu + cu);
@@ -727,7 +751,7 @@ __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backwar
 
 // Sequences of a few steps, a serving step above all: a thread takes V
 // channels from the first step to the last.
-constexpr int kFew = 8;
+constexpr int kFew = 32;
 template <typename T, int GATE, int V>
 __global__ __launch_bounds__(kWG) void few_forward(Args<T> p) {
   using C = typename Compute<T>::type;
@@ -777,10 +801,17 @@ sla_status refuse(const char* msg) {
   return SLA_ERR_INVALID_ARG;
 }
 
-// Channels of a chunk.  Sequences side by side join their chunks side by side.
+// Channels of a chunk.  Narrow chunks have more steps, so fewer of them are
+// joined one after the other; wide ones are filled by shorter sequences.
 int width_of(const sla_linrec_shape& q, bool backward) {
+  const int wide = backward ? kManyBackward : kManyForward;
+  const size_t size = dtype_bytes(q.dtype);
+  // under a quarter of the lanes without a channel
+  if ((q.dim + wide - 1) / wide * wide * 3 > q.dim * 4) return kNarrow;
+  const int64_t length = q.d_offsets ? q.steps / std::max<int64_t>(q.n_seq, 1) : q.steps;
+  if (length < 2 * chunk_of(size, kNarrow, backward)) return wide;
   const int64_t side = (q.d_offsets ? 1 : q.n_seq) * q.dim;
-  return side < 8192 ? kNarrow : backward ? kManyBackward : kManyForward;
+  return side >= 8192 && !(backward && size == 2) ? wide : kNarrow;
 }
 int chunk_of(const sla_linrec_shape& q, bool backward) {
   return chunk_of(dtype_bytes(q.dtype), width_of(q, backward), backward);
@@ -804,9 +835,11 @@ sla_status check_shape(const sla_linrec_shape* q) {
   if (q->gate != SLA_GATE_LINEAR && q->gate != SLA_GATE_SIGMOID) return refuse("unknown gate");
   const int64_t seqs = q->d_offsets ? 1 : q->n_seq;
   if (q->n_seq >= INT32_MAX || q->dim >= (1 << 28) || q->steps >= ((int64_t)1 << 40) ||
-      (__int128)(q->steps / 64 + 1) * q->n_seq >= ((__int128)1 << 60) || (__int128)seqs * q->steps * q->dim >= ((__int128)1 << 60) ||
+      (__int128)(q->steps / 32 + 1) * q->n_seq >= ((__int128)1 << 60) ||
+      (__int128)seqs * q->steps * q->dim >= ((__int128)1 << 60) ||
       (__int128)q->n_seq * q->dim >= ((__int128)1 << 60) ||
-      (__int128)(rows_of(*q, true) + 2 * q->n_seq + 64) * (q->dim / 64 + 64) >= INT32_MAX) {
+      (__int128)(std::max(rows_of(*q, false), rows_of(*q, true)) + 2 * q->n_seq + 64) *
+              (q->dim / 64 + 64) >= INT32_MAX) {
     set_error("sizes beyond what one launch can index");
     return SLA_ERR_UNSUPPORTED;
   }
@@ -886,11 +919,14 @@ Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_
   const int chunk = chunk_of(q, backward);
   p.chunks = (int)std::max<int64_t>(1, (q.steps + chunk - 1) / chunk);
   p.rows = rows_of(q, backward);
+  const int save = chunk_of(q, true);  // a power of two
+  p.save_log = __builtin_ctz(save);
+  p.saves = (q.steps + save - 1) / save;
   // Beyond what the last-level cache holds (256 MB) the rows go past it: forward
   // 4 x 4096 x 4096 bf16 94.6 -> 87.7 us, 262144 x 1024 fp16 384 -> 368 us; up to
   // there the next reader may find them in it.
-  p.streams = (backward ? 5 : 3) * (q.d_offsets ? 1 : q.n_seq) * q.steps * q.dim *
-                  (int64_t)sizeof(T) > ((int64_t)256 << 20);
+  const double elements = (double)(q.d_offsets ? 1 : q.n_seq) * q.steps * q.dim;
+  p.streams = (backward ? 5 : 3) * elements * sizeof(T) > 256 << 20;
   return p;
 }
 
@@ -914,14 +950,8 @@ sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool packed_v, void
   if (chain) {
     p.chains = (int)(q.d_offsets ? p.blocks : q.n_seq * p.blocks);
     p.links = (int)(q.d_offsets ? p.rows : p.chunks);
-    // the number of counters that leaves the fewest workgroups without work
-    p.counters = 1;
-    int64_t least = INT64_MAX;
-    for (int j = 1; j <= kCounters; ++j) {
-      const int64_t n = (int64_t)((p.chains + j - 1) / j) * j;
-      if (n <= least) least = n, p.counters = j;
-    }
-    grid = least * p.links;
+    p.counters = p.chains % kCounters ? 1 : kCounters;
+    grid = (int64_t)p.chains * p.links;
     const Work w = work_of(q);
     char* base = (char*)work;
     p.ticket = (int*)base;
