@@ -107,35 +107,57 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 constexpr uint32_t kInf = 0x7f800000u;
 constexpr uint32_t kMost = (kInf >> 20) - 1;  // the largest finite level
 
+// FINITE: no code of the wave's stands for a value that is not (the step's
+// arithmetic bounds its 8-bit form, and these tests are a fifth of it).
+template <bool FINITE>
 __device__ __forceinline__ float decode(uint32_t code, uint32_t base, uint32_t bad, float worst) {
-  const float v = __uint_as_float((code + base) << 20);
-  return code == 0 ? 0.0f : code == bad ? worst : v;
+  const float v = code == 0 ? 0.0f : __uint_as_float((code + base) << 20);
+  return !FINITE && code == bad ? worst : v;
 }
+template <bool FINITE>
 __device__ __forceinline__ float decode_v(uint32_t c, uint32_t base) {
-  return decode(c, base, kBadV, INFINITY);
+  return decode<FINITE>(c, base, kBadV, INFINITY);
 }
+template <bool FINITE>
 __device__ __forceinline__ float decode_m(uint32_t c, uint32_t base) {
-  return copysignf(decode(c & 127, base, kBadM, NAN), (c & 128) ? -1.0f : 1.0f);
+  const uint32_t sign = (c & 128) << 24;
+  return __uint_as_float(__float_as_uint(decode<FINITE>(c & 127, base, kBadM, NAN)) | sign);
+}
+// Whether one of the four codes in m or v is kBadM or kBadV: a zero byte in
+// the complement, which subtracting one from each byte shows in its top bit.
+__device__ __forceinline__ bool bad_codes(uint32_t m, uint32_t v) {
+  const uint32_t a = (~m & 0x7f7f7f7fu) - 0x01010101u, b = (~v - 0x01010101u) & v;
+  return ((a | b) & 0x80808080u) != 0;
 }
 
-// Largest finite pattern of a wave's block, and the base under which every
-// value rounded up by less than `up` has a code of at most `top`.
-__device__ __forceinline__ uint32_t base_of(const uint32_t (&bits)[kPerLane], int top,
-                                            uint32_t up) {
+// Largest pattern of a wave's block; FINITE: of those that are.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&bits)[kPerLane]) {
   uint32_t mx = 0;
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) mx = max(mx, bits[j] < kInf ? bits[j] : 0);
-  mx = wave_max(mx);
+  for (int j = 0; j < kPerLane; ++j) mx = max(mx, !FINITE || bits[j] < kInf ? bits[j] : 0);
+  return __builtin_amdgcn_readfirstlane(wave_max(mx));
+}
+// The base under which every value up to `mx`, rounded up by less than `up`,
+// has a code of at most `top`.
+__device__ __forceinline__ uint32_t base_of(uint32_t mx, int top, uint32_t up) {
   const uint32_t k = min((mx + up) >> 20, kMost);
   return k > (uint32_t)top ? k - (uint32_t)top : 0;
 }
-__device__ __forceinline__ uint32_t encode_v(uint32_t bits, uint32_t add, uint32_t base) {
+// add < 2^20, so that a zero's code is 0.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t encode(uint32_t bits, uint32_t add, uint32_t base, int least,
+                                           int top, int bad) {
   const int c = (int)((bits + add) >> 20) - (int)base;
-  return bits == 0 ? 0 : bits >= kInf ? kBadV : (uint32_t)min(max(c, 1), kTopV);
+  return !FINITE && bits >= kInf ? bad : (uint32_t)min(max(c, least), top);
 }
+template <bool FINITE>
+__device__ __forceinline__ uint32_t encode_v(uint32_t bits, uint32_t add, uint32_t base) {
+  return encode<FINITE>(bits, add, base, (int)min(bits, 1u), kTopV, kBadV);
+}
+template <bool FINITE>
 __device__ __forceinline__ uint32_t encode_m(uint32_t bits, uint32_t add, uint32_t base) {
-  const int c = (int)((bits + add) >> 20) - (int)base;
-  return bits == 0 ? 0 : bits >= kInf ? kBadM : (uint32_t)min(max(c, 0), kTopM);
+  return encode<FINITE>(bits, add, base, 0, kTopM, kBadM);
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
@@ -170,11 +192,10 @@ __device__ __forceinline__ float update(const Step& q, float m, float v) {
 }
 
 // A bf16 parameter's new value, rounded up with the probability of its
-// remainder (16 random bits).
+// remainder (16 random bits).  A NaN that arithmetic gave is quiet and stays
+// one without its low bits.
 __device__ __forceinline__ bf16_t round_bf16(float x, uint32_t r16) {
-  uint32_t u = __float_as_uint(x);
-  if ((u & kInf) != kInf) u += r16;
-  else if (u & 0x7fffff) u |= 0x400000;  // a NaN stays one without its low bits
+  const uint32_t u = __float_as_uint(x) + (__builtin_isfinite(x) ? r16 : 0);
   return __builtin_bit_cast(bf16_t, (uint16_t)(u >> 16));
 }
 
@@ -262,14 +283,25 @@ __device__ __forceinline__ void step_quad(const Step& q, const Tensor& t, float 
   uint32_t rnd[kPerLane] = {}, mb[kPerLane], vb[kPerLane];
   bf16_t low[kPerLane];
   if (BITS == 8 || KIND == K_BF16) noise(q.key, (uint64_t)at, rnd);
+  if constexpr (BITS == 32) {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) m[j] = d.m.v[j], v[j] = d.v.v[j];
+  } else {
+    auto decode4 = [&](auto finite) {
+      constexpr bool kFinite = decltype(finite)::value;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j)
+        m[j] = decode_m<kFinite>(d.m.v[j], d.bm), v[j] = decode_v<kFinite>(d.v.v[j], d.bv);
+    };
+    if (__any(bad_codes(__builtin_bit_cast(uint32_t, d.m), __builtin_bit_cast(uint32_t, d.v))))
+      decode4(std::false_type{});
+    else decode4(std::true_type{});
+  }
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) {
     const bool in = !PART || i + j < t.numel;
-    if constexpr (BITS == 32) m[j] = d.m.v[j], v[j] = d.v.v[j];
-    else m[j] = decode_m(d.m.v[j], d.bm), v[j] = decode_v(d.v.v[j], d.bv);
-    float g;
-    if constexpr (KIND == K_F64) g = (float)(q.scale ? d.g[j] * (double)scale : d.g[j]);
-    else g = q.scale ? (float)d.g[j] * scale : (float)d.g[j];
+    using W = std::conditional_t<KIND == K_F64, double, float>;
+    const float g = (float)((W)d.g[j] * (W)scale);
     moments(q, g, m[j], v[j]);
     if (!in) m[j] = v[j] = 0.0f;
     const float up = update(q, m[j], v[j]);
@@ -304,12 +336,26 @@ __device__ __forceinline__ void step_quad(const Step& q, const Tensor& t, float 
     store4<NT>(q.st.m32 + at, d.m.v);
     store4<NT>(q.st.v32 + at, d.v.v);
   } else {
-    const uint32_t bm = base_of(mb, kTopM, 0xfffff), bv = base_of(vb, kTopV, 0xfffff);
+    uint32_t bm = top_of<false>(mb), bv = top_of<false>(vb);
+    auto encode4 = [&](auto finite) {
+      constexpr bool kFinite = decltype(finite)::value;
+      bm = base_of(bm, kTopM, 0xfffff);
+      bv = base_of(bv, kTopV, 0xfffff);
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const uint32_t cm = encode_m(mb[j], ((rnd[j] & 0xffff) << 4) + 8, bm);
-      d.m.v[j] = (uint8_t)(cm | (m[j] < 0.0f ? 128u : 0u));
-      d.v.v[j] = (uint8_t)encode_v(vb[j], ((rnd[j] >> 16) << 4) + 8, bv);
+      for (int j = 0; j < kPerLane; ++j) {
+        const uint32_t cm = encode_m<kFinite>(mb[j], ((rnd[j] & 0xffff) << 4) + 8, bm);
+        d.m.v[j] = (uint8_t)(cm | (m[j] < 0.0f ? 128u : 0u));
+        d.v.v[j] = (uint8_t)encode_v<kFinite>(vb[j], ((rnd[j] >> 16) << 4) + 8, bv);
+      }
+    };
+    if (max(bm, bv) < kInf) {
+      encode4(std::true_type{});
+    } else {
+      // (keeps the compiler from doing this for every block beforehand)
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) asm volatile("" : "+v"(mb[j]), "+v"(vb[j]));
+      bm = top_of<true>(mb), bv = top_of<true>(vb);
+      encode4(std::false_type{});
     }
     store4<NT>(q.st.m8 + at, d.m.v);
     store4<NT>(q.st.v8 + at, d.v.v);
@@ -362,8 +408,8 @@ __global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blocks, bf1
   Pack<bf16_t, 4> om, ov;
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) {
-    om.v[j] = (bf16_t)decode_m(cm.v[j], bm);
-    ov.v[j] = (bf16_t)decode_v(cv.v[j], bv);
+    om.v[j] = (bf16_t)decode_m<false>(cm.v[j], bm);
+    ov.v[j] = (bf16_t)decode_v<false>(cv.v[j], bv);
   }
   *(Pack<bf16_t, 4>*)(m + at) = om;
   *(Pack<bf16_t, 4>*)(v + at) = ov;
@@ -381,12 +427,13 @@ __global__ __launch_bounds__(kWG) void adamw_write8(State st, int64_t blocks, co
   uint32_t mb[kPerLane], vb[kPerLane];
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) mb[j] = magnitude(pm.v[j]), vb[j] = magnitude(pv.v[j]);
-  const uint32_t bm = base_of(mb, kTopM, 0x80000), bv = base_of(vb, kTopV, 0x80000);
+  const uint32_t bm = base_of(top_of<true>(mb), kTopM, 0x80000);
+  const uint32_t bv = base_of(top_of<true>(vb), kTopV, 0x80000);
   Pack<uint8_t, 4> cm, cv;
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) {
-    cm.v[j] = (uint8_t)(encode_m(mb[j], 0x80000, bm) | (pm.v[j] < 0.0f ? 128u : 0u));
-    cv.v[j] = (uint8_t)encode_v(vb[j], 0x80000, bv);
+    cm.v[j] = (uint8_t)(encode_m<false>(mb[j], 0x80000, bm) | (pm.v[j] < 0.0f ? 128u : 0u));
+    cv.v[j] = (uint8_t)encode_v<false>(vb[j], 0x80000, bv);
   }
   *(Pack<uint8_t, 4>*)(st.m8 + at) = cm;
   *(Pack<uint8_t, 4>*)(st.v8 + at) = cv;
