@@ -4,7 +4,15 @@
 // elements per lane); in 8 bits a block is also what shares a base.  A
 // device table, written when the handle is created, lists the tensors and
 // the blocks; only the gradients' addresses, which change from step to step,
-// travel with the launch as kernel arguments.
+// travel with the launch as kernel arguments.  Nothing is reduced over more than
+// a block and there are no atomics: a step's bits do not depend on its order.
+//
+// What bounds it: an element's 28 bytes with fp32 states (120M of them 536 to
+// 582 us between cards, 5.8 to 6.3 TB/s) and its 14 bytes with 8-bit ones and a
+// bf16 gradient (60M: 133 us, 6.3 TB/s), where an elementwise sum of large
+// arrays reaches 6.2; with bf16 parameters and 8-bit states (10 bytes) the
+// rounding's arithmetic, some 80 instructions an element (9M: 26 us, 3.5 TB/s);
+// below a million elements the launch (60000 in 24 tensors: 3.4 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -24,14 +32,14 @@ namespace {
 
 constexpr int kBlock = 256;          // elements per block
 constexpr int kPerLane = kBlock / 64;
-constexpr int kWaveBlocks = 2;       // blocks per wave
-constexpr int kChunkBlocks = kWaves * kWaveBlocks;  // per workgroup
+constexpr int kChunkBlocks = kWaves;  // blocks per workgroup
 // Gradient addresses per launch: with the other arguments they stay within
 // the 4 KB that a launch can carry.
 constexpr int kGrads = 448;
 // Bytes of a step above which it goes past the caches (the last-level cache
-// has 256 MB): 120M fp32 elements 640 -> 588 us, 60M with 8-bit states 231 -> 218 us;
-// 9M with 8-bit states (90 MB) 42.2 us past them, 40.9 us through them.
+// has 256 MB).  Through and past them, with the reading back of 8-bit states:
+// 120M fp32 elements 572 and 544 us, 60M with 8-bit states 214 and 202 us,
+// 9M bf16 with 8-bit states (90 MB) 35.3 and 36.2 us.
 constexpr int64_t kCacheBytes = 256 << 20;
 constexpr int kTopM = 126, kTopV = 254;      // highest finite codes
 constexpr int kBadM = 127, kBadV = 255;      // not finite
@@ -83,7 +91,8 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
 __device__ __forceinline__ void noise(uint32_t key, uint64_t e, uint32_t (&r)[kPerLane]) {
   const uint32_t hi = (uint32_t)(e >> 32), k = hi ? key ^ mix(hi) : key;
 #pragma unroll
-  for (uint32_t j = 0; j < kPerLane; ++j) r[j] = mix((uint32_t)e * 0x9E3779B1u + (j * 0x9E3779B1u + k));
+  for (uint32_t j = 0; j < kPerLane; ++j)
+    r[j] = mix((uint32_t)e * 0x9E3779B1u + (j * 0x9E3779B1u + k));
 }
 
 // Largest over the 64 lanes, in every lane: within 16-lane rows by DPP moves,
@@ -366,6 +375,9 @@ __device__ __forceinline__ void step_quad(const Step& q, const Tensor& t, float 
   }
 }
 
+// One step of every parameter of a launch, a block per wave.  (Two or four
+// blocks, all read before the first is stepped: 120M fp32 elements 572 us with one,
+// 581 with two, 580 with four; 9M bf16 with 8-bit states 33.7, 35.4 and 37.6 us.)
 template <int KIND, int BITS, bool NT>
 __global__ __launch_bounds__(kWG) void adamw_step(Step q, Grads grads) {
   const float scale = q.scale ? *q.scale : 1.0f;
@@ -377,26 +389,19 @@ __global__ __launch_bounds__(kWG) void adamw_step(Step q, Grads grads) {
   const auto* gr = global<const typename Types<KIND>::G>(grad);
   const Tensor t = q.tensors[tensor];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t b0 = (int64_t)__builtin_amdgcn_readfirstlane(ch.first) * kChunkBlocks +
-                     wave * kWaveBlocks;
-  if ((b0 + kWaveBlocks) * kBlock <= t.numel) {
-    // all of a wave's blocks are read before the first is stepped
-    Quad<KIND, BITS> d[kWaveBlocks];
-#pragma unroll
-    for (int b = 0; b < kWaveBlocks; ++b) read_quad<KIND, BITS, NT, false>(q, t, gr, b0 + b, d[b]);
-#pragma unroll
-    for (int b = 0; b < kWaveBlocks; ++b) step_quad<KIND, BITS, NT, false>(q, t, scale, b0 + b, d[b]);
-  } else {
-    for (int b = 0; b < kWaveBlocks; ++b) {
-      if ((b0 + b) * kBlock >= t.numel) break;
-      Quad<KIND, BITS> d;
-      read_quad<KIND, BITS, NT, true>(q, t, gr, b0 + b, d);
-      step_quad<KIND, BITS, NT, true>(q, t, scale, b0 + b, d);
-    }
+  const int64_t blk = (int64_t)__builtin_amdgcn_readfirstlane(ch.first) * kChunkBlocks + wave;
+  Quad<KIND, BITS> d;
+  if ((blk + 1) * kBlock <= t.numel) {
+    read_quad<KIND, BITS, NT, false>(q, t, gr, blk, d);
+    step_quad<KIND, BITS, NT, false>(q, t, scale, blk, d);
+  } else if (blk * kBlock < t.numel) {
+    read_quad<KIND, BITS, NT, true>(q, t, gr, blk, d);
+    step_quad<KIND, BITS, NT, true>(q, t, scale, blk, d);
   }
 }
 
 // The values of 8-bit states: four significant bits, which bf16 holds.
+// Bound by its 6 bytes an element: 60M in 63 us, 5.7 TB/s.
 __global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blocks, bf16_t* m,
                                                    bf16_t* v) {
   const int64_t blk = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
@@ -415,7 +420,8 @@ __global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blocks, bf1
   *(Pack<bf16_t, 4>*)(v + at) = ov;
 }
 
-// States from values, to the nearest level.
+// States from values, to the nearest level (10 bytes an element: 60M in
+// 115 us on a first call).
 __global__ __launch_bounds__(kWG) void adamw_write8(State st, int64_t blocks, const float* m,
                                                     const float* v) {
   const int64_t blk = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
@@ -687,8 +693,9 @@ sla_status sla_adamw_step(sla_adamw_t opt, const void* const* h_grads,
     q.chunks = opt->d_chunks + l.chunk0;
     q.tensor0 = l.tensor0;
     const hipStream_t s = (hipStream_t)stream;
-    if (opt->bits == 32) opt->streams ? launch<32, true>(l, q, g, s) : launch<32, false>(l, q, g, s);
-    else opt->streams ? launch<8, true>(l, q, g, s) : launch<8, false>(l, q, g, s);
+    const auto f = opt->bits == 32 ? opt->streams ? launch<32, true> : launch<32, false>
+                                   : opt->streams ? launch<8, true> : launch<8, false>;
+    f(l, q, g, s);
     SLA_HIP(hipGetLastError());
   }
   return SLA_OK;

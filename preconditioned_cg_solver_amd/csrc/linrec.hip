@@ -3,6 +3,14 @@
 // Forward substitution of a unit lower bidiagonal system per sequence and
 // channel, h_t = a_t h_{t-1} + b_t, and back substitution of its transpose
 // for the gradients, lambda_t = dh_t + a_{t+1} lambda_{t+1}.
+//
+// A step is the map h -> a h + b, and maps compose: two in a row are
+// h -> (a2 a1) h + (a2 b1 + b2).  A workgroup reads a chunk of steps, composes
+// them and publishes the result, takes what enters the chunk from the one
+// before it and only then writes its rows, from registers: every row is read
+// and written once, in one launch.  What enters is folded one chunk at a time
+// from the same side whichever way it was found, so the bits do not depend
+// on timing.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -22,8 +30,7 @@ namespace {
 // backward pass holds more per element and spreads a chunk over twice the
 // threads; a chunk of the forward pass is one or more of the backward's.
 constexpr int kForward = 512, kBackward = 1024;
-// Many channels: wide rows, which memory serves faster.  Few: long chunks,
-// for then the time goes into joining one to the next.
+// The channels of wide chunks and of narrow ones (see width_of).
 constexpr int kManyForward = 128, kManyBackward = 256, kNarrow = 64;
 // Whether the forward pass keeps the coefficients between its two passes over
 // a chunk, or the rows as they were loaded, which take half the registers
@@ -283,8 +290,9 @@ __device__ __forceinline__ void tell(int* progress, Progress v) {
 // 89.8, 89.6, 109, 109 us; backward, 131072 x 2048 bf16: 551, 576, 647, 649 us).
 constexpr int kCounters = 2, kTicketStep = 64;
 
-// Marks every word as not written, zeroes the ticket and finds each row's
-// sequence: the last one that begins at or before it.
+// Marks every word as not written, zeroes the tickets and finds each row's
+// sequence: the last one that begins at or before it.  2 to 6 us of a call; a
+// launch of its own, since a chunk may look at any word.
 template <typename C>
 __global__ __launch_bounds__(kWG) void rec_begin(Word<C>* sums, int64_t n_sums, Word<C>* ends,
                                                  int64_t n_ends, int* ticket, int* progress,
@@ -465,6 +473,16 @@ __device__ __forceinline__ void row_fence(int i) {
 
 // One chunk of a sequence.  CHAIN: sequences may have several, joined by the
 // look-back; otherwise each has one.
+//
+// Bound by the bytes of x, gate and h, at the rate at which rows are reached in
+// pieces of 128 or 256 bytes, and by the latency of the joining: 4 x 4096 x 4096
+// bf16 85 us (4.7 TB/s; the chunks without the joining 78 us), 8 x 2048 x 2048
+// bf16 47 us (37 us), 65536 x 512 fp32 82 us (4.9 TB/s), 262144 x 1024 fp16 349
+// us (4.6 TB/s).  A quarter-rate exponential and reciprocal an element leave
+// no room to work the coefficients out twice where registers hold them.
+// Workgroups that stay and fetch the next chunk's rows while they join one
+// took 148 us for the first of these: two fit a compute unit, and neither
+// hides the other's wait.
 template <typename T, int GATE, int W, int V, bool CHAIN>
 __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(Args<T> p) {
   using C = typename Compute<T>::type;
@@ -484,7 +502,8 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
   constexpr bool kKeep = keeps(sizeof(T), W);
   Pack<T, V> x[S], g[S];
   C ka[kKeep ? S : 1][V], kb[kKeep ? S : 1][V];
-  load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams, idle_gate<GATE, T>(), g);
+  load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams,
+                  idle_gate<GATE, T>(), g);
   load_part<S, V>(p.x + w.x + r.at, p.x_step, r.t0, r.nv, r.full, p.streams, (T)0.0f, x);
   auto coefficients = [&](int i, int v, C& a, C& b) {
     b = (C)x[i].v[v];
@@ -592,6 +611,15 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
   }
 }
 
+// One chunk of the adjoint, from the saved state before it.  The composed maps
+// of the forward pass are needed again, for h, beside those of mu; both are
+// taken in the one pass over the rows.
+//
+// Bound as the forward pass, by the bytes of x, gate, dh and the two gradients,
+// and by registers: two workgroups a compute unit leave a thread 64 of them for
+// its 16 elements (16 bits; some are spilt): 8 x 2048 x 2048 bf16 84 us (4.0
+// TB/s; without the joining 75 us), 65536 x 512 fp32 136 us (4.9 TB/s), 120 packed
+// sequences of 833 x 1024 bf16 270 us (3.8 TB/s).
 template <typename T, int GATE, int W, int V, bool CHAIN>
 __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backward(Args<T> p) {
   using C = typename Compute<T>::type;
@@ -624,7 +652,8 @@ __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backwar
 #pragma unroll
     for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0), pu[v] = C(0);
     Pack<T, V> g[S], d[S];
-    load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams, idle_gate<GATE, T>(), g);
+    load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams,
+                    idle_gate<GATE, T>(), g);
     load_part<S, V>(p.x + w.x + r.at, p.x_step, r.t0, r.nv, r.full, p.streams, (T)0.0f, x);
     load_part<S, V>(p.grad_h + w.d + r.at, p.d_step, r.t0, p.grad_h ? r.nv : 0,
                     r.full && p.grad_h, p.streams, (T)0.0f, d);
@@ -750,7 +779,9 @@ __global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backwar
 }
 
 // Sequences of a few steps, a serving step above all: a thread takes V
-// channels from the first step to the last.
+// channels from the first step to the last.  Bound by the launch for a step (16 x
+// 4096 bf16: 3.0 us, the chunks' kernel 7.0), by latency or bytes beyond: 256 x 32 x
+// 4096 bf16 34 us a call, in chunks 91; up to 32 steps it was never the slower.
 constexpr int kFew = 32;
 template <typename T, int GATE, int V>
 __global__ __launch_bounds__(kWG) void few_forward(Args<T> p) {
@@ -802,7 +833,12 @@ sla_status refuse(const char* msg) {
 }
 
 // Channels of a chunk.  Narrow chunks have more steps, so fewer of them are
-// joined one after the other; wide ones are filled by shorter sequences.
+// joined one after the other; wide ones are filled by shorter sequences and
+// reach longer pieces of a row.  Narrow and wide, us: packed 12 of 8333 x 1024
+// bf16, forward 154, 172, backward 249, 337; 120 of 833, forward 195, 185,
+// backward 271, 289; 800 of 125, 394, 350 and 430, 307; dense 8 x 4096 x 1024,
+// bf16 forward 60, 50, backward 93, 100, fp32 backward 141, 132; 1000 x 300 x
+// 64, half of a wide chunk's lanes without a channel, forward 36, 54.
 int width_of(const sla_linrec_shape& q, bool backward) {
   const int wide = backward ? kManyBackward : kManyForward;
   const size_t size = dtype_bytes(q.dtype);
@@ -922,16 +958,19 @@ Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_
   const int save = chunk_of(q, true);  // a power of two
   p.save_log = __builtin_ctz(save);
   p.saves = (q.steps + save - 1) / save;
-  // Beyond what the last-level cache holds (256 MB) the rows go past it: forward
-  // 4 x 4096 x 4096 bf16 94.6 -> 87.7 us, 262144 x 1024 fp16 384 -> 368 us; up to
-  // there the next reader may find them in it.
+  // 16-bit rows beyond what the last-level cache holds (256 MB) go past it:
+  // forward, 4 x 4096 x 4096 bf16 90.9 -> 87.9 us, 262144 x 1024 fp16 352 -> 345 us.
+  // In 32 bits it does not pay: 65536 x 512, both directions, 224 us through it and
+  // 226 us past it.
   const double elements = (double)(q.d_offsets ? 1 : q.n_seq) * q.steps * q.dim;
-  p.streams = (backward ? 5 : 3) * elements * sizeof(T) > 256 << 20;
+  p.streams = sizeof(T) == 2 && (backward ? 5 : 3) * elements * sizeof(T) > 256 << 20;
   return p;
 }
 
 // Channels per thread, where every array's rows allow it: what 8 bytes hold
-// forward, 4 bytes backward.
+// forward (4 x 4096 x 4096 bf16 88.5 us, with 4 bytes 91.8; both directions of 8 x
+// 2048 x 2048 143.2 and 141.8), 4 bytes backward (those 143, with 8 bytes 175:
+// twice as many parts to join, half as many steps in each).
 template <typename T>
 constexpr int most_v(bool backward) {
   return std::max(1, (backward ? 4 : 8) / (int)sizeof(T));
@@ -962,10 +1001,11 @@ sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool packed_v, void
     p.ends = (C*)(base + w.ends_at);
     const int64_t words = p.rows * p.dim;
     const int64_t want = (2 * words / 4 + kWG - 1) / kWG;
-    rec_begin<C><<<dim3((unsigned)std::min<int64_t>(std::max<int64_t>(want, 1), 2048)), kWG, 0, s>>>(
-        (Word<C>*)p.sums, 2 * words, (Word<C>*)p.ends, words, p.ticket, p.progress,
-        progress_words(q, backward), row_seq, p.rows, q.d_offsets, q.n_seq, q.steps,
-        chunk_of(q, backward));
+    const dim3 begin((unsigned)std::min<int64_t>(std::max<int64_t>(want, 1), 2048));
+    rec_begin<C><<<begin, kWG, 0, s>>>((Word<C>*)p.sums, 2 * words, (Word<C>*)p.ends, words,
+                                       p.ticket, p.progress, progress_words(q, backward),
+                                       row_seq, p.rows, q.d_offsets, q.n_seq, q.steps,
+                                       chunk_of(q, backward));
     SLA_HIP(hipGetLastError());
   }
   auto with_v = [&](auto w, auto v) {
@@ -1002,7 +1042,8 @@ sla_status sla_linrec_sizes(const sla_linrec_shape* shape, size_t* saved_bytes,
   const sla_status st = check_shape(shape);
   if (st != SLA_OK) return st;
   if (!saved_bytes || !work_bytes) return refuse("NULL result");
-  *saved_bytes = no_steps(*shape) ? 0 : (size_t)rows_of(*shape, true) * shape->dim * state_bytes(*shape);
+  *saved_bytes =
+      no_steps(*shape) ? 0 : (size_t)rows_of(*shape, true) * shape->dim * state_bytes(*shape);
   *work_bytes = work_of(*shape).bytes;
   return SLA_OK;
 }
@@ -1045,9 +1086,10 @@ sla_status sla_linrec_forward(const sla_linrec_shape* shape, const void* d_x,
       return SLA_OK;
     }
     return run_chunks<M>(q, p, wide, d_work, false, s, [&](auto w, auto v, auto chain, dim3 grid) {
-      if constexpr (decltype(w)::value == kNarrow || decltype(w)::value == kManyForward)
-      rec_forward<T, GATE, decltype(w)::value, decltype(v)::value, decltype(chain)::value>
-          <<<grid, forward_threads<T, decltype(w)::value, decltype(v)::value>(), 0, s>>>(p);
+      constexpr int W = decltype(w)::value, V = decltype(v)::value;
+      if constexpr (W == kNarrow || W == kManyForward)
+        rec_forward<T, GATE, W, V, decltype(chain)::value>
+            <<<grid, (forward_threads<T, W, V>()), 0, s>>>(p);
     });
   });
 }
@@ -1096,9 +1138,9 @@ sla_status sla_linrec_backward(const sla_linrec_shape* shape, const void* d_x,
     p.grad_gate = (T*)d_grad_gate;
     p.grad_h0 = (C*)d_grad_h0;
     return run_chunks<M>(q, p, wide, d_work, true, s, [&](auto w, auto v, auto chain, dim3 grid) {
-      if constexpr (decltype(w)::value == kNarrow || decltype(w)::value == kManyBackward)
-      rec_backward<T, GATE, decltype(w)::value, decltype(v)::value, decltype(chain)::value>
-          <<<grid, kBackward, 0, s>>>(p);
+      constexpr int W = decltype(w)::value, V = decltype(v)::value;
+      if constexpr (W == kNarrow || W == kManyBackward)
+        rec_backward<T, GATE, W, V, decltype(chain)::value><<<grid, kBackward, 0, s>>>(p);
     });
   });
 }

@@ -26,7 +26,8 @@
   solve).  Sources on the nodes of a 64 x 64 grid relax towards a driving
   signal, h_t = a h_{t-1} + (1 - a) s u_t with a rate a = sigmoid(g) and a
   strength s per node; some of the fields that they cause over a short time
-  by diffusion, A x_t = h_t with A = I + dt L / h^2, are observed.  g and s are learnt from the observations: the recurrence along time
+  by diffusion, A x_t = h_t with A = I + dt L / h^2, are observed.  g and s
+  are learnt from the observations: the recurrence along time
   (autograd.linear_recurrence), the solves of all observed times at once,
   their adjoint, the recurrence's adjoint and an AdamW step over both
   parameters, with states of ``--bits`` bits.
@@ -209,7 +210,8 @@ def learn(iters: int = 300, bits: int = 32, steps: int = 256, snapshots: int = 1
 
     out = {"grid": "64x64", "n": n, "steps": steps, "snapshots": snapshots, "bits": bits,
            "iterations": iters, "loss_first": float(losses[0]), "loss_last": float(losses[-1]),
-           "rate_error": off(g.detach(), true_g, 3.0), "strength_error": off(s.detach(), true_s, 1.0),
+           "rate_error": off(g.detach(), true_g, 3.0),
+           "strength_error": off(s.detach(), true_s, 1.0),
            "ms_per_iteration": None if each is None else round(each * 1e3, 3)}
     for h in (A, G):
         h.destroy()

@@ -105,13 +105,15 @@ def test_packed_chunk_shapes(dt, d):
     check(got, reference(dt, "sigmoid", x, g, h0, offsets, dh, dl), (dt, d))
 
 
-def test_past_the_caches():
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_past_the_caches(dtype):
     """More than 256 MB of rows: the same bits as a part of the channels alone,
     which goes through the caches."""
-    say("recurrence streams")
+    say("recurrence streams", dtype)
     n, steps, d = 2, 1500, 16_384
     gen = torch.Generator(device=DEV).manual_seed(5)
-    x, gate, dh = (torch.randn(n, steps, d, device=DEV, generator=gen) for _ in range(3))
+    x, gate, dh = (torch.randn(n, steps, d, device=DEV, generator=gen).to(dtype)
+                   for _ in range(3))
     h, last, saved = B.sla_linrec_forward(x, gate, save=True)
     dx, dg, _ = B.sla_linrec_backward(x, gate, saved, dh)
     part = slice(4096, 8192 + 64)  # as many channels: the same chunks
