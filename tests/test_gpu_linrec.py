@@ -105,6 +105,35 @@ def test_packed_chunk_shapes(dt, d):
     check(got, reference(dt, "sigmoid", x, g, h0, offsets, dh, dl), (dt, d))
 
 
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f64", "f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,steps,d", [(8, 769, 1040), (2, 600, 120), (1, 2049, 8200),
+                                       (3, 1030, 180), (4, 33, 64), (3, 40, 301)])
+def test_saved_states_between_other_chunks(dt, mode, n, steps, d):
+    """Lengths and channels for which the two passes cut a sequence differently
+    (the forward pass wide, the backward pass narrow), and lengths just past
+    those that are not cut."""
+    say("recurrence two chunkings", dt, mode, n, steps, d)
+    x, g, h0, dh, dl = make(dt, mode, (n, steps), d, n, 16)
+    got = run(dt, mode, x, g, h0, None, dh, dl)
+    check(got, reference(dt, mode, x, g, h0, None, dh, dl), (dt, mode, n, steps, d))
+
+
+@pytest.mark.parametrize("dt", ["f64", "f32", "bf16"])
+@pytest.mark.parametrize("lens,d", [([700, 0, 900, 1, 513, 1100], 120),
+                                    ([700, 0, 900, 1, 513, 1100], 1024),
+                                    ([5, 3000, 5, 5, 5, 5, 5], 192), ([1] * 300 + [400], 130),
+                                    ([0, 0, 5000, 0], 64)])
+def test_packed_with_rows_to_spare(dt, lens, d):
+    """Sequences much shorter or longer than the mean length, which sets the
+    chunks: rows past a sequence's end, chains of many chunks among them."""
+    offsets = np.concatenate([[0], np.cumsum(lens)])
+    say("recurrence rows to spare", dt, len(lens), int(offsets[-1]), d)
+    x, g, h0, dh, dl = make(dt, "sigmoid", (int(offsets[-1]),), d, len(lens), 17)
+    got = run(dt, "sigmoid", x, g, h0, offsets, dh, dl)
+    check(got, reference(dt, "sigmoid", x, g, h0, offsets, dh, dl), (dt, lens[:3], d))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_past_the_caches(dtype):
     """More than 256 MB of rows: the same bits as a part of the channels alone,
