@@ -27,26 +27,29 @@ namespace {
 
 // A workgroup takes a chunk: W channels of as many steps as its registers
 // hold.  A thread has V neighbouring channels of consecutive steps.  The
-// backward pass holds more per element and spreads a chunk over twice the
-// threads; a chunk of the forward pass is one or more of the backward's.
-constexpr int kForward = 512, kBackward = 1024;
-// The channels of wide chunks and of narrow ones (see width_of).
-constexpr int kManyForward = 128, kManyBackward = 256, kNarrow = 64;
-// Whether the forward pass keeps the coefficients between its two passes over
-// a chunk, or the rows as they were loaded, which take half the registers
-// in 16 bits and allow a chunk of twice the steps.
-constexpr bool keeps(size_t size, int width) { return size > 2 || width != kNarrow; }
+// backward pass holds more per element, in chunks of half the steps.
+constexpr int kThreads = 512;
+// The channels of narrow chunks, and of the forward pass's wide ones (see
+// width_of).
+constexpr int kNarrow = 64, kWide = 128;
 constexpr int chunk_of(size_t size, int width, bool backward) {
-  return (size == 8 ? 8192 : backward || keeps(size, width) ? 16384 : 32768) / width;
+  return (size == 8 || backward ? 8192 : 16384) / width;
 }
 template <typename T, int W, bool BACKWARD>
 constexpr int chunk_steps() {
   return chunk_of(sizeof(T), W, BACKWARD);
 }
+// The steps from one saved state to the next: a chunk of the backward pass.
+constexpr int kSave = chunk_of(2, kNarrow, true);
+static_assert(kSave == chunk_of(8, kNarrow, true), "of any type");
+// Whether the forward pass keeps the coefficients between its two passes over
+// a chunk, or the rows as they were loaded, which in 16 bits take half the
+// registers and let half the threads hold a chunk.
+constexpr bool keeps(size_t size, int width) { return size > 2 || width != kNarrow; }
 // Rows that are kept as loaded but not in pairs take a register an element.
 template <typename T, int W, int V>
 constexpr int forward_threads() {
-  return !keeps(sizeof(T), W) && V == 1 ? 2 * kForward : kForward;
+  return keeps(sizeof(T), W) || V == 1 ? kThreads : kThreads / 2;
 }
 
 // 1 / (1 + e^-g), the coefficient, and 1 / (1 + e^g), the weight of x, neither
@@ -86,8 +89,6 @@ struct Args {
   T* h;
   C* h_last;
   C* saved;      // the state after each chunk of the backward pass
-  int save_log;  // log2 of those chunks' steps
-  int64_t saves;     // dense: of each sequence
   T* grad_x;
   T* grad_gate;
   C* grad_h0;
@@ -476,10 +477,11 @@ __device__ __forceinline__ void row_fence(int i) {
 //
 // Bound by the bytes of x, gate and h, at the rate at which rows are reached in
 // pieces of 128 or 256 bytes, and by the latency of the joining: 4 x 4096 x 4096
-// bf16 85 us (4.7 TB/s; the chunks without the joining 78 us), 8 x 2048 x 2048
-// bf16 47 us (37 us), 65536 x 512 fp32 82 us (4.9 TB/s), 262144 x 1024 fp16 349
-// us (4.6 TB/s).  A quarter-rate exponential and reciprocal an element leave
-// no room to work the coefficients out twice where registers hold them.
+// bf16 84 us (4.8 TB/s; the chunks without the joining 78 us), 8 x 2048 x 2048
+// bf16 47 us (37 us), 65536 x 512 fp32 84 to 90 us (4.5 to 4.8 TB/s), 262144 x 1024
+// fp16 331 us (4.9 TB/s; in chunks of twice the steps and threads 349 us).  A
+// quarter-rate exponential and reciprocal an element leave no room to work the
+// coefficients out twice where registers hold them.
 // Workgroups that stay and fetch the next chunk's rows while they join one
 // took 148 us for the first of these: two fit a compute unit, and neither
 // hides the other's wait.
@@ -494,7 +496,7 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
   Where w;
   if (!my_chunk<W, CHAIN, false>(p, w, block)) return;
   if (CHAIN && unused_row<W, P::kChunk>(p, w, block)) return;
-  static_assert(chunk_steps<T, kManyBackward, true>() % S == 0, "saved states fall between parts");
+  static_assert(kSave % S == 0, "saved states fall between parts");
   const P r = my_part<P>(p, w, block);
 
   // The rows as loaded or, where they fit, the coefficients they give; else
@@ -574,10 +576,11 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
       s_m[q][threadIdx.x] = h;
       h = next;
       // the state where a chunk of the backward pass ends and another follows
-      const int64_t t = w.c * P::kChunk + (q + 1) * S, k = t >> p.save_log;
-      if (p.saved && k << p.save_log == t && t < w.len && act) {
-        const int64_t row = p.offsets ? (w.first >> p.save_log) + w.s : w.s * p.saves;
-        *lane_ptr(p.saved + (row + k - 1) * p.dim + ch0, at) = h;
+      const int64_t t = w.c * P::kChunk + (q + 1) * S;
+      if (p.saved && t % kSave == 0 && t < w.len && act) {
+        const int64_t row = p.offsets ? w.first / kSave + w.s
+                                      : w.s * ((p.steps + kSave - 1) / kSave);
+        *lane_ptr(p.saved + (row + t / kSave - 1) * p.dim + ch0, at) = h;
       }
     }
   }
@@ -616,18 +619,19 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
 // taken in the one pass over the rows.
 //
 // Bound as the forward pass, by the bytes of x, gate, dh and the two gradients,
-// and by registers: two workgroups a compute unit leave a thread 64 of them for
-// its 16 elements (16 bits; some are spilt): 8 x 2048 x 2048 bf16 84 us (4.0
-// TB/s; without the joining 75 us), 65536 x 512 fp32 136 us (4.9 TB/s), 120 packed
-// sequences of 833 x 1024 bf16 270 us (3.8 TB/s).
-template <typename T, int GATE, int W, int V, bool CHAIN>
-__global__ __launch_bounds__(kBackward, sizeof(T) == 2 ? 8 : 4) void rec_backward(Args<T> p) {
+// and by registers: in 16 bits a thread has 64 of them for its 16 elements (some
+// are spilt), so that four workgroups share a compute unit: 8 x 2048 x 2048 bf16 80
+// us (4.2 TB/s; with two workgroups of 1024 threads 86 us), 65536 x 512 fp32 134 us
+// (5.0 TB/s), 120 packed sequences of 833 x 1024 bf16 268 us (3.8 TB/s).
+template <typename T, int GATE, int V, bool CHAIN>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward(Args<T> p) {
   using C = typename Compute<T>::type;
-  using P = Part<T, W, V, kBackward, true>;
+  constexpr int W = kNarrow;
+  using P = Part<T, W, V, kThreads, true>;
   constexpr bool kSig = GATE == SLA_GATE_SIGMOID;
   constexpr int S = P::S, kSubs = P::kSubs;
   __shared__ C s_a[kSubs][W], s_m[kSubs][W], s_u[kSubs][W];
-  __shared__ Pack<T, V> s_d[S][kBackward];
+  __shared__ Pack<T, V> s_d[S][kThreads];
   int block;
   Where w;
   if (!my_chunk<W, CHAIN, true>(p, w, block)) return;
@@ -833,21 +837,18 @@ sla_status refuse(const char* msg) {
 }
 
 // Channels of a chunk.  Narrow chunks have more steps, so fewer of them are
-// joined one after the other; wide ones are filled by shorter sequences and
-// reach longer pieces of a row.  Narrow and wide, us: packed 12 of 8333 x 1024
-// bf16, forward 154, 172, backward 249, 337; 120 of 833, forward 195, 185,
-// backward 271, 289; 800 of 125, 394, 350 and 430, 307; dense 8 x 4096 x 1024,
-// bf16 forward 60, 50, backward 93, 100, fp32 backward 141, 132; 1000 x 300 x
-// 64, half of a wide chunk's lanes without a channel, forward 36, 54.
+// joined one after the other; wide ones reach longer pieces of a row, which
+// pays where many sequences and channels stand side by side.  Forward, narrow and
+// wide, us: dense bf16 8 x 4096 x 1024 56, 50, 1000 x 300 x 256 130, 117, 1 x 65536 x 512
+// fp32 93, 119; packed bf16 x 1024, 12 sequences of 8333 151, 180, 120 of 833 161,
+// 187, 800 of 125 220, 246 (fp32 x 512: 156, 136).  The backward pass with 256
+// channels: 92 and 129, 193 and 221, 144 and 296; 264 and 600, 269 and 453, 276
+// and 407.
 int width_of(const sla_linrec_shape& q, bool backward) {
-  const int wide = backward ? kManyBackward : kManyForward;
-  const size_t size = dtype_bytes(q.dtype);
-  // under a quarter of the lanes without a channel
-  if ((q.dim + wide - 1) / wide * wide * 3 > q.dim * 4) return kNarrow;
-  const int64_t length = q.d_offsets ? q.steps / std::max<int64_t>(q.n_seq, 1) : q.steps;
-  if (length < 2 * chunk_of(size, kNarrow, backward)) return wide;
-  const int64_t side = (q.d_offsets ? 1 : q.n_seq) * q.dim;
-  return side >= 8192 && !(backward && size == 2) ? wide : kNarrow;
+  if (backward || q.d_offsets || q.n_seq * q.dim < 8192) return kNarrow;
+  // under a quarter of the lanes without a channel: 1000 x 300 x 64 bf16, forward, 36
+  // us narrow and 54 wide
+  return (q.dim + kWide - 1) / kWide * kWide * 3 > q.dim * 4 ? kNarrow : kWide;
 }
 int chunk_of(const sla_linrec_shape& q, bool backward) {
   return chunk_of(dtype_bytes(q.dtype), width_of(q, backward), backward);
@@ -955,9 +956,6 @@ Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_
   const int chunk = chunk_of(q, backward);
   p.chunks = (int)std::max<int64_t>(1, (q.steps + chunk - 1) / chunk);
   p.rows = rows_of(q, backward);
-  const int save = chunk_of(q, true);  // a power of two
-  p.save_log = __builtin_ctz(save);
-  p.saves = (q.steps + save - 1) / save;
   // 16-bit rows beyond what the last-level cache holds (256 MB) go past it:
   // forward, 4 x 4096 x 4096 bf16 90.9 -> 87.9 us, 262144 x 1024 fp16 352 -> 345 us.
   // In 32 bits it does not pay: 65536 x 512, both directions, 224 us through it and
@@ -968,9 +966,9 @@ Args<T> common_args(const sla_linrec_shape& q, const void* x, int64_t xs, int64_
 }
 
 // Channels per thread, where every array's rows allow it: what 8 bytes hold
-// forward (4 x 4096 x 4096 bf16 88.5 us, with 4 bytes 91.8; both directions of 8 x
-// 2048 x 2048 143.2 and 141.8), 4 bytes backward (those 143, with 8 bytes 175:
-// twice as many parts to join, half as many steps in each).
+// forward (4 x 4096 x 4096 bf16 88.5 us a call, with 4 bytes 91.8), 4 bytes backward
+// (both directions of 8 x 2048 x 2048 143 us, with 8 bytes 175: twice as many
+// parts to join, half as many steps in each).
 template <typename T>
 constexpr int most_v(bool backward) {
   return std::max(1, (backward ? 4 : 8) / (int)sizeof(T));
@@ -1017,8 +1015,7 @@ sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool packed_v, void
     else with_v(w, std::integral_constant<int, 1>{});
   };
   if (width == kNarrow) with_w(std::integral_constant<int, kNarrow>{});
-  else if (backward) with_w(std::integral_constant<int, kManyBackward>{});
-  else with_w(std::integral_constant<int, kManyForward>{});
+  else with_w(std::integral_constant<int, kWide>{});
   SLA_HIP(hipGetLastError());
   return SLA_OK;
 }
@@ -1087,9 +1084,8 @@ sla_status sla_linrec_forward(const sla_linrec_shape* shape, const void* d_x,
     }
     return run_chunks<M>(q, p, wide, d_work, false, s, [&](auto w, auto v, auto chain, dim3 grid) {
       constexpr int W = decltype(w)::value, V = decltype(v)::value;
-      if constexpr (W == kNarrow || W == kManyForward)
-        rec_forward<T, GATE, W, V, decltype(chain)::value>
-            <<<grid, (forward_threads<T, W, V>()), 0, s>>>(p);
+      rec_forward<T, GATE, W, V, decltype(chain)::value>
+          <<<grid, (forward_threads<T, W, V>()), 0, s>>>(p);
     });
   });
 }
@@ -1138,9 +1134,9 @@ sla_status sla_linrec_backward(const sla_linrec_shape* shape, const void* d_x,
     p.grad_gate = (T*)d_grad_gate;
     p.grad_h0 = (C*)d_grad_h0;
     return run_chunks<M>(q, p, wide, d_work, true, s, [&](auto w, auto v, auto chain, dim3 grid) {
-      constexpr int W = decltype(w)::value, V = decltype(v)::value;
-      if constexpr (W == kNarrow || W == kManyBackward)
-        rec_backward<T, GATE, W, V, decltype(chain)::value><<<grid, kBackward, 0, s>>>(p);
+      if constexpr (decltype(w)::value == kNarrow)
+        rec_backward<T, GATE, decltype(v)::value, decltype(chain)::value>
+            <<<grid, kThreads, 0, s>>>(p);
     });
   });
 }

@@ -111,8 +111,8 @@ def test_packed_chunk_shapes(dt, d):
                                        (3, 1030, 180), (4, 33, 64), (3, 40, 301)])
 def test_saved_states_between_other_chunks(dt, mode, n, steps, d):
     """Lengths and channels for which the two passes cut a sequence differently
-    (the forward pass wide, the backward pass narrow), and lengths just past
-    those that are not cut."""
+    (the forward pass in chunks of 64, 128 or 256 steps, the backward pass of
+    128), and lengths just past those that are not cut."""
     say("recurrence two chunkings", dt, mode, n, steps, d)
     x, g, h0, dh, dl = make(dt, mode, (n, steps), d, n, 16)
     got = run(dt, mode, x, g, h0, None, dh, dl)
