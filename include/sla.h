@@ -435,6 +435,9 @@ sla_status sla_pcg_solve_noalloc(sla_mat_t A, sla_mat_t G, double eps, const voi
  * Non-finite values propagate as in the formulas; a gate of -infinity
  * (sigmoid: then a <= 2^-125, 0 in fp64) or 0 (linear) cuts the sequence there
  * unless h_{t-1} is itself non-finite.
+ * Linear coefficients may have any size.  Where products of them leave the
+ * range of the type and the states do not, the call takes longer, but the
+ * states are those of the formulas.
  */
 typedef enum { SLA_GATE_LINEAR = 0, SLA_GATE_SIGMOID = 1, SLA_GATE_RANGE_ = 0x7fffffff } sla_gate;
 

@@ -52,6 +52,81 @@ constexpr int forward_threads() {
   return keeps(sizeof(T), W) || V == 1 ? kThreads : kThreads / 2;
 }
 
+// Products of coefficients can leave the range of their type where the states
+// that they carry do not: 300 steps that double a state of zero, a coefficient
+// of zero after very large ones, a large state that shrinks by more than the
+// type can express, an infinite one that stays infinite.
+//
+// A product is therefore zero only where a coefficient is, and the least number
+// where it underflowed.  The sigmoid's coefficients, at most 1 (UNIT), lose no
+// more than that.  With linear gates
+//  - a part (a thread's steps) whose product lost more has NaN in its place;
+//  - a chunk whose map (a, m) is not finite, or whose product lost more, does
+//    not offer it: what leaves it is taken from part to part;
+//  - a small product is not applied where what it lost shows (loses);
+//  - where the parts' maps fail, the steps of the channel in the chunk are taken
+//    one by one, from memory, by the wave that joins the parts.
+template <typename C>
+struct Range {
+  static constexpr bool k64 = sizeof(C) == 8;
+  static constexpr C kNormal = k64 ? C(0x1p-1022) : C(0x1p-126f);
+  static constexpr C kLeast = k64 ? C(0x1p-1074) : C(0x1p-149f);
+  // A product that underflowed and then grows by kGrowth at most is known to
+  // kLeast kGrowth, which is a rounding error of kSmall.
+  static constexpr C kGrowth = k64 ? C(0x1p64) : C(0x1p24);
+  static constexpr C kSmall = k64 ? C(0x1p-950) : C(0x1p-100);
+};
+template <typename C>
+__device__ __forceinline__ bool infinite(C v) {
+  return fabs(v) == C(INFINITY);
+}
+// A product whose smallest factor is `least`.
+template <typename C>
+__device__ __forceinline__ C not_zero(C product, C least) {
+  return ((product == C(0)) & (least != C(0))) ? copysign(Range<C>::kLeast, product) : product;
+}
+// Whether a h + m loses what it should hold of the state h: a may be off by
+// kLeast kGrowth, and m does not hide it.
+template <typename C>
+__device__ __forceinline__ bool loses(C a, C h, C m) {
+  const C shows = fabs(h) * Range<C>::kSmall;
+  return (fabs(a) < Range<C>::kSmall) & (a != C(0)) & (fabs(m) < shows) & (shows < C(INFINITY));
+}
+
+// Follows the coefficients of a part and their product.
+template <bool UNIT, typename C>
+struct Factors {
+  C least = C(1), low = C(1), most = C(0);  // smallest coefficient, product; largest coefficient
+  __device__ __forceinline__ void take(C a, C product) {
+    least = min(least, fabs(a));
+    if constexpr (!UNIT) low = min(low, fabs(product)), most = max(most, fabs(a));
+  }
+  // The product, unless it grew after it had underflowed and matters, for no
+  // coefficient is zero.  (No branches: the compiler would move the pass over
+  // the rows into them.)
+  __device__ __forceinline__ C checked(C product) const {
+    const C a = not_zero(product, least);
+    if constexpr (UNIT) return a;
+    return ((low < Range<C>::kNormal) & (most > C(1)) & (least != C(0))) ? C(NAN) : a;
+  }
+};
+// Follows the parts of a chunk and their product.
+template <bool UNIT, typename C>
+struct Joined {
+  C least = C(1), low = C(1), growth = C(1);  // smallest part, product; all growth
+  __device__ __forceinline__ void take(C part, C product) {
+    least = min(least, fabs(part));
+    if constexpr (!UNIT) low = min(low, fabs(product)), growth *= max(fabs(part), C(1));
+  }
+  // Whether the map (product, m) stands for the chunk.
+  __device__ __forceinline__ bool whole(C& product, C m) const {
+    product = not_zero(product, least);
+    if constexpr (UNIT) return true;
+    return __builtin_isfinite(product) && __builtin_isfinite(m) &&
+           (min(low, least) >= Range<C>::kNormal || growth <= Range<C>::kGrowth);
+  }
+};
+
 // 1 / (1 + e^-g), the coefficient, and 1 / (1 + e^g), the weight of x, neither
 // as a difference of nearly equal numbers.
 __device__ __forceinline__ void sigmoid2(float g, float& a, float& keep) {
@@ -204,10 +279,14 @@ enum Progress { kNothing = 0, kSums = 1, kEnd = 2 };
 // each chunk's own end is computed, so the bits do not depend on how far the
 // look went.  progress, ends and sums point at the nearest chunk's.
 
+// Nothing is carried over a sum that does not stand for its chunk: a chunk
+// without a map publishes none, and one whose map loses what it should carry is
+// not used; then that chunk's end is waited for.
+
 // The nearest two, in one trip to memory (the backward pass with four: 8 x 4096 x
 // 1024 bf16 104 -> 124 us, for what is read in vain; forward 45.8 -> 47.6 us).
 constexpr int kNear = 2;
-template <int STEP, typename C>
+template <int STEP, bool UNIT, typename C>
 __device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_t bytes,
                                            int64_t dim, int have, C& carry) {
   C e[kNear], a[kNear], m[kNear];
@@ -229,24 +308,28 @@ __device__ __forceinline__ bool near_carry(const C* ends, const C* sums, uint32_
   }
   if (at < 0) return false;
   carry = e[0];
+  bool ok = true;
 #pragma unroll
   for (int j = kNear - 1; j >= 0; --j) {
     if (j == at) carry = e[j];
-    if (j + 1 < kNear && j < at) carry = a[j] * carry + m[j];
+    if (j + 1 < kNear && j < at) {
+      ok = ok && (UNIT || !loses(a[j], carry, m[j]));
+      carry = a[j] * carry + m[j];
+    }
   }
-  return true;
+  return __all(ok);
 }
 
-// Every chunk publishes its sums before it waits for anything, and a chunk
-// waits only for chunks whose tickets were drawn before its own, by
+// Every chunk publishes its sums, if it has any, before it waits for anything,
+// and a chunk waits only for chunks whose tickets were drawn before its own, by
 // workgroups that therefore run already: the wait ends.
 constexpr int kReach = 32, kBatch = 8;
-template <int STEP, typename C>
+template <int STEP, bool UNIT, typename C>
 __device__ __forceinline__ C wait_carry(const int* progress, const C* ends, const C* sums,
                                         uint32_t bytes, int64_t dim, int64_t have) {
   const int n = (int)min(have, (int64_t)kReach), lane = threadIdx.x & 63;
   C near = C(0);
-  if (near_carry<STEP>(ends, sums, bytes, dim, n, near)) return near;
+  if (near_carry<STEP, UNIT>(ends, sums, bytes, dim, n, near)) return near;
   for (;; __builtin_amdgcn_s_sleep(1)) {
     int f = kNothing;
     if (lane < n)
@@ -270,7 +353,7 @@ __device__ __forceinline__ C wait_carry(const int* progress, const C* ends, cons
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         if (top - 1 - q >= 0) {
-          ok = ok && written(a[q]) && written(m[q]);
+          ok = ok && written(a[q]) && written(m[q]) && (UNIT || !loses(a[q], h, m[q]));
           h = a[q] * h + m[q];
         }
       }
@@ -472,6 +555,66 @@ __device__ __forceinline__ void row_fence(int i) {
   if ((i + 1) * V % 4 == 0) __builtin_amdgcn_sched_barrier(0);
 }
 
+// The linear steps of a lane's channel, ch0 + lane, in a chunk one by one, from
+// memory, where the parts' maps do not stand for them; `enter` takes what enters
+// part q (and, of states, what leaves the last).
+template <typename P, typename C, typename T, typename F>
+__device__ __forceinline__ C walk_states(const Args<T>& p, const Where& w, int64_t ch0, C h,
+                                         F enter) {
+  const int64_t t0 = w.c * P::kChunk;
+  const T* g = p.gate + w.g + t0 * p.g_step + ch0;
+  const T* x = p.x + w.x + t0 * p.x_step + ch0;
+  const uint32_t lane = threadIdx.x * (uint32_t)sizeof(T);
+  int n = (int)min(w.len - t0, (int64_t)P::kChunk);
+#pragma unroll 1
+  for (int q = 0; q < P::kSubs; ++q) {
+    enter(q, h);
+#pragma unroll 1
+    for (int i = 0; i < P::S && n > 0; ++i, --n) {
+      h = (C)*lane_ptr(g, lane) * h + (C)*lane_ptr(x, lane);
+      g += p.g_step, x += p.x_step;
+    }
+  }
+  enter(P::kSubs, h);
+  return h;
+}
+// The adjoint, from the chunk's end to its beginning.
+template <typename P, typename C, typename T, typename F>
+__device__ __forceinline__ C walk_adjoint(const Args<T>& p, const Where& w, int64_t ch0, C mu,
+                                          F enter) {
+  const int64_t t0 = w.c * P::kChunk;
+  const int n = (int)min(w.len - t0, (int64_t)P::kChunk);
+  const T* g = p.gate + w.g + (t0 + n) * p.g_step + ch0;
+  const T* d = p.grad_h + w.d + (t0 + n) * p.d_step + ch0;
+  const uint32_t lane = threadIdx.x * (uint32_t)sizeof(T);
+#pragma unroll 1
+  for (int q = P::kSubs - 1; q >= 0; --q) {
+    enter(q, mu);
+#pragma unroll 1
+    for (int i = min(n - q * P::S, P::S); i > 0; --i) {
+      g -= p.g_step, d -= p.d_step;
+      mu = (C)*lane_ptr(g, lane) * ((p.grad_h ? (C)*lane_ptr(d, lane) : C(0)) + mu);
+    }
+  }
+  return mu;
+}
+// Whether that is needed: `from` entered the chunk and the parts' maps, part(0)
+// the first taken, made `to` of it, by way of state(0) = from, state(1) ...,
+// `high` the largest.  Once not finite, a state stays so, so its last value tells.
+template <int N, typename C, typename F, typename G>
+__device__ __forceinline__ bool went_wrong(C from, C to, C high, F part, G state) {
+  bool wrong = to != to || (infinite(to) && !infinite(from));
+  if (high > Range<C>::kGrowth) {
+#pragma unroll 1
+    for (int k = 0; k < N; ++k) {
+      const C a = fabs(part(k)), after = k + 1 < N ? state(k + 1) : to;
+      wrong = wrong || (a < Range<C>::kNormal && a != C(0) &&
+                        fabs(after) < fabs(state(k)) * Range<C>::kSmall);
+    }
+  }
+  return wrong && from == from;
+}
+
 // One chunk of a sequence.  CHAIN: sequences may have several, joined by the
 // look-back; otherwise each has one.
 //
@@ -517,7 +660,12 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
     }
   };
   {
+    // Where the registers are full of rows, a product that came out as zero is
+    // looked into afterwards: 262144 x 1024 fp16 343 us, 350 with every
+    // coefficient followed (120 packed sequences of 833 x 1024 bf16 154 and 164).
+    constexpr bool kFollow = !kSig || kKeep || V == 1;
     C pa[V], pm[V];
+    Factors<kSig, C> f[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0);
 #pragma unroll
@@ -529,11 +677,23 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
         if constexpr (kKeep) ka[i][v] = a, kb[i][v] = b;
         pm[v] = a * pm[v] + b;
         pa[v] *= a;
+        if constexpr (kFollow) f[v].take(a, pa[v]);
       }
       row_fence<V>(i);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_a[r.sub][r.c0 + v] = pa[v], s_m[r.sub][r.c0 + v] = pm[v];
+    for (int v = 0; v < V; ++v) {
+      if constexpr (kFollow) {
+        pa[v] = f[v].checked(pa[v]);
+      } else if (pa[v] == C(0)) {
+        C least = (C)g[0].v[v], keep;
+#pragma unroll
+        for (int i = 1; i < S; ++i) least = min(least, (C)g[i].v[v]);
+        sigmoid2(least, least, keep);
+        pa[v] = not_zero(pa[v], least);
+      }
+      s_a[r.sub][r.c0 + v] = pa[v], s_m[r.sub][r.c0 + v] = pm[v];
+    }
   }
   __syncthreads();
   // From here a lane has a channel, in the first W / 64 waves.
@@ -544,44 +704,69 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
   C *ends = p.ends + row0, *sums = p.sums + row0 + w.row * p.dim;
   int* mark = p.progress + w.mark + (int64_t)(threadIdx.x >> 6) * p.links;
   C ca = C(1), cm = C(0), h = C(0);
+  bool whole = true;  // the chunk's map stands for it
   if (CHAIN && join) {
+    Joined<kSig, C> f;
 #pragma unroll 4
     for (int q = 0; q < kSubs; ++q) {
       const C pa = s_a[q][threadIdx.x];
       cm = pa * cm + s_m[q][threadIdx.x];
       ca *= pa;
+      f.take(pa, ca);
     }
-    if (act) {
-      publish(sums, at, ca);
-      publish(sums + p.dim, at, cm);
+    whole = f.whole(ca, cm);
+    if (kSig || __all(whole || !act)) {
+      if (act) {
+        publish(sums, at, ca);
+        publish(sums + p.dim, at, cm);
+      }
+      tell(mark, kSums);
     }
-    tell(mark, kSums);
   }
   if (join) {
     if (w.c == 0) {
       if (p.h0) h = *lane_ptr(p.h0 + w.s * p.dim + ch0, at);
     } else if constexpr (CHAIN) {
-      h = wait_carry<-1>(mark - 1, ends - p.dim, sums - 2 * p.dim, at, p.dim, w.c);
+      h = wait_carry<-1, kSig>(mark - 1, ends - p.dim, sums - 2 * p.dim, at, p.dim, w.c);
     }
-    if constexpr (CHAIN) {
-      if (act) publish(ends, at, ca * h + cm);
+    whole = whole && (kSig || !loses(ca, h, cm));
+    const bool now = CHAIN && (kSig || __all(whole || !act));
+    const C from = h, end = ca * h + cm;
+    if (now) {
+      if (act) publish(ends, at, end);
       tell(mark, kEnd);
     }
     if (w.len == 0 && w.c == 0 && act && p.h_last)
       *lane_ptr(p.h_last + w.s * p.dim + ch0, at) = h;
-    // what enters each part, in the place of its sum
-#pragma unroll 4
-    for (int q = 0; q < kSubs; ++q) {
-      const C next = s_a[q][threadIdx.x] * h + s_m[q][threadIdx.x];
-      s_m[q][threadIdx.x] = h;
-      h = next;
-      // the state where a chunk of the backward pass ends and another follows
-      const int64_t t = w.c * P::kChunk + (q + 1) * S;
+    // the state where a chunk of the backward pass ends and another follows
+    auto save = [&](int q, C h) {
+      const int64_t t = w.c * P::kChunk + q * S;
       if (p.saved && t % kSave == 0 && t < w.len && act) {
         const int64_t row = p.offsets ? w.first / kSave + w.s
                                       : w.s * ((p.steps + kSave - 1) / kSave);
         *lane_ptr(p.saved + (row + t / kSave - 1) * p.dim + ch0, at) = h;
       }
+    };
+    // what enters each part, in the place of its sum
+    C high = C(0);
+#pragma unroll 4
+    for (int q = 0; q < kSubs; ++q) {
+      const C next = s_a[q][threadIdx.x] * h + s_m[q][threadIdx.x];
+      if constexpr (!kSig) high = max(high, fabs(h));
+      s_m[q][threadIdx.x] = h;
+      h = next;
+      save(q + 1, h);
+    }
+    if (!kSig && act &&
+        went_wrong<kSubs>(from, h, high, [&](int q) { return s_a[q][threadIdx.x]; },
+                          [&](int q) { return s_m[q][threadIdx.x]; }))
+      h = walk_states<P>(p, w, ch0, from, [&](int q, C h) {
+        if (q < kSubs) s_m[q][threadIdx.x] = h;
+        if (q > 0) save(q, h);
+      });
+    if (CHAIN && !kSig && !now) {
+      if (act) publish(ends, at, whole ? end : h);
+      tell(mark, kEnd);
     }
   }
   __syncthreads();
@@ -653,8 +838,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward
   };
   {
     C pa[V], pm[V], pu[V];
+    Factors<kSig, C> k[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0), pu[v] = C(0);
+    constexpr bool kRoom = sizeof(T) == 4;  // for the coefficients themselves
+    C ka[kRoom ? S : 1][V];
     Pack<T, V> g[S], d[S];
     load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams,
                     idle_gate<GATE, T>(), g);
@@ -672,16 +860,32 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward
           f[i][v] = fold(a, keep);
           b *= keep;
         }
+        if constexpr (kRoom) ka[i][v] = a;
         pm[v] = a * pm[v] + b;
         pa[v] *= a;
-        pu[v] = pa[v] * (C)d[i].v[v] + pu[v];  // mu leaving the part, from a zero start
+        k[v].take(a, pa[v]);
       }
       s_d[i][threadIdx.x] = d[i];
       forget(x[i]);
       row_fence<V>(i);
     }
+    // mu leaving the part, from a zero start; from its end, so that no product
+    // of coefficients comes in
+#pragma unroll
+    for (int i = S - 1; i >= 0; --i) {
+      const Pack<T, V> d = s_d[i][threadIdx.x];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        C a, keep;
+        if constexpr (kRoom) a = ka[i][v];
+        else step(i, v, a, keep);
+        pu[v] = a * ((C)d.v[v] + pu[v]);
+      }
+      row_fence<V>(i);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      pa[v] = k[v].checked(pa[v]);
       s_a[r.sub][r.c0 + v] = pa[v];
       s_m[r.sub][r.c0 + v] = pm[v];
       s_u[r.sub][r.c0 + v] = pu[v];
@@ -694,47 +898,76 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward
   const bool join = threadIdx.x < W, act = (int)threadIdx.x < channels;
   const uint32_t at = act ? threadIdx.x * (uint32_t)sizeof(C) : 0;
   C *ends = p.ends + row0, *sums = p.sums + row0 + w.row * p.dim;
-  int* mark = p.progress + w.mark + (int64_t)(threadIdx.x >> 6) * p.links;
+  int* mark = p.progress + w.mark;
   C ca = C(1), cu = C(0), mu = C(0);
   if (join) {
+    bool whole = true;  // the chunk's map of mu stands for it
     if constexpr (CHAIN) {
+      Joined<kSig, C> k;
 #pragma unroll 4
       for (int q = kSubs - 1; q >= 0; --q) {
         const C pa = s_a[q][threadIdx.x];
         cu = pa * cu + s_u[q][threadIdx.x];
         ca *= pa;
+        k.take(pa, ca);
       }
-      if (act) {
-        publish(sums, at, ca);
-        publish(sums + p.dim, at, cu);
+      whole = k.whole(ca, cu);
+      if (kSig || __all(whole || !act)) {
+        if (act) {
+          publish(sums, at, ca);
+          publish(sums + p.dim, at, cu);
+        }
+        tell(mark, kSums);
       }
-      tell(mark, kSums);
     }
     C h = C(0);
     if (w.c > 0) h = *lane_ptr(p.saved + row0 - p.dim, at);
     else if (p.h0) h = *lane_ptr(p.h0 + state0, at);
+    const C h_from = h;
     // what enters each part from before, in the place of its sum
+    C high = C(0);
 #pragma unroll 4
     for (int q = 0; q < kSubs; ++q) {
       const C next = s_a[q][threadIdx.x] * h + s_m[q][threadIdx.x];
+      if constexpr (!kSig) high = max(high, fabs(h));
       s_m[q][threadIdx.x] = h;
       h = next;
     }
+    if (!kSig && act &&
+        went_wrong<kSubs>(h_from, h, high, [&](int q) { return s_a[q][threadIdx.x]; },
+                          [&](int q) { return s_m[q][threadIdx.x]; }))
+      walk_states<P>(p, w, ch0, h_from, [&](int q, C h) {
+        if (q < kSubs) s_m[q][threadIdx.x] = h;
+      });
     if (w.after == 0) {
       if (p.grad_last) mu = *lane_ptr(p.grad_last + state0, at);
     } else if constexpr (CHAIN) {
-      mu = wait_carry<1>(mark + 1, ends + p.dim, sums + 2 * p.dim, at, p.dim, w.after);
+      mu = wait_carry<1, kSig>(mark + 1, ends + p.dim, sums + 2 * p.dim, at, p.dim, w.after);
     }
-    if constexpr (CHAIN) {
-      if (act) publish(ends, at, ca * mu + cu);
+    whole = whole && (kSig || !loses(ca, mu, cu));
+    const bool now = CHAIN && (kSig || __all(whole || !act));
+    const C from = mu, end = ca * mu + cu;
+    if (now) {
+      if (act) publish(ends, at, end);
       tell(mark, kEnd);
     }
     if (w.len == 0 && w.c == 0 && act && p.grad_h0) *lane_ptr(p.grad_h0 + state0, at) = mu;
+    high = C(0);
 #pragma unroll 4
     for (int q = kSubs - 1; q >= 0; --q) {
       const C next = s_a[q][threadIdx.x] * mu + s_u[q][threadIdx.x];
+      if constexpr (!kSig) high = max(high, fabs(mu));
       s_u[q][threadIdx.x] = mu;
       mu = next;
+    }
+    if (!kSig && act &&
+        went_wrong<kSubs>(from, mu, high,
+                          [&](int k) { return s_a[kSubs - 1 - k][threadIdx.x]; },
+                          [&](int k) { return s_u[kSubs - 1 - k][threadIdx.x]; }))
+      mu = walk_adjoint<P>(p, w, ch0, from, [&](int q, C mu) { s_u[q][threadIdx.x] = mu; });
+    if (CHAIN && !kSig && !now) {
+      if (act) publish(ends, at, whole ? end : mu);
+      tell(mark, kEnd);
     }
   }
   __syncthreads();
