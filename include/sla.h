@@ -453,7 +453,7 @@ typedef struct {
 /* Bytes of d_saved (the states the backward pass starts its recomputation
  * from, one every 128 steps) and of d_work for either direction (0: none needed).
  * Errors: SLA_ERR_INVALID_ARG (NULL, negative size, unknown dtype or gate),
- * SLA_ERR_UNSUPPORTED (a size beyond what one launch can index). */
+ * SLA_ERR_UNSUPPORTED (a size beyond what a call can index). */
 sla_status sla_linrec_sizes(const sla_linrec_shape *shape, size_t *saved_bytes,
                             size_t *work_bytes);
 

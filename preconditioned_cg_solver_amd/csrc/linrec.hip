@@ -90,7 +90,8 @@ __device__ __forceinline__ C not_zero(C product, C least) {
 template <typename C>
 __device__ __forceinline__ bool loses(C a, C h, C m) {
   const C shows = fabs(h) * Range<C>::kSmall;
-  return (fabs(a) < Range<C>::kSmall) & (a != C(0)) & (fabs(m) < shows) & (shows < C(INFINITY));
+  const bool small = fabs(a) < Range<C>::kSmall, hidden = !(fabs(m) < shows);
+  return small & !hidden & (a != C(0)) & (shows < C(INFINITY));
 }
 
 // Follows the coefficients of a part and their product.
@@ -174,6 +175,7 @@ struct Args {
   int chains, links, counters;  // chains of chunks, chunks of each, counters of tickets
   int blocks;        // channel blocks
   int64_t rows;      // chunks of all sequences (packed: at most)
+  unsigned before;   // workgroups of earlier launches of the call
   bool streams;      // the rows go past the caches
   // joining the chunks of a sequence
   int* ticket;
@@ -408,13 +410,14 @@ __global__ __launch_bounds__(kWG) void rec_begin(Word<C>* sums, int64_t n_sums, 
 template <int W, bool CHAIN, bool REVERSE, typename T>
 __device__ __forceinline__ bool my_chunk(const Args<T>& p, Where& w, int& block) {
   if constexpr (!CHAIN) {
-    const int64_t s = blockIdx.x / (unsigned)p.blocks;
-    block = blockIdx.x % (unsigned)p.blocks;
+    const unsigned group = p.before + blockIdx.x;
+    const int64_t s = group / (unsigned)p.blocks;
+    block = group % (unsigned)p.blocks;
     w = locate<chunk_steps<T, W, REVERSE>()>(p, s, p.offsets ? 0 : s * p.chunks);
     return true;
   } else {
     __shared__ int drawn;
-    const unsigned J = p.counters, j = blockIdx.x % J;
+    const unsigned J = p.counters, j = blockIdx.x % J;  // (p.before is even)
     if (threadIdx.x == 0)
       drawn = __hip_atomic_fetch_add(p.ticket + j * (kTicketStep / sizeof(int)), 1,
                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -1023,7 +1026,7 @@ constexpr int kFew = 32;
 template <typename T, int GATE, int V>
 __global__ __launch_bounds__(kWG) void few_forward(Args<T> p) {
   using C = typename Compute<T>::type;
-  const int64_t k = (int64_t)blockIdx.x * kWG + threadIdx.x, per = p.dim / V;
+  const int64_t k = ((int64_t)p.before + blockIdx.x) * kWG + threadIdx.x, per = p.dim / V;
   if (k >= p.n_seq * per) return;
   const int64_t s = k / per, at = k % per * V;
   int64_t first = 0, len = p.steps;
@@ -1110,7 +1113,7 @@ sla_status check_shape(const sla_linrec_shape* q) {
       (__int128)q->n_seq * q->dim >= ((__int128)1 << 60) ||
       (__int128)(std::max(rows_of(*q, false), rows_of(*q, true)) + 2 * q->n_seq + 64) *
               (q->dim / 64 + 64) >= INT32_MAX) {
-    set_error("sizes beyond what one launch can index");
+    set_error("sizes beyond what a call can index");
     return SLA_ERR_UNSUPPORTED;
   }
   return SLA_OK;
@@ -1207,6 +1210,20 @@ constexpr int most_v(bool backward) {
   return std::max(1, (backward ? 4 : 8) / (int)sizeof(T));
 }
 
+// A launch has less than 2^32 threads: calls launch(grid) for `groups`
+// workgroups in as many launches as they need.  (A chunk waits for tickets drawn
+// before its own, in the same launch or an earlier one.)
+template <typename T, typename F>
+sla_status in_launches(Args<T>& p, int64_t groups, F&& launch) {
+  constexpr int64_t kMost = (((int64_t)1 << 32) - 1) / kThreads & ~(int64_t)1;
+  for (int64_t at = 0; at < groups; at += kMost) {
+    p.before = (unsigned)at;
+    launch(dim3((unsigned)std::min(groups - at, kMost)));
+    SLA_HIP(hipGetLastError());
+  }
+  return SLA_OK;
+}
+
 // Sets up the chunks' joining and calls launch(W, V, CHAIN, grid), the first
 // three as types.
 template <int M, typename T, typename F>
@@ -1240,17 +1257,17 @@ sla_status run_chunks(const sla_linrec_shape& q, Args<T>& p, bool packed_v, void
     SLA_HIP(hipGetLastError());
   }
   auto with_v = [&](auto w, auto v) {
-    if (chain) launch(w, v, std::true_type{}, dim3((unsigned)grid));
-    else launch(w, v, std::false_type{}, dim3((unsigned)grid));
+    return in_launches(p, grid, [&](dim3 g) {
+      if (chain) launch(w, v, std::true_type{}, g);
+      else launch(w, v, std::false_type{}, g);
+    });
   };
   auto with_w = [&](auto w) {
-    if (packed_v) with_v(w, std::integral_constant<int, M>{});
-    else with_v(w, std::integral_constant<int, 1>{});
+    return packed_v ? with_v(w, std::integral_constant<int, M>{})
+                    : with_v(w, std::integral_constant<int, 1>{});
   };
-  if (width == kNarrow) with_w(std::integral_constant<int, kNarrow>{});
-  else with_w(std::integral_constant<int, kWide>{});
-  SLA_HIP(hipGetLastError());
-  return SLA_OK;
+  return width == kNarrow ? with_w(std::integral_constant<int, kNarrow>{})
+                          : with_w(std::integral_constant<int, kWide>{});
 }
 
 sla_status check_work(const sla_linrec_shape& q, const void* work, size_t bytes) {
@@ -1309,11 +1326,10 @@ sla_status sla_linrec_forward(const sla_linrec_shape* shape, const void* d_x,
     p.saved = (C*)d_saved;
     if (q.steps <= kFew) {
       const int64_t n = q.n_seq * (q.dim / (wide ? M : 1));
-      const dim3 grid((unsigned)((n + kWG - 1) / kWG));
-      if (wide) few_forward<T, GATE, M><<<grid, kWG, 0, s>>>(p);
-      else few_forward<T, GATE, 1><<<grid, kWG, 0, s>>>(p);
-      SLA_HIP(hipGetLastError());
-      return SLA_OK;
+      return in_launches(p, (n + kWG - 1) / kWG, [&](dim3 grid) {
+        if (wide) few_forward<T, GATE, M><<<grid, kWG, 0, s>>>(p);
+        else few_forward<T, GATE, 1><<<grid, kWG, 0, s>>>(p);
+      });
     }
     return run_chunks<M>(q, p, wide, d_work, false, s, [&](auto w, auto v, auto chain, dim3 grid) {
       constexpr int W = decltype(w)::value, V = decltype(v)::value;
