@@ -15,6 +15,7 @@
 // below a million elements the launch (60000 in 24 tensors: 3.4 us).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -402,9 +403,9 @@ __global__ __launch_bounds__(kWG) void adamw_step(Step q, Grads grads) {
 
 // The values of 8-bit states: four significant bits, which bf16 holds.
 // Bound by its 6 bytes an element: 60M in 63 us, 5.7 TB/s.
-__global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blocks, bf16_t* m,
-                                                   bf16_t* v) {
-  const int64_t blk = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+__global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blk0, int64_t blocks,
+                                                   bf16_t* m, bf16_t* v) {
+  const int64_t blk = blk0 + (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (blk >= blocks) return;
   const int64_t at = blk * kBlock + kPerLane * (threadIdx.x & 63);
   const auto cm = *(const Pack<uint8_t, 4>*)(st.m8 + at);
@@ -422,9 +423,9 @@ __global__ __launch_bounds__(kWG) void adamw_read8(State st, int64_t blocks, bf1
 
 // States from values, to the nearest level (10 bytes an element: 60M in
 // 115 us on a first call).
-__global__ __launch_bounds__(kWG) void adamw_write8(State st, int64_t blocks, const float* m,
-                                                    const float* v) {
-  const int64_t blk = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+__global__ __launch_bounds__(kWG) void adamw_write8(State st, int64_t blk0, int64_t blocks,
+                                                    const float* m, const float* v) {
+  const int64_t blk = blk0 + (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (blk >= blocks) return;
   const int lane = threadIdx.x & 63;
   const int64_t at = blk * kBlock + kPerLane * lane;
@@ -446,10 +447,12 @@ __global__ __launch_bounds__(kWG) void adamw_write8(State st, int64_t blocks, co
   if (lane == 0) st.mbase[blk] = (uint16_t)bm, st.vbase[blk] = (uint16_t)bv;
 }
 
-// Plain copies between the 32-bit states and the caller's arrays.
-__global__ __launch_bounds__(kWG) void copy4(const float* a, float* b, int64_t quads) {
-  const int64_t i = (int64_t)blockIdx.x * kWG + threadIdx.x;
-  if (i < quads) ((Pack<float, 4>*)b)[i] = ((const Pack<float, 4>*)a)[i];
+// Plain copies between the 32-bit states and the caller's arrays: a lane copies
+// as much of a block as it steps.
+__global__ __launch_bounds__(kWG) void copy4(const float* a, float* b, int64_t blk0,
+                                             int64_t blocks) {
+  const int64_t i = blk0 * 64 + (int64_t)blockIdx.x * kWG + threadIdx.x;
+  if (i < blocks * 64) ((Pack<float, 4>*)b)[i] = ((const Pack<float, 4>*)a)[i];
 }
 
 sla_status refuse(const char* msg) {
@@ -509,8 +512,21 @@ sla_status check_tensors(const sla_adamw_tensor* ts, int32_t n, int32_t bits, Si
   return SLA_OK;
 }
 
+// A launch has less than 2^32 threads.
+constexpr int64_t kMostGroups = (((int64_t)1 << 32) - 1) / kWG;
+// Calls launch(first block, grid) for all blocks, one a wave.
+template <typename F>
+sla_status in_launches(int64_t blocks, F&& launch) {
+  for (int64_t at = 0; at < blocks; at += kMostGroups * kWaves) {
+    const int64_t groups = (blocks - at + kWaves - 1) / kWaves;
+    launch(at, dim3((unsigned)std::min(groups, kMostGroups)));
+    SLA_HIP(hipGetLastError());
+  }
+  return SLA_OK;
+}
+
 // One launch of a kind: a range of its tensors (kGrads at most) and of its
-// chunks.
+// chunks (kMostGroups at most).
 struct Launch {
   int kind;
   int32_t tensor0, tensors;
@@ -559,15 +575,18 @@ sla_status build(sla_adamw* o, const sla_adamw_tensor* ts, void* d_state, void* 
       if (kind_of(ts[i]) != kind || ts[i].numel == 0) continue;
       const int32_t pos = (int32_t)o->order.size(), local = pos - o->kind0[kind];
       if (local % kGrads == 0) o->launches.push_back({kind, local, 0, nc, 0});
-      Launch& l = o->launches.back();
       o->order.push_back(i);
       o->align.push_back(dtype_bytes(ts[i].grad_dtype));
       ht[pos] = {ts[i].d_param, ts[i].d_copy, ts[i].numel, block0[i]};
       const int64_t nb = (ts[i].numel + kBlock - 1) / kBlock;
-      for (int64_t b = 0; b < nb; b += kChunkBlocks)
+      for (int64_t b = 0; b < nb; b += kChunkBlocks) {
+        if (o->launches.back().chunks == kMostGroups)
+          o->launches.push_back({kind, local, 0, nc, 0});
+        Launch& l = o->launches.back();
         hc[nc++] = {local, (int32_t)(b / kChunkBlocks)};
-      l.tensors = local - l.tensor0 + 1;
-      l.chunks = nc - l.chunk0;
+        l.tensors = local - l.tensor0 + 1;
+        ++l.chunks;
+      }
     }
   }
   o->d_tensors = (const Tensor*)d_table;
@@ -707,17 +726,14 @@ sla_status sla_adamw_get_state(sla_adamw_t opt, void* d_m, void* d_v, void* stre
   if (!d_m || !d_v || d_m == d_v) return refuse("m and v must be distinct non-NULL arrays");
   if (!aligned(d_m, 16) || !aligned(d_v, 16)) return refuse("m and v must be 16-byte aligned");
   hipStream_t s = (hipStream_t)stream;
-  if (opt->bits == 32) {
-    const int64_t quads = opt->blocks * (kBlock / 4);
-    const dim3 grid((unsigned)((quads + kWG - 1) / kWG));
-    copy4<<<grid, kWG, 0, s>>>(opt->st.m32, (float*)d_m, quads);
-    copy4<<<grid, kWG, 0, s>>>(opt->st.v32, (float*)d_v, quads);
-  } else {
-    adamw_read8<<<dim3((unsigned)((opt->blocks + kWaves - 1) / kWaves)), kWG, 0, s>>>(
-        opt->st, opt->blocks, (bf16_t*)d_m, (bf16_t*)d_v);
-  }
-  SLA_HIP(hipGetLastError());
-  return SLA_OK;
+  return in_launches(opt->blocks, [&](int64_t blk0, dim3 grid) {
+    if (opt->bits == 32) {
+      copy4<<<grid, kWG, 0, s>>>(opt->st.m32, (float*)d_m, blk0, opt->blocks);
+      copy4<<<grid, kWG, 0, s>>>(opt->st.v32, (float*)d_v, blk0, opt->blocks);
+    } else {
+      adamw_read8<<<grid, kWG, 0, s>>>(opt->st, blk0, opt->blocks, (bf16_t*)d_m, (bf16_t*)d_v);
+    }
+  });
 }
 
 sla_status sla_adamw_set_state(sla_adamw_t opt, const float* d_m, const float* d_v,
@@ -727,17 +743,14 @@ sla_status sla_adamw_set_state(sla_adamw_t opt, const float* d_m, const float* d
   if (!d_m || !d_v) return refuse("m and v must be non-NULL arrays");
   if (!aligned(d_m, 16) || !aligned(d_v, 16)) return refuse("m and v must be 16-byte aligned");
   hipStream_t s = (hipStream_t)stream;
-  if (opt->bits == 32) {
-    const int64_t quads = opt->blocks * (kBlock / 4);
-    const dim3 grid((unsigned)((quads + kWG - 1) / kWG));
-    copy4<<<grid, kWG, 0, s>>>(d_m, opt->st.m32, quads);
-    copy4<<<grid, kWG, 0, s>>>(d_v, opt->st.v32, quads);
-  } else {
-    adamw_write8<<<dim3((unsigned)((opt->blocks + kWaves - 1) / kWaves)), kWG, 0, s>>>(
-        opt->st, opt->blocks, d_m, d_v);
-  }
-  SLA_HIP(hipGetLastError());
-  return SLA_OK;
+  return in_launches(opt->blocks, [&](int64_t blk0, dim3 grid) {
+    if (opt->bits == 32) {
+      copy4<<<grid, kWG, 0, s>>>(d_m, opt->st.m32, blk0, opt->blocks);
+      copy4<<<grid, kWG, 0, s>>>(d_v, opt->st.v32, blk0, opt->blocks);
+    } else {
+      adamw_write8<<<grid, kWG, 0, s>>>(opt->st, blk0, opt->blocks, d_m, d_v);
+    }
+  });
 }
 
 }  // extern "C"

@@ -1,4 +1,6 @@
-"""Recurrences that need more threads than one launch has (2^32 - 1)."""
+"""Recurrences and AdamW steps that need more threads than one launch has
+(2^32 - 1), and element places beyond 2^32."""
+import numpy as np
 import pytest
 import torch
 
@@ -79,3 +81,49 @@ def test_serving_step_of_more_channels_than_threads():
     one, state, _ = B.sla_linrec_forward(x, g)
     for at in (slice(0, 3), slice(n - 3, n)):
         assert torch.equal(h[at], one.expand(3, 1, d)) and torch.equal(last[at], state.expand(3, d))
+
+
+def test_adamw_of_more_blocks_than_threads():
+    """17.5e9 bf16 parameters with 8-bit states, one gradient for all five
+    tensors: the step and the reading of the states at the first elements, at the
+    first of the second launch and at the last, bit for bit; the setting at all."""
+    room(220)
+    size, k = 3_500_000_007, 5
+    say("adamw, elements", size * k)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    g = torch.empty(size, dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    ps = [torch.ones(size, dtype=torch.bfloat16, device=DEV) for _ in range(k)]
+    opt = B.sla_adamw_create(ps, state_bits=8)
+    B.sla_adamw_step(opt, [g] * k, step=1, seed=6, lr=1e-2)
+    m, v = B.sla_adamw_get_state(opt)
+    torch.cuda.synchronize()
+    second = (2 ** 24 - 1) * 1024  # elements of the first launch's chunks of four blocks
+    for at in (0, second - 512, opt.starts[1] + 5120, opt.starts[4] + size // 256 * 256 - 512):
+        t = max(i for i in range(k) if opt.starts[i] <= at)
+        i = at - opt.starts[t]
+        n = min(1024, size - i)
+        gr = S.pad_to_blocks([g[i:i + n].float().cpu().numpy()])
+        key = int(S.mix(6 ^ int(S.mix(int(S.mix(1))))))
+        e = at + np.arange(len(gr), dtype=np.uint64)
+        hi = e >> np.uint64(32)
+        keys = np.where(hi > 0, np.uint64(key) ^ S.mix(hi), np.uint64(key))
+        r = S.mix((e & np.uint64(0xFFFFFFFF)) * np.uint64(0x9E3779B1) + keys)
+        wm, wv = S.moments32(np.zeros_like(gr), np.zeros_like(gr), gr, 0.9, 0.999)
+        wm = S.levels(wm, ((r & np.uint64(0xFFFF)) << np.uint64(4)) + np.uint64(8), 126, 0)
+        wv = S.levels(wv, ((r >> np.uint64(16)) << np.uint64(4)) + np.uint64(8), 254, 1)
+        assert np.array_equal(m[at:at + n].float().cpu().numpy(), wm[:n]), at
+        assert np.array_equal(v[at:at + n].float().cpu().numpy(), wv[:n]), at
+        # the first step moves each parameter by lr against its gradient's sign
+        # (and by lr wd = 1e-4), to a bf16 neighbour: 2^-7 either way
+        p = ps[t][i:i + n].float().cpu().numpy()
+        want = 1 - 1e-2 * np.sign(gr[:n]) - 1e-4
+        assert np.all(np.abs(p - want) <= 2.0 ** -7), at
+    del m, v, g
+    # ones, in the highest codes of their blocks, throughout
+    ones = torch.ones(opt.padded, device=DEV)
+    B.sla_adamw_set_state(opt, ones, ones)
+    n = opt.padded
+    assert bool((opt.state[:n] == 126).all()) and bool((opt.state[n:2 * n] == 254).all())
+    bases = opt.state[2 * n:].view(torch.int16)
+    assert bool((bases[:n // 256] == 1016 - 126).all())
+    assert bool((bases[n // 256:] == 1016 - 254).all())
