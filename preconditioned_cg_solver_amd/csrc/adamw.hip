@@ -195,9 +195,9 @@ struct Types<K_F64> {
 // rate m / (root sqrt(v) + eps), by the hardware's root and reciprocal (each
 // within a unit in the last place; the full-precision sequences would make
 // the 8-bit step wait for its arithmetic).  They take no subnormal numbers:
-// v counts as 2^-126 at least.
+// v counts as 2^-126 at least, unless it is NaN (the maximum that keeps those).
 __device__ __forceinline__ float update(const Step& q, float m, float v) {
-  const float s = __builtin_amdgcn_sqrtf(fmaxf(v, 0x1p-126f));
+  const float s = __builtin_amdgcn_sqrtf(__builtin_elementwise_maximum(v, 0x1p-126f));
   return m * __builtin_amdgcn_rcpf(s * q.root + q.eps) * q.rate;
 }
 
