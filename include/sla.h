@@ -556,13 +556,15 @@ sla_status sla_adamw_destroy(sla_adamw_t opt);
 /*
  * One step.  h_grads[i] (host array of device pointers) is the gradient of
  * tensor i, contiguous, in its grad_dtype; NULL leaves tensor i and its
- * states as they are.  d_grad_scale (may be NULL) is a device fp32 number
- * that multiplies every gradient; if it is not finite the step changes
- * nothing.  Asynchronous on `stream`; allocates nothing and copies nothing,
- * so it can be captured in a HIP graph (the gradients' addresses and the
- * step number are then fixed).  SLA_ERR_INVALID_ARG on NULL arguments,
- * misaligned gradients, lr or weight_decay or eps negative or not finite,
- * betas outside [0, 1), step < 1.
+ * states as they are.  Of tensors that share memory (tied weights given twice,
+ * or copies) one at most can have a gradient.  Gradients must not overlap what
+ * the step writes.  d_grad_scale (may be NULL) is a device fp32 number that
+ * multiplies every gradient; if it is not finite the step changes nothing.
+ * Asynchronous on `stream`; allocates nothing and copies nothing, so it can be
+ * captured in a HIP graph (the gradients' addresses and the step number are
+ * then fixed).  SLA_ERR_INVALID_ARG on NULL arguments, misaligned gradients,
+ * gradients of tensors that share memory, lr or weight_decay or eps negative or
+ * not finite, betas outside [0, 1), step < 1.
  */
 sla_status sla_adamw_step(sla_adamw_t opt, const void *const *h_grads,
                           const sla_adamw_hyper *hyper, const float *d_grad_scale, void *stream);

@@ -899,7 +899,8 @@ def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
                    beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
                    grad_scale: Optional[torch.Tensor] = None, seed: int = 0, stream=None) -> None:
     """One step (number `step`, from 1) of every parameter from its gradient
-    (None leaves a parameter and its states alone).  grad_scale: a float32
+    (None leaves a parameter and its states alone; of parameters that share
+    memory, tied weights given twice, one at most can have one).  grad_scale: a float32
     device number that multiplies the gradients; one that is not finite makes
     the step change nothing.  seed: of the stochastic rounding."""
     if len(grads) != len(opt.params):

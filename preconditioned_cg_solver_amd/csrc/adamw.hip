@@ -533,6 +533,41 @@ struct Launch {
   int64_t chunk0, chunks;
 };
 
+// Memory that a step writes for a tensor.
+struct Span {
+  uintptr_t begin, end;
+  int32_t tensor;
+};
+// Whether two of the spans that `used` takes overlap; they are sorted by begin.
+template <typename F>
+bool overlap(const std::vector<Span>& spans, F&& used) {
+  uintptr_t end = 0;
+  for (const Span& s : spans) {
+    if (!used(s.tensor)) continue;
+    if (s.begin < end) return true;
+    end = std::max(end, s.end);
+  }
+  return false;
+}
+// The spans that overlap another one, sorted.
+std::vector<Span> shared_spans(const sla_adamw_tensor* ts, int32_t n) {
+  std::vector<Span> all, some;
+  for (int32_t i = 0; i < n; ++i) {
+    if (ts[i].numel == 0) continue;
+    const uintptr_t p = (uintptr_t)ts[i].d_param, c = (uintptr_t)ts[i].d_copy;
+    all.push_back({p, p + ts[i].numel * dtype_bytes(ts[i].dtype), i});
+    if (c) all.push_back({c, c + ts[i].numel * dtype_bytes(SLA_BF16), i});
+  }
+  std::sort(all.begin(), all.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t end = 0;  // of those before
+  for (size_t k = 0; k < all.size(); ++k) {
+    if (all[k].begin < end || (k + 1 < all.size() && all[k + 1].begin < all[k].end))
+      some.push_back(all[k]);
+    end = std::max(end, all[k].end);
+  }
+  return some;
+}
+
 }  // namespace
 }  // namespace sla
 
@@ -547,6 +582,7 @@ struct sla_adamw {
   std::vector<int32_t> order;              // caller's index of each
   std::vector<size_t> align;               // of its gradient
   std::vector<sla::Launch> launches;
+  std::vector<sla::Span> shared;           // of tensors that share memory
 };
 
 namespace sla {
@@ -567,6 +603,7 @@ sla_status build(sla_adamw* o, const sla_adamw_tensor* ts, void* d_state, void* 
                                      (o->bits == 32 ? 16 : 4));
   }
   o->blocks = blocks;
+  o->shared = shared_spans(ts, o->n);
   o->streams = bytes > kCacheBytes;
   int64_t nc = 0;
   for (int kind = 0; kind < K_KINDS; ++kind) {
@@ -690,6 +727,8 @@ sla_status sla_adamw_step(sla_adamw_t opt, const void* const* h_grads,
   for (size_t k = 0; k < opt->order.size(); ++k)
     if (!aligned(h_grads[opt->order[k]], opt->align[k]))
       return refuse("a gradient is not aligned to its elements");
+  if (overlap(opt->shared, [&](int32_t i) { return h_grads[i] != nullptr; }))
+    return refuse("tensors that share memory have gradients in the same step");
   TraceRange tr("sla_adamw_step");
   Step q{};
   q.st = opt->st;

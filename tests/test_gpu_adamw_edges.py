@@ -32,3 +32,49 @@ def test_a_second_moment_that_is_not_a_number(dtype, bits):
     assert torch.equal(torch.isnan(p), bad) and torch.equal(p[~bad], q[~bad])
     vs = B.sla_adamw_get_state(a)[1][:n]
     assert not bool(torch.isfinite(vs[bad]).any())
+
+
+def test_tensors_that_share_memory():
+    """Two entries with the same memory are not stepped at once, whether whole,
+    in part or through a copy; one of them alone is, as are neighbours."""
+    say("adamw shared memory")
+    flat = torch.ones(4000, device=DEV)
+    low = torch.zeros(4000, device=DEV, dtype=torch.bfloat16)
+    g = torch.full((1000,), 0.5, device=DEV)
+
+    def step(spans, grads, copies=None):
+        opt = B.sla_adamw_create([flat[a:a + 1000] for a in spans],
+                                 copies=None if copies is None else
+                                 [None if c is None else low[c:c + 1000] for c in copies])
+        B.sla_adamw_step(opt, [g if k else None for k in grads], step=1, lr=1e-3)
+
+    for spans, grads, copies in (([0, 0], (1, 1), None), ([0, 2000, 999], (1, 1, 1), None),
+                                 ([1500, 0, 3000, 2499], (1, 1, 0, 1), None),
+                                 ([0, 1000], (1, 1), [0, 999]),
+                                 ([0, 1000, 2000], (1, 0, 1), [500, None, 0])):
+        before = flat.clone()
+        with pytest.raises(B.SlaError, match="share memory"):
+            step(spans, grads, copies)
+        assert torch.equal(flat, before) and not bool(low.any())
+    for spans, grads, copies in (([0, 0], (1, 0), None), ([0, 2000, 999], (0, 1, 1), None),
+                                 ([500, 0, 1000], (0, 1, 1), None), ([3000, 0, 1000], (1, 1, 1), None),
+                                 ([0, 1000], (1, 1), [1000, 0]), ([0, 1000], (1, 0), [0, 999])):
+        before = flat.clone()
+        step(spans, grads, copies)
+        moved = torch.zeros_like(flat, dtype=torch.bool)
+        for a, k in zip(spans, grads):
+            moved[a:a + 1000] |= bool(k)
+        assert torch.equal(flat != before, moved), (spans, grads)
+
+
+def test_many_tensors_with_the_same_memory():
+    """Three entries of one weight; each may be the one that is stepped."""
+    say("adamw tied three times")
+    w, g = torch.ones(300, device=DEV), torch.ones(300, device=DEV)
+    opt = B.sla_adamw_create([w, torch.ones(5, device=DEV), w, w])
+    for k in (0, 2, 3):
+        grads = [None, torch.ones(5, device=DEV), None, None]
+        grads[k] = g
+        before = w.clone()
+        B.sla_adamw_step(opt, grads, step=1, lr=1e-2)
+        assert bool((w < before).all())
