@@ -672,6 +672,11 @@ def _enter(dev: torch.device, stream):
 _SAME_STREAM = contextlib.nullcontext()
 
 
+# Tells autograd that tensors were written, so that a backward pass that has
+# saved one raises instead of using its new values.
+_written = torch.autograd.graph.increment_version
+
+
 def _raw(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -758,6 +763,7 @@ def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.T
     n_saved, n_work = _linrec_sizes(q)
     with ctx:
         h = _like(x)
+        given = h_last
         if h_last is None:
             h_last = _like(h0) if h0 is not None else \
                 torch.empty((q.n_seq, q.dim), dtype=sdt, device=dev)
@@ -766,6 +772,8 @@ def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.T
         work = torch.empty(n_work, dtype=torch.uint8, device=dev) if n_work else None
     _check(lib().sla_linrec_forward(ctypes.byref(q), *px, *pg, p0, _raw(h), pl, _raw(saved),
                                     _raw(work), n_work, raw))
+    if given is not None:
+        _written(given)
     return h, h_last, saved
 
 
@@ -812,6 +820,7 @@ class Adamw:
             at += -(-p.numel() // 256) * 256
         self._want = [(p.numel(), dt) for p, dt in zip(params, grad_dtypes)]
         self._ptrs = (ctypes.c_void_p * max(len(params), 1))()
+        self._writes = [state, *params, *(c for c in copies if c is not None)]
 
     @property
     def device(self):
@@ -905,22 +914,28 @@ def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
     the step change nothing.  seed: of the stochastic rounding."""
     if len(grads) != len(opt.params):
         raise ValueError(f"{len(grads)} gradients for {len(opt.params)} parameters")
-    dev, ptrs = opt.device, opt._ptrs
-    on = dev.index
-    for i, (g, (n, dt)) in enumerate(zip(grads, opt._want)):
+    dev, ptrs, writes, missing = opt.device, opt._ptrs, opt._writes, False
+    on, at = dev.index, []
+    for g, (n, dt) in zip(grads, opt._want):
         if g is None:
-            ptrs[i] = None
+            at.append(None)
+            missing = True
             continue
         if g.dtype is not dt or g.numel() != n or g.get_device() != on or not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be a contiguous {dt} tensor of {n} elements "
-                             f"on {dev}")
-        ptrs[i] = g.data_ptr()
+            raise ValueError(f"gradient {len(at)} must be a contiguous {dt} tensor of {n} "
+                             f"elements on {dev}")
+        at.append(g.data_ptr())
+    ptrs[:len(at)] = at
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                    or grad_scale.device != dev):
         raise ValueError("grad_scale must be one float32 number on the parameters' device")
     hyper = AdamwHyper(lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFFFFFFFFFF)
     raw, _ = _enter(dev, stream)
     _check(lib().sla_adamw_step(opt.handle, ptrs, ctypes.byref(hyper), _raw(grad_scale), raw))
+    if missing:
+        own = [t for g, *t in zip(grads, opt.params, opt.copies) if g is not None]
+        writes = [opt.state, *(t for ts in own for t in ts if t is not None)]
+    _written(writes)
 
 
 def sla_adamw_get_state(opt: Adamw, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -947,3 +962,4 @@ def sla_adamw_set_state(opt: Adamw, m: torch.Tensor, v: torch.Tensor, stream=Non
                              f"elements on {opt.device}")
     raw, _ = _enter(opt.device, stream)
     _check(lib().sla_adamw_set_state(opt.handle, _raw(m), _raw(v), raw))
+    _written(opt.state)

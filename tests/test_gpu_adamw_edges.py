@@ -78,3 +78,58 @@ def test_many_tensors_with_the_same_memory():
         before = w.clone()
         B.sla_adamw_step(opt, grads, step=1, lr=1e-2)
         assert bool((w < before).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_between_forward_and_backward_is_noticed(bits):
+    """What autograd has saved and a step has written since is an error in the
+    backward pass; what the step left alone is not."""
+    say("adamw and autograd", bits)
+    w, u, x = (torch.rand(300, device=DEV, requires_grad=True) for _ in range(3))
+    low = torch.zeros(300, device=DEV, dtype=torch.bfloat16)
+    opt = B.sla_adamw_create([w, u], state_bits=bits, copies=[low, None])
+    g = torch.ones(300, device=DEV)
+    for used, grads, fails in ((w, [g, None], True), (w, [g, g], True), (w, [None, g], False),
+                               (u, [g, None], False), (low, [g, None], True),
+                               (low, [None, g], False)):
+        loss = (x * used).sum()
+        B.sla_adamw_step(opt, grads, step=1, lr=1e-3)
+        if fails:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+        else:
+            loss.backward()
+    m, _ = B.sla_adamw_get_state(opt)
+    if bits == 32:  # the handle's own buffer
+        for write in (lambda: B.sla_adamw_step(opt, [g, g], step=2, lr=1e-3),
+                      lambda: B.sla_adamw_set_state(opt, torch.zeros_like(m), torch.zeros_like(m))):
+            loss = (x * m[:300]).sum()
+            write()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+
+
+def test_a_last_state_that_autograd_has_saved():
+    say("recurrence and autograd: h_last given")
+    x, g = (torch.randn(2, 5, 8, device=DEV) for _ in range(2))
+    scale = torch.rand(2, 8, device=DEV, requires_grad=True)
+    state = torch.rand(2, 8, device=DEV)
+    loss = (scale * state).sum()
+    B.sla_linrec_forward(x, g, h0=state, h_last=state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_in_inference_mode():
+    """Tensors without versions are written all the same."""
+    say("operators in inference mode")
+    with torch.inference_mode():
+        x, g = (torch.randn(2, 5, 8, device=DEV) for _ in range(2))
+        state = torch.rand(2, 8, device=DEV)
+        _, want, _ = B.sla_linrec_forward(x, g, h0=state)
+        B.sla_linrec_forward(x, g, h0=state, h_last=state)
+        assert torch.equal(state, want)
+        p = torch.ones(300, device=DEV)
+        opt = B.sla_adamw_create([p])
+        B.sla_adamw_step(opt, [torch.ones(300, device=DEV)], step=1, lr=1e-2)
+        assert bool((p < 1).all())
