@@ -72,6 +72,8 @@ def lib_path() -> str:
 def lib():
     """Load the library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = lib_path()
@@ -654,22 +656,34 @@ def _device_of(named) -> torch.device:
 
 
 def _enter(dev: torch.device, stream):
-    """(raw stream, context in which to allocate): results and scratch belong
-    to the stream that the kernels run on.  Kernels are launched on the
-    current device, which has to be the tensors'."""
+    """(raw stream, context in which to allocate, stream on which to record what
+    the call uses): results and scratch belong to the stream that the kernels run
+    on.  Kernels are launched on the current device, which has to be the tensors'.
+
+    Tensors that are used on a given torch.cuda.Stream are recorded on it, so
+    that their memory is not reused before the call's work is done.  A stream
+    given by its raw pointer (or as ExternalStream) may not live that long: there
+    the caller keeps the tensors until then."""
     if dev.index is not None and dev.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
         # current_stream() would make an object of it: 2.5 us of a serving step's 17
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _SAME_STREAM
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _SAME_STREAM, None
     if not hasattr(stream, "cuda_stream"):
         raw = stream.value if isinstance(stream, ctypes.c_void_p) else stream
         stream = torch.cuda.ExternalStream(raw or 0, device=dev)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    lasts = not isinstance(stream, torch.cuda.ExternalStream)
+    return stream.cuda_stream, torch.cuda.stream(stream), stream if lasts else None
 
 
 _SAME_STREAM = contextlib.nullcontext()
+
+
+def _record(stream, *tensors):
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 # Tells autograd that tensors were written, so that a backward pass that has
@@ -752,6 +766,8 @@ def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.T
     sequences begins; slices of a wider tensor and expanded ones are taken as
     they are.  h0 and h_last: (sequences, channels) float32 (float64 for
     float64); h_last may be given, h0 itself included, to be overwritten.
+    `stream` (a torch stream or a raw pointer) has to be ordered after what made
+    the inputs; given as a raw pointer, the caller keeps them until it is done.
     Returns (h, h_last, saved); `saved` (None unless save) is what the
     backward pass needs."""
     q, sdt = _linrec_shape(x, gate, offsets, mode)
@@ -759,7 +775,7 @@ def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.T
     p0, pl = _states(h0, "h0", q, sdt), _states(h_last, "h_last", q, sdt)
     dev = _device_of((("x", x), ("gate", gate), ("h0", h0), ("offsets", offsets),
                       ("h_last", h_last)))
-    raw, ctx = _enter(dev, stream)
+    raw, ctx, used = _enter(dev, stream)
     n_saved, n_work = _linrec_sizes(q)
     with ctx:
         h = _like(x)
@@ -772,6 +788,8 @@ def sla_linrec_forward(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.T
         work = torch.empty(n_work, dtype=torch.uint8, device=dev) if n_work else None
     _check(lib().sla_linrec_forward(ctypes.byref(q), *px, *pg, p0, _raw(h), pl, _raw(saved),
                                     _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, x, gate, h0, offsets, given)
     if given is not None:
         _written(given)
     return h, h_last, saved
@@ -784,7 +802,8 @@ def sla_linrec_backward(x: torch.Tensor, gate: torch.Tensor, saved: torch.Tensor
                         offsets: Optional[torch.Tensor] = None, mode: str = "sigmoid",
                         stream=None):
     """Gradients (of x, of gate, of h0 or None) from those of h and h_last
-    (None: zero); the other arguments are the forward call's."""
+    (None: zero); the other arguments are the forward call's, and `stream` is
+    taken as there."""
     q, sdt = _linrec_shape(x, gate, offsets, mode)
     px, pg = _steps_in(x, "x", x), _steps_in(gate, "gate", x)
     pd = _steps_in(grad_h, "grad_h", x)
@@ -795,13 +814,15 @@ def sla_linrec_backward(x: torch.Tensor, gate: torch.Tensor, saved: torch.Tensor
     if saved.dtype != sdt or not saved.is_contiguous() or \
             saved.numel() * sdt.itemsize != n_saved:
         raise ValueError("saved must be the forward call's")
-    raw, ctx = _enter(dev, stream)
+    raw, ctx, used = _enter(dev, stream)
     with ctx:
         dx, dg = _like(x), _like(x)
         dh0 = _like(h0) if h0 is not None else None
         work = torch.empty(n_work, dtype=torch.uint8, device=dev) if n_work else None
     _check(lib().sla_linrec_backward(ctypes.byref(q), *px, *pg, p0, _raw(saved), *pd, pl,
                                      _raw(dx), _raw(dg), _raw(dh0), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, x, gate, saved, grad_h, grad_last, h0, offsets)
     return dx, dg, dh0
 
 
@@ -820,11 +841,21 @@ class Adamw:
             at += -(-p.numel() // 256) * 256
         self._want = [(p.numel(), dt) for p, dt in zip(params, grad_dtypes)]
         self._ptrs = (ctypes.c_void_p * max(len(params), 1))()
+        self._streams = set()  # on which what the handle holds is known to be used
         self._writes = [state, *params, *(c for c in copies if c is not None)]
 
     @property
     def device(self):
         return self.state.device
+
+    def _use(self, raw, used, stream):
+        """Record what the handle holds on a stream that is not in _streams yet."""
+        if stream is None:
+            used = torch.cuda.current_stream()
+            used = None if isinstance(used, torch.cuda.ExternalStream) else used
+        if used is not None:
+            _record(used, *self._writes, self._table)
+            self._streams.add(raw)
 
     def views(self, flat: torch.Tensor):
         """The parts of a padded array that belong to each parameter, in its shape."""
@@ -890,14 +921,17 @@ def sla_adamw_create(params, state_bits: int = 32, grad_dtype=None, copies=None,
     dev = _device_of([("a parameter", p) for p in params] + [("a copy", c) for c in copies])
     if dev is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    raw, ctx = _enter(dev, stream)
+    raw, ctx, _ = _enter(dev, stream)
     with ctx:
         state = torch.zeros(sb, dtype=torch.uint8, device=dev)
         table = torch.empty(tb, dtype=torch.uint8, device=dev)
     h = ctypes.c_void_p()
     _check(lib().sla_adamw_create(ctypes.byref(h), ts, len(params), int(state_bits), _raw(state),
                                   sb, _raw(table), tb, raw))
-    return Adamw(h, params, copies, gd, int(state_bits), state, table, padded)
+    opt = Adamw(h, params, copies, gd, int(state_bits), state, table, padded)
+    if stream is None:
+        opt._streams.add(raw)
+    return opt
 
 
 def sla_adamw_destroy(opt: Adamw) -> None:
@@ -911,7 +945,8 @@ def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
     (None leaves a parameter and its states alone; of parameters that share
     memory, tied weights given twice, one at most can have one).  grad_scale: a float32
     device number that multiplies the gradients; one that is not finite makes
-    the step change nothing.  seed: of the stochastic rounding."""
+    the step change nothing.  seed: of the stochastic rounding.  stream: as in
+    sla_linrec_forward; the handle, too, is kept until a raw stream is done."""
     if len(grads) != len(opt.params):
         raise ValueError(f"{len(grads)} gradients for {len(opt.params)} parameters")
     dev, ptrs, writes, missing = opt.device, opt._ptrs, opt._writes, False
@@ -930,8 +965,12 @@ def sla_adamw_step(opt: Adamw, grads, step: int, lr: float, beta1: float = 0.9,
                                    or grad_scale.device != dev):
         raise ValueError("grad_scale must be one float32 number on the parameters' device")
     hyper = AdamwHyper(lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFFFFFFFFFF)
-    raw, _ = _enter(dev, stream)
+    raw, _, used = _enter(dev, stream)
     _check(lib().sla_adamw_step(opt.handle, ptrs, ctypes.byref(hyper), _raw(grad_scale), raw))
+    if raw not in opt._streams:
+        opt._use(raw, used, stream)
+    if used is not None:
+        _record(used, *grads, grad_scale)
     if missing:
         own = [t for g, *t in zip(grads, opt.params, opt.copies) if g is not None]
         writes = [opt.state, *(t for ts in own for t in ts if t is not None)]
@@ -944,11 +983,13 @@ def sla_adamw_get_state(opt: Adamw, stream=None) -> Tuple[torch.Tensor, torch.Te
     if opt.state_bits == 32:
         f = opt.state.view(torch.float32)
         return f[:opt.padded], f[opt.padded:]
-    raw, ctx = _enter(opt.device, stream)
+    raw, ctx, used = _enter(opt.device, stream)
     with ctx:
         m = torch.empty(opt.padded, dtype=torch.bfloat16, device=opt.device)
         v = torch.empty(opt.padded, dtype=torch.bfloat16, device=opt.device)
     _check(lib().sla_adamw_get_state(opt.handle, _raw(m), _raw(v), raw))
+    if raw not in opt._streams:
+        opt._use(raw, used, stream)
     return m, v
 
 
@@ -960,6 +1001,10 @@ def sla_adamw_set_state(opt: Adamw, m: torch.Tensor, v: torch.Tensor, stream=Non
                 or t.device != opt.device:
             raise ValueError(f"{name} must be a contiguous float32 tensor of {opt.padded} "
                              f"elements on {opt.device}")
-    raw, _ = _enter(opt.device, stream)
+    raw, _, used = _enter(opt.device, stream)
     _check(lib().sla_adamw_set_state(opt.handle, _raw(m), _raw(v), raw))
+    if raw not in opt._streams:
+        opt._use(raw, used, stream)
+    if used is not None:
+        _record(used, m, v)
     _written(opt.state)

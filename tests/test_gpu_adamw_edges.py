@@ -133,3 +133,88 @@ def test_in_inference_mode():
         opt = B.sla_adamw_create([p])
         B.sla_adamw_step(opt, [torch.ones(300, device=DEV)], step=1, lr=1e-2)
         assert bool((p < 1).all())
+
+
+def busy(stream):
+    """Work of some milliseconds on the stream."""
+    with torch.cuda.stream(stream):
+        big = torch.ones(1 << 27, device=DEV)
+        for _ in range(30):
+            big.mul_(1.0)
+
+
+def test_inputs_freed_while_another_stream_reads_them():
+    """Memory of inputs given up right after a call on another stream is not
+    handed out again before that call has read it."""
+    say("operators on another stream, inputs freed")
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    shape = (4, 700, 64)
+    base = [torch.randn(shape, device=DEV, generator=gen) for _ in range(3)]
+    h0 = torch.randn(4, 64, device=DEV, generator=gen)
+    off = torch.tensor([0, 700, 1400, 2100, 2800], device=DEV)
+    flat = [t.view(2800, 64) for t in base]
+    h, last, saved = B.sla_linrec_forward(flat[0], flat[1], h0=h0, offsets=off, save=True)
+    want = [h, last, *B.sla_linrec_backward(flat[0], flat[1], saved, flat[2], grad_last=h0, h0=h0,
+                                            offsets=off)]
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        x, g, d = (t.clone() for t in flat)
+        state, offsets = h0.clone(), off.clone()
+        torch.cuda.synchronize()
+        busy(s)
+        h, last, saved = B.sla_linrec_forward(x, g, h0=state, offsets=offsets, save=True, stream=s)
+        got = [h, last, *B.sla_linrec_backward(x, g, saved, d, grad_last=state, h0=state,
+                                               offsets=offsets, stream=s)]
+        sizes = [(t.shape, t.dtype) for t in (x, g, d, state, offsets)]
+        del x, g, d, state, offsets, saved
+        for k in range(4):  # would take the same memory, if it were free
+            for shp, dt in sizes:
+                torch.full(shp, 77, dtype=dt, device=DEV)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_handle_freed_while_another_stream_steps(given):
+    """The same for an AdamW handle's memory, its parameters and gradients."""
+    say("adamw on another stream, handle freed", given)
+    n = 1 << 20
+    p0, g0 = torch.randn(n, device=DEV), torch.randn(n, device=DEV)
+    ref = p0.clone()
+    o = B.sla_adamw_create([ref], state_bits=8)
+    for t in (1, 2):
+        B.sla_adamw_step(o, [g0], step=t, lr=1e-2)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        p, g, scale = p0.clone(), g0.clone(), torch.ones(1, device=DEV)
+        opt = B.sla_adamw_create([p], state_bits=8)
+        torch.cuda.synchronize()
+        busy(s)
+        with torch.cuda.stream(s) if not given else torch.cuda.stream(torch.cuda.current_stream()):
+            for t in (1, 2):
+                B.sla_adamw_step(opt, [g], step=t, lr=1e-2, grad_scale=scale,
+                                 stream=s if given else None)
+        if not given:  # as with torch's own operations in a stream's context
+            g.record_stream(s)
+            scale.record_stream(s)
+        state, table = opt.state.numel(), opt._table.numel()
+        del g, scale, opt
+        for k in range(4):
+            for size in (4 * n, state, table, 4):
+                torch.full((size,), 77, dtype=torch.uint8, device=DEV)
+        s.synchronize()
+        assert torch.equal(p, ref)
+
+
+def test_a_stream_given_by_its_pointer():
+    say("operators on a raw stream")
+    s = torch.cuda.Stream()
+    p, g = torch.ones(300, device=DEV), torch.ones(300, device=DEV)
+    x = torch.randn(2, 300, 8, device=DEV)
+    torch.cuda.synchronize()
+    for raw in (s.cuda_stream, torch.cuda.ExternalStream(s.cuda_stream)):
+        opt = B.sla_adamw_create([p], stream=raw)
+        B.sla_adamw_step(opt, [g], step=1, lr=1e-2, stream=raw)
+        h, _, _ = B.sla_linrec_forward(x, x, stream=raw)
+        s.synchronize()
+        assert bool((p < 1).all()) and torch.equal(h, B.sla_linrec_forward(x, x)[0])
