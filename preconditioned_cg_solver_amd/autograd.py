@@ -9,11 +9,14 @@ Only x is saved between forward and backward.
 
 linear_recurrence does the same for the lower bidiagonal system of a gated
 recurrence along a sequence: forward substitution, and the transposed solve
-for the gradients; besides the inputs it saves a state every 32 to 256 steps.
+for the gradients; besides the inputs it saves a state every 128 steps.
+
+The gradients are differentiable no further: differentiating them raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -31,6 +34,7 @@ class PCGSolve(torch.autograd.Function):
         return x
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_x):
         (x,) = ctx.saved_tensors
         grad_b, grad_vals, _ = B.sla_pcg_adjoint(ctx.A, ctx.G, ctx.eps, x, grad_x.contiguous(),
@@ -55,6 +59,7 @@ class LinearRecurrence(torch.autograd.Function):
         return h, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_h, grad_last):
         x, gate, h0, offsets, saved = ctx.saved_tensors
         if grad_h is not None and grad_h.shape[-1] > 1 and grad_h.stride(-1) != 1:

@@ -45,6 +45,7 @@ import time
 
 import numpy as np
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import autograd as AG
 from . import binding as B
@@ -160,6 +161,7 @@ class _SolveColumns(torch.autograd.Function):
         return B.sla_pcg_solve_multi(A, G, eps, rhs.contiguous(), rtol=rtol, maxit=maxit)[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         A, G, eps, rtol, maxit = ctx.args
         # A does not depend on the parameters: of its adjoint only dL/dB is used
