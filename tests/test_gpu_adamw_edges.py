@@ -218,3 +218,69 @@ def test_a_stream_given_by_its_pointer():
         h, _, _ = B.sla_linrec_forward(x, x, stream=raw)
         s.synchronize()
         assert bool((p < 1).all()) and torch.equal(h, B.sla_linrec_forward(x, x)[0])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_past_the_caches(bits):
+    """A step that moves more than 256 MB reads and writes past the caches: its
+    small tensors (partial blocks, any alignment, every type, bf16 copies) have
+    the bits of a step of their own, which goes through them, and so have the
+    ends of the large one."""
+    say("adamw past the caches", bits)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    kinds = [(torch.float32, torch.float32), (torch.float32, torch.bfloat16),
+             (torch.bfloat16, torch.bfloat16), (torch.float64, torch.float64)]
+    parts, grads, low = [], [], []
+    for k, n in enumerate([1, 3, 255, 256, 257, 1021, 4095, 4096, 10_000] * 4):
+        pd, gd = kinds[k % 4]
+        shift = k % 5
+        parts.append(torch.randn(n + 8, device=DEV, generator=gen).to(pd)[shift:shift + n])
+        grads.append(torch.randn(n + 8, device=DEV, generator=gen).to(gd)[k % 3:k % 3 + n])
+        low.append(torch.zeros(n + 1, device=DEV, dtype=torch.bfloat16)[k % 2:k % 2 + n]
+                   if pd == torch.float32 else None)
+    n = 20_000_003
+    big, gbig = torch.randn(n, device=DEV, generator=gen), torch.randn(n, device=DEV, generator=gen)
+
+    def run(tail, gtail):
+        ps = [torch.empty_like(torch.zeros(p.numel() + 8, device=DEV, dtype=p.dtype))
+              [k % 5:k % 5 + p.numel()].copy_(p) for k, p in enumerate(parts)] + [tail.clone()]
+        cs = [None if c is None else torch.zeros_like(c) for c in low] + [None]
+        opt = B.sla_adamw_create(ps, state_bits=bits, grad_dtype=[g.dtype for g in grads] +
+                                 [torch.float32], copies=cs)
+        for t in (1, 2, 3):
+            B.sla_adamw_step(opt, grads + [gtail], step=t, lr=1e-2, seed=9)
+        return opt, ps, cs, B.sla_adamw_get_state(opt)
+
+    head = 256 * 40
+    big_opt, big_ps, big_cs, big_state = run(big, gbig)
+    opt, ps, cs, state = run(big[:head], gbig[:head])
+    for a, b in zip(big_ps[:-1] + [big_ps[-1][:head]] + big_cs, ps + cs):
+        assert (a is None and b is None) or torch.equal(a, b)
+    for a, b in zip(big_state, state):
+        assert torch.equal(a[:opt.padded], b)
+    # 32-bit states know no place, so the end can be compared as well
+    if bits == 32:
+        end = n // 256 * 256 - head
+        _, ps, _, state = run(big[end:], gbig[end:])
+        assert torch.equal(big_ps[-1][end:], ps[-1])
+        for a, b in zip(big_state, state):
+            size = n - end
+            at, small = big_opt.starts[-1] + end, opt.starts[-1]
+            assert torch.equal(a[at:at + size], b[small:small + size])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_read_through_the_c_entry(bits):
+    """sla_adamw_get_state copies 32-bit states out as well."""
+    say("adamw states in C", bits)
+    p, g = torch.randn(3000, device=DEV), torch.randn(3000, device=DEV)
+    opt = B.sla_adamw_create([p], state_bits=bits)
+    B.sla_adamw_step(opt, [g], step=1, lr=1e-2)
+    want = B.sla_adamw_get_state(opt)
+    out = [torch.full_like(t, 7.0) for t in want]
+    raw = torch.cuda.current_stream().cuda_stream
+    assert B.lib().sla_adamw_get_state(opt.handle, out[0].data_ptr(), out[1].data_ptr(), raw) == 0
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert B.lib().sla_adamw_get_state(opt.handle, out[0].data_ptr(), out[0].data_ptr(), raw) == -1
+    state, table, padded = B.sla_adamw_sizes([p], bits)
+    assert (state, padded) == (opt.state.numel(), opt.padded) and table == opt._table.numel()

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import say
+from preconditioned_cg_solver_amd import binding as B
+from gpu_util import DEV, say
 from test_gpu_linrec import check, make, reference, run
 import seq_util as S
 
@@ -219,3 +220,44 @@ def test_same_bits_whichever_way_what_enters_was_found():
         again = run("f32", "linear", x, g, h0, None, dh, dl)
         for k in first:
             assert torch.equal(first[k].nan_to_num(7.0), again[k].nan_to_num(7.0)), k
+
+
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [8192, 8191])
+@pytest.mark.parametrize("packed", [False, True])
+def test_16_bit_rows_past_the_caches(mode, dtype, d, packed):
+    """Calls of more than 256 MB of 16-bit rows read and write past the caches:
+    a quarter of the channels alone, which goes through them, has the same bits,
+    in whole chunks and in the last ones of sequences, in packs of channels and one
+    by one."""
+    say("recurrence past the caches", mode, dtype, d, packed)
+    n, steps = 4, 2000 + 77
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    shape = (n * steps, d) if packed else (n, steps, d)
+    x, g, dh = (torch.randn(shape, device=DEV, generator=gen).mul_(0.4).to(dtype)
+                for _ in range(3))
+    h0, dl = (torch.randn(n, d, device=DEV, generator=gen) for _ in range(2))
+    off = torch.tensor([0, 1, 900, 900, n * steps], device=DEV) if packed else None
+
+    def call(at):
+        a, b, c = (t[..., at].contiguous() for t in (x, g, dh))
+        s, e = h0[:, at].contiguous(), dl[:, at].contiguous()
+        h, last, saved = B.sla_linrec_forward(a, b, h0=s, offsets=off, mode=mode, save=True)
+        return [h, last, *B.sla_linrec_backward(a, b, saved, c, grad_last=e, h0=s, offsets=off,
+                                                mode=mode)]
+
+    part = slice(4096, 6144 + d % 2)  # as many channels a thread
+    for a, b in zip(call(slice(0, d)), call(part)):
+        assert torch.equal(a[..., part], b)
+
+
+def test_sizes_are_those_of_a_call():
+    say("recurrence sizes")
+    x = torch.randn(2, 700, 96, device=DEV)
+    _, _, saved = B.sla_linrec_forward(x, x, save=True)
+    assert B.sla_linrec_sizes(x, x)[0] == saved.numel() * 4
+    off = torch.tensor([0, 700, 1400], device=DEV)
+    flat = x.view(1400, 96)
+    _, _, saved = B.sla_linrec_forward(flat, flat, offsets=off, save=True)
+    assert B.sla_linrec_sizes(flat, flat, off)[0] == saved.numel() * 4
