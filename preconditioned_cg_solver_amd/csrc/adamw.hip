@@ -9,10 +9,10 @@
 //
 // What bounds it: an element's 28 bytes with fp32 states (120M of them 536 to
 // 582 us between cards, 5.8 to 6.3 TB/s) and its 14 bytes with 8-bit ones and a
-// bf16 gradient (60M: 133 us, 6.3 TB/s), where an elementwise sum of large
-// arrays reaches 6.2; with bf16 parameters and 8-bit states (10 bytes) the
-// rounding's arithmetic, some 80 instructions an element (9M: 26 us, 3.5 TB/s);
-// below a million elements the launch (60000 in 24 tensors: 3.4 us).
+// bf16 gradient (60M: 131 to 140 us, 6.0 to 6.4 TB/s), where an elementwise sum
+// of large arrays reaches 6.2; with bf16 parameters and 8-bit states (10 bytes)
+// the rounding's arithmetic, some 80 instructions an element (9M: 26 to 27 us,
+// 3.5 TB/s); below a million elements the launch (60000 in 24 tensors: 3.3 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -27,7 +27,7 @@ namespace {
 
 // A workgroup takes a chunk: W channels of as many steps as its registers
 // hold.  A thread has V neighbouring channels of consecutive steps.  The
-// backward pass holds more per element, in chunks of half the steps.
+// backward pass holds more per element, in chunks of 128 steps for every type.
 constexpr int kThreads = 512;
 // The channels of narrow chunks, and of the forward pass's wide ones (see
 // width_of).
@@ -66,6 +66,8 @@ constexpr int forward_threads() {
 //  - a small product is not applied where what it lost shows (loses);
 //  - where the parts' maps fail, the steps of the channel in the chunk are taken
 //    one by one, from memory, by the wave that joins the parts.
+// Forward, 65536 x 512 fp32, where an ordinary call takes 93 us: chunks without
+// maps throughout 0.43 ms, every step one by one 17 ms (8 x 2048 x 2048: 0.63 ms).
 template <typename C>
 struct Range {
   static constexpr bool k64 = sizeof(C) == 8;
@@ -623,11 +625,12 @@ __device__ __forceinline__ bool went_wrong(C from, C to, C high, F part, G state
 //
 // Bound by the bytes of x, gate and h, at the rate at which rows are reached in
 // pieces of 128 or 256 bytes, and by the latency of the joining: 4 x 4096 x 4096
-// bf16 84 us (4.8 TB/s; the chunks without the joining 78 us), 8 x 2048 x 2048
-// bf16 47 us (37 us), 65536 x 512 fp32 84 to 90 us (4.5 to 4.8 TB/s), 262144 x 1024
-// fp16 331 us (4.9 TB/s; in chunks of twice the steps and threads 349 us).  A
-// quarter-rate exponential and reciprocal an element leave no room to work the
-// coefficients out twice where registers hold them.
+// bf16 84 to 88 us (4.6 to 4.8 TB/s; the chunks without the joining 78 us), 8 x 2048
+// x 2048 bf16 48 us (37 us), 65536 x 512 fp32 88 us (4.6 TB/s), 262144 x 1024 fp16 331
+// to 343 us (4.7 to 4.9 TB/s; in chunks of twice the steps and threads 349 us), 120
+// packed sequences of 833 x 1024 bf16 150 us (4.1 TB/s).  A quarter-rate exponential
+// and reciprocal an element leave no room to work the coefficients out twice
+// where registers hold them.
 // Workgroups that stay and fetch the next chunk's rows while they join one
 // took 148 us for the first of these: two fit a compute unit, and neither
 // hides the other's wait.
@@ -803,14 +806,19 @@ __global__ __launch_bounds__((forward_threads<T, W, V>()), 4) void rec_forward(A
 }
 
 // One chunk of the adjoint, from the saved state before it.  The composed maps
-// of the forward pass are needed again, for h, beside those of mu; both are
-// taken in the one pass over the rows.
+// of the forward pass are needed again, for h, beside those of mu.  The sum of a
+// part's map of mu is taken from the part's end, in a pass of its own over the
+// registers: taken with the product of the coefficients before each step, in
+// the pass that loads them, it would be NaN where that product leaves its range
+// (and 8 x 2048 x 2048 bf16 took 89 us instead of 86, fp64 4 x 2048 x 1024 101 instead
+// of 85, for the registers that the products held; where most steps of a part lie
+// past the sequence's end it costs, 256 x 32 x 4096 bf16 130 and 135 us).
 //
 // Bound as the forward pass, by the bytes of x, gate, dh and the two gradients,
-// and by registers: in 16 bits a thread has 64 of them for its 16 elements (some
-// are spilt), so that four workgroups share a compute unit: 8 x 2048 x 2048 bf16 80
-// us (4.2 TB/s; with two workgroups of 1024 threads 86 us), 65536 x 512 fp32 134 us
-// (5.0 TB/s), 120 packed sequences of 833 x 1024 bf16 268 us (3.8 TB/s).
+// and by registers: in 16 bits a thread has 64 of them for its 16 elements, so
+// that four workgroups share a compute unit: 8 x 2048 x 2048 bf16 79 us (4.3 TB/s),
+// 65536 x 512 fp32 140 us (4.8 TB/s), 120 packed sequences of 833 x 1024 bf16 266 us
+// (3.8 TB/s).
 template <typename T, int GATE, int V, bool CHAIN>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward(Args<T> p) {
   using C = typename Compute<T>::type;
@@ -844,7 +852,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void rec_backward
     Factors<kSig, C> k[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) pa[v] = C(1), pm[v] = C(0), pu[v] = C(0);
-    constexpr bool kRoom = sizeof(T) == 4;  // for the coefficients themselves
+    // Room to keep the coefficients for the second pass, beside f: 8 x 2048 x 2048
+    // fp32 142 us, 145 with those worked out from f; in fp64 the registers overflow
+    // (99 us for 86).
+    constexpr bool kRoom = sizeof(T) == 4;
     C ka[kRoom ? S : 1][V];
     Pack<T, V> g[S], d[S];
     load_part<S, V>(p.gate + w.g + r.at, p.g_step, r.t0, r.nv, r.full, p.streams,
@@ -1077,9 +1088,10 @@ sla_status refuse(const char* msg) {
 // pays where many sequences and channels stand side by side.  Forward, narrow and
 // wide, us: dense bf16 8 x 4096 x 1024 56, 50, 1000 x 300 x 256 130, 117, 1 x 65536 x 512
 // fp32 93, 119; packed bf16 x 1024, 12 sequences of 8333 151, 180, 120 of 833 161,
-// 187, 800 of 125 220, 246 (fp32 x 512: 156, 136).  The backward pass with 256
-// channels: 92 and 129, 193 and 221, 144 and 296; 264 and 600, 269 and 453, 276
-// and 407.
+// 187, 800 of 125 220, 246 (fp32 x 512: 156, 136).  The backward pass, narrow and
+// with chunks of 256 channels, which are not here any more: 92 and 129, 193 and
+// 221, 144 and 296; 264 and 600, 269 and 453, 276 and 407; for sequences of some 32
+// steps the wide ones were the faster.
 int width_of(const sla_linrec_shape& q, bool backward) {
   if (backward || q.d_offsets || q.n_seq * q.dim < 8192) return kNarrow;
   // under a quarter of the lanes without a channel: 1000 x 300 x 64 bf16, forward, 36

@@ -57,7 +57,8 @@ def test_tensors_that_share_memory():
             step(spans, grads, copies)
         assert torch.equal(flat, before) and not bool(low.any())
     for spans, grads, copies in (([0, 0], (1, 0), None), ([0, 2000, 999], (0, 1, 1), None),
-                                 ([500, 0, 1000], (0, 1, 1), None), ([3000, 0, 1000], (1, 1, 1), None),
+                                 ([500, 0, 1000], (0, 1, 1), None),
+                                 ([3000, 0, 1000], (1, 1, 1), None),
                                  ([0, 1000], (1, 1), [1000, 0]), ([0, 1000], (1, 0), [0, 999])):
         before = flat.clone()
         step(spans, grads, copies)

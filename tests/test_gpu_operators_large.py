@@ -34,7 +34,8 @@ def test_recurrence_of_many_single_steps():
                             (dx, lam, dh.abs() + dl.abs()),
                             (dg, lam * h0, (dh.abs() + dl.abs()) * h0.abs()),
                             (dh0, g * lam, g.abs() * (dh.abs() + dl.abs()))):
-        assert bool(((got.reshape(-1).double() - want).abs() <= 4 * S.U32 * size + 2.0 ** -140).all())
+        off = (got.reshape(-1).double() - want).abs()
+        assert bool((off <= 4 * S.U32 * size + 2.0 ** -140).all())
 
 
 @pytest.mark.parametrize("packed", [False, True])
