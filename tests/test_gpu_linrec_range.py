@@ -169,6 +169,31 @@ def test_infinite_states_stay_infinite(mode, dt, steps, strength):
     check_kinds(got, want, base, (mode, dt, steps, strength))
 
 
+@pytest.mark.parametrize("mode", ["linear", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,steps,d", [(2, 600, 68), (2, 600, 4100), (3, 100, 64)])
+def test_infinite_states_in_packs_of_channels(mode, dt, n, steps, d):
+    """The same where a thread has several channels, in narrow and wide chunks and
+    in a single one; a coefficient of zero makes a NaN of an infinite state and
+    forgets a finite one."""
+    say("recurrence infinite states in packs", mode, dt, n, steps, d)
+    x, g, h0, dh, dl = make(dt, mode, (n, steps), d, n, 40)
+    cut = 0.0 if mode == "linear" else -np.inf
+    g[:, :, 40:] = 2.0 ** -14 if mode == "linear" else -40.0
+    g[:, 70, 51:56] = cut
+    base = reference(dt, mode, x, g, h0, None, dh, dl)
+    x, h0, dh, dl = (v.copy() for v in (x, h0, dh, dl))
+    h0[0, 41], h0[1, 42], h0[0, 52] = np.inf, -np.inf, np.inf
+    x[0, 33, 43], x[0, 20, 53] = -np.inf, np.inf
+    dl[0, 45], dl[1, 54] = np.inf, -np.inf
+    dh[0, steps // 2, 47], dh[1, 80, 55] = np.inf, np.inf
+    want = stepwise(x, g, h0, mode, dh, dl)
+    assert np.all(np.isnan(want["h"][0, 70:, 52:54])) and np.all(np.isinf(want["h"][0, :, 41]))
+    assert np.all(np.isnan(want["dx"][1, :70, 54:56]))
+    got = run(dt, mode, x, g, h0, None, dh, dl)
+    check_kinds(got, want, base, (mode, dt, n, steps, d))
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_a_zero_coefficient_and_an_infinite_state(dt):
     """What the formulas make of it: not a number, from there on."""
