@@ -578,6 +578,178 @@ sla_status sla_adamw_get_state(sla_adamw_t opt, void *d_m, void *d_v, void *stre
  * kept exactly).  v must not be negative.  Asynchronous on `stream`. */
 sla_status sla_adamw_set_state(sla_adamw_t opt, const float *d_m, const float *d_v, void *stream);
 
+/*
+ * Operators of a sequence block of models trained through the solver: a short
+ * causal convolution, a selective scan, and the norms before and after the
+ * block, each with its adjoint.  As for the recurrences above: sequences are
+ * dense (n_seq, steps, dim) or packed (steps, dim) with d_offsets; element
+ * (s, t, c) of a strided input lies at s * seq_stride + t * step_stride + c
+ * (packed inputs ignore the sequence's stride; strides are >= 0); outputs are
+ * dense; parameters, states of scans and their gradients are fp32 (fp64 for
+ * SLA_F64), as are all sums and products; each output is rounded once, when
+ * stored.  Calls are asynchronous on `stream` and allocate nothing, so they can be
+ * captured in a HIP graph.  Two calls on different streams need workspaces of
+ * their own.  Sums are made in a fixed order: two runs give the same bits.
+ * Outputs must not overlap inputs or each other, but where said otherwise.
+ * Whatever the offsets of packed sequences hold, no access leaves the arrays.
+ */
+
+/*
+ * Causal convolution along a sequence, per channel, with 2 to 4 taps:
+ *   pre_t = bias + sum_{k < width} weight[k] x_{t - width + 1 + k},
+ *   y_t = pre_t (SLA_ACT_NONE) or pre_t / (1 + exp(-pre_t)) (SLA_ACT_SILU),
+ * where x_{0}, x_{-1}, .. (the width - 1 inputs before a sequence) are its state,
+ * (n_seq, width - 1, dim), oldest first, zeros if d_state is NULL.  d_last
+ * receives the state for what follows: the last width - 1 of state and inputs.
+ * Both have the inputs' dtype: they are copies.  d_last may be d_state itself,
+ * updated in place.  weight is (dim, width), bias (dim), NULL for none.
+ */
+typedef enum { SLA_ACT_NONE = 0, SLA_ACT_SILU = 1, SLA_ACT_RANGE_ = 0x7fffffff } sla_act;
+
+typedef struct {
+    int64_t n_seq;             /* sequences                                       */
+    int64_t steps;             /* steps of each (dense) or of all (packed)        */
+    int64_t dim;               /* channels                                        */
+    int64_t width;             /* taps: 2, 3 or 4                                 */
+    const int64_t *d_offsets;  /* NULL: dense                                     */
+    sla_dtype dtype;
+    sla_act act;
+} sla_conv_shape;
+
+/* Bytes of the backward pass's d_work.  Errors: SLA_ERR_INVALID_ARG (NULL, negative
+ * size, unknown dtype or act), SLA_ERR_UNSUPPORTED (width, sizes beyond what a call
+ * can index). */
+sla_status sla_conv_sizes(const sla_conv_shape *shape, size_t *work_bytes);
+
+/* d_last may be NULL: not wanted.  SLA_ERR_INVALID_ARG on NULL arrays, negative
+ * strides or an output that is an input. */
+sla_status sla_conv_forward(const sla_conv_shape *shape, const void *d_x, int64_t x_seq_stride,
+                            int64_t x_step_stride, const void *d_weight, const void *d_bias,
+                            const void *d_state, void *d_y, void *d_last, void *stream);
+
+/* Gradients from those of y (d_grad_y; NULL: zeros) and of the last state (d_grad_last;
+ * NULL: zeros).  d_grad_bias and d_grad_state may be NULL: not wanted. */
+sla_status sla_conv_backward(const sla_conv_shape *shape, const void *d_x, int64_t x_seq_stride,
+                             int64_t x_step_stride, const void *d_weight, const void *d_bias,
+                             const void *d_state, const void *d_grad_y, int64_t grad_seq_stride,
+                             int64_t grad_step_stride, const void *d_grad_last, void *d_grad_x,
+                             void *d_grad_weight, void *d_grad_bias, void *d_grad_state,
+                             void *d_work, size_t work_bytes, void *stream);
+
+/*
+ * Selective scan: per channel c of group g and state n <= 16,
+ *   delta_t = softplus(dt_t + dt_bias) (softplus = 1) or dt_t + dt_bias (0),
+ *   h_t[n] = exp(delta_t A[c][n]) h_{t-1}[n] + delta_t x_t B_t[g][n],
+ *   s_t = sum_n C_t[g][n] h_t[n] + D x_t,   y_t = s_t z_t / (1 + exp(-z_t)),
+ * without the last factor if there is no z.  The dim channels are `groups` equal
+ * groups of neighbours.  x, dt, z: (n_seq, steps, dim) or (steps, dim) when packed;
+ * B and C: (.., groups, n_state), rows adjacent within a step; A: (dim, n_state); D and
+ * dt_bias: (dim), NULL for zeros; states: (n_seq, dim, n_state).
+ *
+ * A coefficient exp(delta A) under 2^-126 counts as 0 (fp64: 2^-1074).  Where a
+ * sequence is cut into chunks, which long ones of few channels are, a chunk's
+ * product of coefficients is exp(A sum of its deltas).  A state that is not finite
+ * makes the ones that follow in its sequence not finite.
+ */
+typedef struct {
+    int64_t n_seq, steps, dim, n_state, groups;
+    const int64_t *d_offsets;  /* NULL: dense */
+    sla_dtype dtype;
+    int32_t softplus;
+} sla_selscan_shape;
+
+/* The inputs, with the strides of those that may have some. */
+typedef struct {
+    const void *d_x, *d_dt, *d_z, *d_b, *d_c;  /* d_z: NULL for none */
+    int64_t x_seq, x_step, dt_seq, dt_step, z_seq, z_step, b_seq, b_step, c_seq, c_step;
+    const void *d_a, *d_d, *d_dt_bias;  /* d_d, d_dt_bias: NULL for zeros */
+    const void *d_h0;                   /* NULL: zeros */
+} sla_selscan_in;
+
+/* Bytes of d_saved (the states that the backward pass starts from, one every 16
+ * steps, 8 in fp64) and of d_work for each direction (0: none needed). */
+sla_status sla_selscan_sizes(const sla_selscan_shape *shape, size_t *saved_bytes,
+                             size_t *forward_bytes, size_t *backward_bytes);
+
+/* d_h_last (NULL: not wanted; of dense sequences it may be d_h0, updated in place)
+ * and d_saved (NULL: no backward pass will follow) are optional.  One serving step is
+ * steps = 1. */
+sla_status sla_selscan_forward(const sla_selscan_shape *shape, const sla_selscan_in *in, void *d_y,
+                               void *d_h_last, void *d_saved, void *d_work, size_t work_bytes,
+                               void *stream);
+
+/* Gradients of everything, those of NULL inputs not wanted (d_grad_z and d_grad_h0 are
+ * then ignored; d_grad_d and d_grad_dt_bias may be NULL).  grad_b and grad_c are
+ * sums over the channels of a group, dense. */
+typedef struct {
+    void *d_x, *d_dt, *d_z, *d_b, *d_c, *d_a, *d_d, *d_dt_bias, *d_h0;
+} sla_selscan_grads;
+
+/* d_saved is what the forward call on the same arguments wrote; d_grad_y may be strided;
+ * d_grad_last (NULL: zeros) is the gradient of the last states. */
+sla_status sla_selscan_backward(const sla_selscan_shape *shape, const sla_selscan_in *in,
+                                const void *d_saved, const void *d_grad_y, int64_t grad_seq,
+                                int64_t grad_step, const void *d_grad_last,
+                                const sla_selscan_grads *grads, void *d_work, size_t work_bytes,
+                                void *stream);
+
+/*
+ * The norms before and after a block, of rows of dim elements:
+ *   in:   r = residual + scale x,  y = weight r / rms(r)
+ *   out:  n = weight u / rms(u) with u = x silu(gate)     (SLA_GATE_FIRST)
+ *         n = weight x / rms(x) silu(gate)                (SLA_NORM_FIRST)
+ *         out = residual + scale n
+ * with rms(v) = sqrt(mean(v^2) + eps) and silu(v) = v / (1 + exp(-v)).  residual (then 0),
+ * scale (then 1) and gate (then no factor) may be NULL.  x, y and gate have `dtype`;
+ * residual, r and out have `stream`, which is `dtype` or, for 16 bits, SLA_F32.  weight
+ * and scale are (dim).  The norm of r is taken before r is rounded.  Rows of x, residual and
+ * gate lie x_row, .. elements apart (>= 0); all other arrays are dense.  d_rstd
+ * receives 1 / rms of each row, which the backward pass starts from (NULL: none will
+ * follow).
+ */
+typedef enum { SLA_GATE_FIRST = 0, SLA_NORM_FIRST = 1, SLA_ORDER_RANGE_ = 0x7fffffff } sla_norm_order;
+
+typedef struct {
+    int64_t rows, dim;
+    sla_dtype dtype, stream;
+    double eps;
+} sla_norm_shape;
+
+/* Bytes of the backward passes' d_work.  Errors: SLA_ERR_INVALID_ARG (NULL, negative
+ * size, eps negative or not finite, unknown dtypes), SLA_ERR_UNSUPPORTED (sizes beyond what a
+ * call can index). */
+sla_status sla_norm_sizes(const sla_norm_shape *shape, size_t *work_bytes);
+
+/* Without residual and scale, r is x: then d_r has to be NULL.  d_r may be d_residual
+ * where that is dense, updated in place. */
+sla_status sla_norm_in_forward(const sla_norm_shape *shape, const void *d_x, int64_t x_row,
+                               const void *d_residual, int64_t residual_row, const void *d_scale,
+                               const void *d_weight, void *d_y, void *d_r, void *d_rstd,
+                               void *stream);
+/* d_grad_r (NULL: zeros) is the gradient of r by its other uses, of type `stream`.
+ * d_grad_residual (NULL: not wanted) is the gradient of r by all uses; d_grad_x, of type
+ * `dtype`, is scale times it; d_grad_scale may be NULL: not wanted. */
+sla_status sla_norm_in_backward(const sla_norm_shape *shape, const void *d_grad_y,
+                                const void *d_grad_r, const void *d_x, int64_t x_row,
+                                const void *d_residual, int64_t residual_row, const void *d_scale,
+                                const void *d_weight, const void *d_rstd, void *d_grad_x,
+                                void *d_grad_residual, void *d_grad_weight, void *d_grad_scale,
+                                void *d_work, size_t work_bytes, void *stream);
+
+/* d_out may be d_residual where that is dense, updated in place. */
+sla_status sla_norm_out_forward(const sla_norm_shape *shape, sla_norm_order order, const void *d_x,
+                                int64_t x_row, const void *d_gate, int64_t gate_row,
+                                const void *d_residual, int64_t residual_row, const void *d_scale,
+                                const void *d_weight, void *d_out, void *d_rstd, void *stream);
+/* d_grad_out has type `stream`; it is the residual's gradient as it stands.
+ * d_grad_gate (for a gate) and d_grad_scale (for a scale) are written. */
+sla_status sla_norm_out_backward(const sla_norm_shape *shape, sla_norm_order order,
+                                 const void *d_grad_out, const void *d_x, int64_t x_row,
+                                 const void *d_gate, int64_t gate_row, const void *d_scale,
+                                 const void *d_weight, const void *d_rstd, void *d_grad_x,
+                                 void *d_grad_gate, void *d_grad_weight, void *d_grad_scale,
+                                 void *d_work, size_t work_bytes, void *stream);
+
 /* Human-readable name of a status, and the calling thread's last error text. */
 const char *sla_status_string(sla_status st);
 const char *sla_last_error(void);

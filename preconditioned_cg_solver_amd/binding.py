@@ -23,6 +23,8 @@ LIB_PATH = os.path.join(PKG, "libsla.so")
 
 SLA_F64, SLA_F32, SLA_BF16, SLA_F16 = 0, 1, 2, 3
 SLA_GATE_LINEAR, SLA_GATE_SIGMOID = 0, 1
+SLA_ACT_NONE, SLA_ACT_SILU = 0, 1
+SLA_GATE_FIRST, SLA_NORM_FIRST = 0, 1
 SLA_BUILD_TRANSPOSE, SLA_VALIDATE = 1, 2
 STATUS = {0: "SLA_OK", 1: "SLA_NOT_CONVERGED", -1: "SLA_ERR_INVALID_ARG", -2: "SLA_ERR_UNSUPPORTED",
           -3: "SLA_ERR_BREAKDOWN", -4: "SLA_ERR_NONFINITE", -5: "SLA_ERR_HIP", -6: "SLA_ERR_OOM"}
@@ -56,6 +58,36 @@ class AdamwHyper(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int64), ("steps", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("d_offsets", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("act", ctypes.c_int)]
+
+
+class SelscanShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int64), ("steps", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("n_state", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("d_offsets", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("softplus", ctypes.c_int32)]
+
+
+class SelscanIn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_dt", "d_z", "d_b", "d_c")] + \
+        [(n, ctypes.c_int64) for n in ("x_seq", "x_step", "dt_seq", "dt_step", "z_seq", "z_step",
+                                       "b_seq", "b_step", "c_seq", "c_step")] + \
+        [(n, ctypes.c_void_p) for n in ("d_a", "d_d", "d_dt_bias", "d_h0")]
+
+
+class SelscanGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_dt", "d_z", "d_b", "d_c", "d_a", "d_d",
+                                               "d_dt_bias", "d_h0")]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("stream", ctypes.c_int), ("eps", ctypes.c_double)]
 
 
 _lib = None
@@ -132,6 +164,22 @@ def _declare(L):
         "sla_adamw_step": ([vp, vp, vp, vp, vp], st),
         "sla_adamw_get_state": ([vp, vp, vp, vp], st),
         "sla_adamw_set_state": ([vp, vp, vp, vp], st),
+        "sla_conv_sizes": ([vp, ctypes.POINTER(sz)], st),
+        "sla_conv_forward": ([vp, vp, i64, i64, vp, vp, vp, vp, vp, vp], st),
+        "sla_conv_backward": ([vp, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp,
+                               sz, vp], st),
+        "sla_selscan_sizes": ([vp, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)],
+                              st),
+        "sla_selscan_forward": ([vp, vp, vp, vp, vp, vp, sz, vp], st),
+        "sla_selscan_backward": ([vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp], st),
+        "sla_norm_sizes": ([vp, ctypes.POINTER(sz)], st),
+        "sla_norm_in_forward": ([vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp], st),
+        "sla_norm_in_backward": ([vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                  vp], st),
+        "sla_norm_out_forward": ([vp, ctypes.c_int, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp],
+                                 st),
+        "sla_norm_out_backward": ([vp, ctypes.c_int, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                   vp, vp, sz, vp], st),
         "sla_status_string": ([st], ctypes.c_char_p),
         "sla_last_error": ([], ctypes.c_char_p),
         "sla_set_profiling": ([i32], st),
@@ -1008,3 +1056,425 @@ def sla_adamw_set_state(opt: Adamw, m: torch.Tensor, v: torch.Tensor, stream=Non
     if used is not None:
         _record(used, m, v)
     _written(opt.state)
+
+
+# ----- operators of a sequence block: convolution, selective scan, norms -----
+
+_ACTS = {"none": SLA_ACT_NONE, "silu": SLA_ACT_SILU}
+_ORDERS = {"gate_first": SLA_GATE_FIRST, "norm_first": SLA_NORM_FIRST}
+
+
+def _sequences(x, offsets, name: str = "x"):
+    """(sequences, steps, channels) of a dense or a packed tensor."""
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError(f"{name} must be (sequences, steps, channels), or give offsets")
+        return tuple(x.shape)
+    if x.dim() != 2:
+        raise ValueError(f"packed {name} must be (steps, channels)")
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1 \
+            or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 vector of sequences + 1 entries")
+    return (offsets.numel() - 1, *x.shape)
+
+
+def _param_dtype(x) -> torch.dtype:
+    return torch.float64 if x.dtype == torch.float64 else torch.float32
+
+
+def _dense(t, name: str, shape, dtype) -> Optional[int]:
+    """Pointer of an optional contiguous tensor of a given shape and dtype."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype}")
+    return t.data_ptr()
+
+
+def _scratch(n: int, dev):
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
+def _conv_shape(x, weight, offsets, act) -> ConvShape:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    n, t, d = _sequences(x, offsets)
+    if weight.dim() != 2 or weight.shape[0] != d:
+        raise ValueError("weight must be (channels, taps)")
+    return ConvShape(n, t, d, weight.shape[1], None if offsets is None else offsets.data_ptr(),
+                     _DTYPES[x.dtype], _ACTS[act])
+
+
+def _conv_sizes(q: ConvShape) -> int:
+    work = ctypes.c_size_t()
+    _check(lib().sla_conv_sizes(ctypes.byref(q), ctypes.byref(work)))
+    return work.value
+
+
+def sla_conv_sizes(x, weight, offsets=None, act: str = "silu") -> int:
+    """Bytes of the backward pass's workspace."""
+    return _conv_sizes(_conv_shape(x, weight, offsets, act))
+
+
+def sla_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     state: Optional[torch.Tensor] = None,
+                     offsets: Optional[torch.Tensor] = None, act: str = "silu",
+                     last: Optional[torch.Tensor] = None, stream=None):
+    """y_t = act(bias + sum_k weight[:, k] x_{t - taps + 1 + k}) along each sequence, per
+    channel, with 2 to 4 taps and act "silu" or "none".
+
+    x as in sla_linrec_forward, strided or packed; weight (channels, taps) and bias
+    (channels) float32 (float64 for float64).  state (sequences, taps - 1, channels), of
+    x's dtype: the inputs before each sequence, oldest first (None: zeros); last, of the same
+    form, receives what follows needs, and may be state itself.  `stream` as in
+    sla_linrec_forward.  Returns (y, last)."""
+    q = _conv_shape(x, weight, offsets, act)
+    pt = _param_dtype(x)
+    held = (q.n_seq, q.width - 1, q.dim)
+    px = _steps_in(x, "x", x)
+    pw, pb = _dense(weight, "weight", (q.dim, q.width), pt), _dense(bias, "bias", (q.dim,), pt)
+    ps, pl = _dense(state, "state", held, x.dtype), _dense(last, "last", held, x.dtype)
+    dev = _device_of((("x", x), ("weight", weight), ("bias", bias), ("state", state),
+                      ("offsets", offsets), ("last", last)))
+    _conv_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    given = last
+    with ctx:
+        y = _like(x)
+        if last is None:
+            last = torch.empty(held, dtype=x.dtype, device=dev)
+            pl = _raw(last)
+    _check(lib().sla_conv_forward(ctypes.byref(q), *px, pw, pb, ps, _raw(y), pl, raw))
+    if used is not None:
+        _record(used, x, weight, bias, state, offsets, given)
+    if given is not None:
+        _written(given)
+    return y, last
+
+
+def sla_conv_backward(x: torch.Tensor, weight: torch.Tensor, grad_y: Optional[torch.Tensor],
+                      bias: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                      grad_last: Optional[torch.Tensor] = None,
+                      offsets: Optional[torch.Tensor] = None, act: str = "silu", stream=None):
+    """Gradients (of x, weight, bias or None, state or None) from those of y and last
+    (None: zero); the other arguments are the forward call's."""
+    q = _conv_shape(x, weight, offsets, act)
+    pt = _param_dtype(x)
+    held = (q.n_seq, q.width - 1, q.dim)
+    px, pd = _steps_in(x, "x", x), _steps_in(grad_y, "grad_y", x)
+    pw, pb = _dense(weight, "weight", (q.dim, q.width), pt), _dense(bias, "bias", (q.dim,), pt)
+    ps, pl = _dense(state, "state", held, x.dtype), _dense(grad_last, "grad_last", held, x.dtype)
+    dev = _device_of((("x", x), ("weight", weight), ("grad_y", grad_y), ("bias", bias),
+                      ("state", state), ("grad_last", grad_last), ("offsets", offsets)))
+    n_work = _conv_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    with ctx:
+        dx, dw = _like(x), _like(weight)
+        db = _like(bias) if bias is not None else None
+        dstate = _like(state) if state is not None else None
+        work = _scratch(n_work, dev)
+    _check(lib().sla_conv_backward(ctypes.byref(q), *px, pw, pb, ps, *pd, pl, _raw(dx), _raw(dw),
+                                   _raw(db), _raw(dstate), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, x, weight, grad_y, bias, state, grad_last, offsets)
+    return dx, dw, db, dstate
+
+
+def _shared_in(t, name: str, x, q):
+    """(pointer, sequence stride, step stride) of B or C."""
+    want = (*x.shape[:-1], q.groups, q.n_state)
+    if tuple(t.shape) != want or t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {want} of x's dtype")
+    st = t.stride()
+    if t.numel() and (t.shape[-1] > 1 and st[-1] != 1 or
+                      t.shape[-2] > 1 and st[-2] != t.shape[-1]):
+        raise ValueError(f"{name}'s groups and states must be adjacent")
+    return t.data_ptr(), (st[0] if len(st) == 4 else 0), st[-3]
+
+
+class _Selscan:
+    """The checked arguments of a selective scan."""
+
+    def __init__(self, x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus):
+        n, t, d = _sequences(x, offsets)
+        if B.dim() != x.dim() + 1 or A.dim() != 2:
+            raise ValueError("B and C must be (.., groups, states), A (channels, states)")
+        self.q = q = SelscanShape(n, t, d, B.shape[-1], B.shape[-2],
+                                  None if offsets is None else offsets.data_ptr(),
+                                  _DTYPES[x.dtype], 1 if softplus else 0)
+        self.pt = pt = _param_dtype(x)
+        px, pu, pz = _steps_in(x, "x", x), _steps_in(dt, "dt", x), _steps_in(z, "z", x)
+        pb, pc = _shared_in(B, "B", x, q), _shared_in(C, "C", x, q)
+        self.held = (n, d, q.n_state)
+        self.given = SelscanIn(
+            px[0], pu[0], pz[0], pb[0], pc[0], *px[1:], *pu[1:], *pz[1:], *pb[1:], *pc[1:],
+            _dense(A, "A", (d, q.n_state), pt), _dense(D, "D", (d,), pt),
+            _dense(dt_bias, "dt_bias", (d,), pt), _dense(h0, "h0", self.held, pt))
+        self.tensors = (x, dt, A, B, C, D, z, dt_bias, h0, offsets)
+        self.named = tuple(zip(("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0", "offsets"),
+                               self.tensors))
+        s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().sla_selscan_sizes(ctypes.byref(q), ctypes.byref(s), ctypes.byref(f),
+                                       ctypes.byref(b)))
+        self.sizes = s.value, f.value, b.value
+
+
+def sla_selscan_sizes(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, offsets=None,
+                      softplus: bool = True) -> Tuple[int, int, int]:
+    """Bytes of (the states kept for the backward pass, the forward pass's workspace, the
+    backward pass's)."""
+    return _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus).sizes
+
+
+def sla_selscan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        C: torch.Tensor, D: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None,
+                        dt_bias: Optional[torch.Tensor] = None,
+                        h0: Optional[torch.Tensor] = None,
+                        offsets: Optional[torch.Tensor] = None, softplus: bool = True,
+                        save: bool = False, h_last: Optional[torch.Tensor] = None, stream=None):
+    """A selective scan along each sequence: with delta = softplus(dt + dt_bias) (or
+    dt + dt_bias), per channel and state
+        h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,
+    and y_t = (C_t . h_t + D x_t) silu(z_t), without the last factor if z is None.
+
+    x, dt, z as x in sla_linrec_forward, strided or packed; B and C (.., groups, states) of
+    x's dtype, at most 16 states, channels in equal groups of neighbours; A (channels,
+    states), D and dt_bias (channels) and the states h0, h_last (sequences, channels,
+    states) float32 (float64 for float64).  h_last may be given to be overwritten, for dense
+    sequences h0 itself.  `stream` as in sla_linrec_forward.  Returns (y, h_last, saved);
+    `saved` (None unless save) is what the backward pass needs."""
+    a = _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
+    pl = _dense(h_last, "h_last", a.held, a.pt)
+    dev = _device_of(a.named + (("h_last", h_last),))
+    n_saved, n_work, _ = a.sizes
+    raw, ctx, used = _enter(dev, stream)
+    given = h_last
+    with ctx:
+        y = _like(x)
+        if h_last is None:
+            h_last = torch.empty(a.held, dtype=a.pt, device=dev)
+            pl = _raw(h_last)
+        saved = torch.empty(n_saved // a.pt.itemsize, dtype=a.pt, device=dev) if save else None
+        work = _scratch(n_work, dev)
+    _check(lib().sla_selscan_forward(ctypes.byref(a.q), ctypes.byref(a.given), _raw(y), pl,
+                                     _raw(saved), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, *a.tensors, given)
+    if given is not None:
+        _written(given)
+    return y, h_last, saved
+
+
+def sla_selscan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                         C: torch.Tensor, saved: torch.Tensor, grad_y: torch.Tensor,
+                         grad_last: Optional[torch.Tensor] = None,
+                         D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                         dt_bias: Optional[torch.Tensor] = None,
+                         h0: Optional[torch.Tensor] = None,
+                         offsets: Optional[torch.Tensor] = None, softplus: bool = True,
+                         stream=None):
+    """Gradients of (x, dt, A, B, C, D, z, dt_bias, h0), None for those not given, from
+    those of y and of h_last (None: zero); the other arguments are the forward call's."""
+    a = _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
+    pd = _steps_in(grad_y, "grad_y", x)
+    pl = _dense(grad_last, "grad_last", a.held, a.pt)
+    dev = _device_of(a.named + (("saved", saved), ("grad_y", grad_y), ("grad_last", grad_last)))
+    n_saved, _, n_work = a.sizes
+    if saved.dtype != a.pt or not saved.is_contiguous() or \
+            saved.numel() * a.pt.itemsize != n_saved:
+        raise ValueError("saved must be the forward call's")
+    raw, ctx, used = _enter(dev, stream)
+    with ctx:
+        out = [None if t is None else _like(t) for t in (x, dt, A, B, C, D, z, dt_bias, h0)]
+        work = _scratch(n_work, dev)
+    dx, ddt, dA, dB, dC, dD, dz, dbias, dh0 = (_raw(t) for t in out)
+    grads = SelscanGrads(dx, ddt, dz, dB, dC, dA, dD, dbias, dh0)
+    _check(lib().sla_selscan_backward(ctypes.byref(a.q), ctypes.byref(a.given), _raw(saved), *pd,
+                                      pl, ctypes.byref(grads), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, *a.tensors, saved, grad_y, grad_last)
+    return tuple(out)
+
+
+def _rows_of(t, name: str, dim: int):
+    """(pointer, rows, elements from row to row) of a tensor of rows, its last dimension."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() < 1 or t.shape[-1] != dim:
+        raise ValueError(f"{name} must have {dim} elements in its last dimension")
+    rows = t.numel() // dim if dim else 0
+    if t.is_contiguous():
+        return t.data_ptr(), rows, dim
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s elements must be adjacent (last stride 1)")
+    step = want = None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = want = s
+        elif s != want:
+            raise ValueError(f"{name}'s rows must lie evenly spaced")
+        want *= n
+    return t.data_ptr(), rows, dim if step is None else step
+
+
+def _norm_shape(x, stream_dtype, eps) -> NormShape:
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x must have rows")
+    if stream_dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {stream_dtype}")
+    d = x.shape[-1]
+    return NormShape(x.numel() // d if d else 0, d, _DTYPES[x.dtype], _DTYPES[stream_dtype], eps)
+
+
+def _norm_sizes(q: NormShape) -> int:
+    work = ctypes.c_size_t()
+    _check(lib().sla_norm_sizes(ctypes.byref(q), ctypes.byref(work)))
+    return work.value
+
+
+def sla_norm_sizes(x, residual=None) -> int:
+    """Bytes of the backward passes' workspace."""
+    return _norm_sizes(_norm_shape(x, x.dtype if residual is None else residual.dtype, 0.0))
+
+
+def _like_x(t, name: str, x, dtype):
+    if t is not None and (tuple(t.shape) != tuple(x.shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must have x's shape and dtype {dtype}")
+    return t
+
+
+def sla_norm_in_forward(x: torch.Tensor, weight: torch.Tensor,
+                        residual: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None):
+    """The norm before a block: r = residual + scale x (without residual: scale x; without
+    both: x itself), y = weight r / sqrt(mean(r^2) + eps) along the last dimension.
+
+    weight and scale: (dim) float32 (float64 for float64); residual has x's dtype or, where
+    that has 16 bits, float32, and r has the same.  x and residual may be slices of wider
+    tensors whose rows lie evenly spaced.  `stream` as in sla_linrec_forward.  Returns (y, r,
+    rstd); rstd is what the backward pass needs."""
+    _like_x(residual, "residual", x, x.dtype if residual is None else residual.dtype)
+    rt = x.dtype if residual is None else residual.dtype
+    q = _norm_shape(x, rt, eps)
+    pt = _param_dtype(x)
+    px, pr = _rows_of(x, "x", q.dim), _rows_of(residual, "residual", q.dim)
+    pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
+    dev = _device_of((("x", x), ("weight", weight), ("residual", residual), ("scale", scale)))
+    _norm_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    same = residual is None and scale is None
+    with ctx:
+        y = _like(x)
+        r = x if same else torch.empty(x.shape, dtype=rt, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=pt, device=dev)
+    _check(lib().sla_norm_in_forward(ctypes.byref(q), px[0], px[2], pr[0], pr[2], ps, pw, _raw(y),
+                                     None if same else _raw(r), _raw(rstd), raw))
+    if used is not None:
+        _record(used, x, weight, residual, scale)
+    return y, r, rstd
+
+
+def sla_norm_in_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                         rstd: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                         scale: Optional[torch.Tensor] = None,
+                         grad_r: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of (x, residual, weight, scale or None) from those of y and r (None: zero);
+    the other arguments are the forward call's.  The residual's gradient is that of r by
+    both uses; where that of x is the same (no scale, one dtype) they are one tensor."""
+    _like_x(residual, "residual", x, x.dtype if residual is None else residual.dtype)
+    rt = x.dtype if residual is None else residual.dtype
+    q = _norm_shape(x, rt, 0.0)
+    pt = _param_dtype(x)
+    px, pr = _rows_of(x, "x", q.dim), _rows_of(residual, "residual", q.dim)
+    pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
+    py, pg = _dense(grad_y, "grad_y", x.shape, x.dtype), _dense(grad_r, "grad_r", x.shape, rt)
+    pd = _dense(rstd, "rstd", x.shape[:-1], pt)
+    dev = _device_of((("grad_y", grad_y), ("x", x), ("weight", weight), ("rstd", rstd),
+                      ("residual", residual), ("scale", scale), ("grad_r", grad_r)))
+    n_work = _norm_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    apart = scale is not None or rt != x.dtype
+    with ctx:
+        dx, dw = _like(x), _like(weight)
+        dres = torch.empty(x.shape, dtype=rt, device=dev) if apart else dx
+        dscale = _like(scale) if scale is not None else None
+        work = _scratch(n_work, dev)
+    _check(lib().sla_norm_in_backward(ctypes.byref(q), py, pg, px[0], px[2], pr[0], pr[2], ps, pw,
+                                      pd, _raw(dx), _raw(dres) if apart else None, _raw(dw),
+                                      _raw(dscale), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, grad_y, x, weight, rstd, residual, scale, grad_r)
+    return dx, dres, dw, dscale
+
+
+def sla_norm_out_forward(x: torch.Tensor, weight: torch.Tensor,
+                         gate: Optional[torch.Tensor] = None,
+                         residual: Optional[torch.Tensor] = None,
+                         scale: Optional[torch.Tensor] = None, order: str = "gate_first",
+                         eps: float = 1e-5, stream=None):
+    """The norm after a block with its gate: n = weight u / sqrt(mean(u^2) + eps) with
+    u = x silu(gate) ("gate_first"), or that of x, times silu(gate) ("norm_first"); out =
+    residual + scale n.  gate, residual and scale are optional; gate has x's dtype,
+    residual, scale, weight and `stream` are as in sla_norm_in_forward, and out has the
+    residual's dtype (else x's).  Returns (out, rstd)."""
+    if order not in _ORDERS:
+        raise ValueError(f"order must be one of {sorted(_ORDERS)}, got {order!r}")
+    _like_x(gate, "gate", x, x.dtype)
+    _like_x(residual, "residual", x, x.dtype if residual is None else residual.dtype)
+    rt = x.dtype if residual is None else residual.dtype
+    q = _norm_shape(x, rt, eps)
+    pt = _param_dtype(x)
+    px, pg = _rows_of(x, "x", q.dim), _rows_of(gate, "gate", q.dim)
+    pr = _rows_of(residual, "residual", q.dim)
+    pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
+    dev = _device_of((("x", x), ("weight", weight), ("gate", gate), ("residual", residual),
+                      ("scale", scale)))
+    _norm_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    with ctx:
+        out = torch.empty(x.shape, dtype=rt, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=pt, device=dev)
+    _check(lib().sla_norm_out_forward(ctypes.byref(q), _ORDERS[order], px[0], px[2], pg[0], pg[2],
+                                      pr[0], pr[2], ps, pw, _raw(out), _raw(rstd), raw))
+    if used is not None:
+        _record(used, x, weight, gate, residual, scale)
+    return out, rstd
+
+
+def sla_norm_out_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                          rstd: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                          scale: Optional[torch.Tensor] = None, order: str = "gate_first",
+                          stream=None):
+    """Gradients of (x, gate or None, weight, scale or None) from that of out, which is the
+    residual's as it stands; the other arguments are the forward call's."""
+    if order not in _ORDERS:
+        raise ValueError(f"order must be one of {sorted(_ORDERS)}, got {order!r}")
+    _like_x(gate, "gate", x, x.dtype)
+    q = _norm_shape(x, grad_out.dtype, 0.0)
+    pt = _param_dtype(x)
+    px, pg = _rows_of(x, "x", q.dim), _rows_of(gate, "gate", q.dim)
+    pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
+    po = _dense(grad_out, "grad_out", x.shape, grad_out.dtype)
+    pd = _dense(rstd, "rstd", x.shape[:-1], pt)
+    dev = _device_of((("grad_out", grad_out), ("x", x), ("weight", weight), ("rstd", rstd),
+                      ("gate", gate), ("scale", scale)))
+    n_work = _norm_sizes(q)
+    raw, ctx, used = _enter(dev, stream)
+    with ctx:
+        dx, dw = _like(x), _like(weight)
+        dgate = _like(gate) if gate is not None else None
+        dscale = _like(scale) if scale is not None else None
+        work = _scratch(n_work, dev)
+    _check(lib().sla_norm_out_backward(ctypes.byref(q), _ORDERS[order], po, px[0], px[2], pg[0],
+                                       pg[2], ps, pw, pd, _raw(dx), _raw(dgate), _raw(dw),
+                                       _raw(dscale), _raw(work), n_work, raw))
+    if used is not None:
+        _record(used, grad_out, x, weight, rstd, gate, scale)
+    return dx, dgate, dw, dscale

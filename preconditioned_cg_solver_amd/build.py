@@ -17,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsla.so")
 LIB_DEBUG = os.path.join(PKG, "libsla_debug.so")
 SOURCES = ["setup.hip", "solver.hip", "multi.hip", "noalloc.hip", "linrec.hip", "adamw.hip",
+           "selscan.hip", "selscan_back.hip", "conv.hip", "norm_in.hip", "norm_out.hip",
            "host_util.cpp", "spectrum.cpp", "trace.cpp", "api.cpp"]
 ARCH = os.environ.get("SLA_OFFLOAD_ARCH", "gfx950")
 

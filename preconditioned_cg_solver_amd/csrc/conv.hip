@@ -1,0 +1,597 @@
+// Short causal convolutions along a sequence, per channel, and their adjoint.
+//
+// Both directions are bound by bytes: x in and y out; x and dL/dy in and dL/dx out.
+// A thread has V neighbouring channels and walks a run of steps with the last
+// inputs in registers, so each is read once but for the few before a run; the
+// loads of a group of steps are on their way together.  Backward it also carries the
+// unfinished sums of dL/dx, and works pre and its slope out again.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "rowsum.h"
+
+namespace sla {
+namespace {
+
+constexpr int kLanes = 64;
+
+template <typename T>
+struct ConvArgs {
+  using C = typename Compute<T>::type;
+  const T *x, *state, *grad_y, *grad_last;
+  int64_t x_seq, x_step, gy_seq, gy_step;
+  const C *weight, *bias;
+  T *y, *last, *grad_x, *grad_state;
+  C* part;  // [workgroup row][tap, then bias][channel]
+  const int64_t* offsets;
+  int64_t n_seq, steps, dim;
+  int64_t before;  // workgroups of earlier launches of the call
+  int blocks;      // of 64 lanes' channels
+  int run;         // steps of a thread
+  int64_t runs;    // of a sequence (packed: of all)
+  int64_t all;     // runs of the call
+  bool silu;
+  bool inlined;    // whoever walks a sequence's last step writes its last state
+};
+
+// The sequence that a step is in.
+struct Seq {
+  int64_t s, begin, end;
+};
+template <typename T>
+__device__ __forceinline__ Seq seq_at(const ConvArgs<T>& p, int64_t dense, int64_t t) {
+  if (!p.offsets) return {dense, 0, p.steps};
+  const int64_t s = sequence_of(p.offsets, p.n_seq, t);
+  return {s, p.offsets[s], p.offsets[s + 1]};
+}
+
+// A thread's run of steps.
+struct Run {
+  int64_t dense, t0, t1, at, col;
+  bool some;
+};
+template <int V, typename T>
+__device__ __forceinline__ Run run_of(const ConvArgs<T>& p) {
+  const int64_t k = p.before + blockIdx.x;
+  const int64_t run = k / p.blocks * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Run r;
+  r.col = (k % p.blocks * kLanes + (threadIdx.x & 63)) * V;
+  r.some = run < p.all && r.col < p.dim;
+  r.dense = p.offsets ? 0 : run / p.runs;
+  r.t0 = (run - r.dense * p.runs) * p.run;
+  r.t1 = min(r.t0 + p.run, p.steps);
+  r.at = p.offsets ? 0 : r.dense * p.steps;
+  return r;
+}
+
+// The input at time t of a sequence, or what its state holds there.
+template <int K, int V, typename T>
+__device__ __forceinline__ Pack<T, V> input_at(const ConvArgs<T>& p, const T* x, const Seq& q,
+                                               int64_t t, int64_t col) {
+  Pack<T, V> r{};
+  if (t >= q.begin) {
+    if (t >= 0) r = *(const Pack<T, V>*)(x + t * p.x_step);
+  } else if (p.state) {
+    const int64_t j = min(max(t - q.begin + K - 1, (int64_t)0), (int64_t)(K - 2));
+    r = *(const Pack<T, V>*)(p.state + (q.s * (K - 1) + j) * p.dim + col);
+  }
+  return r;
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
+  using C = typename Compute<T>::type;
+  constexpr int U = 8;
+  const Run r = run_of<V>(p);
+  if (!r.some) return;
+  C w[K][V], bias[V], past[K - 1][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][v] = p.weight[(r.col + v) * K + k];
+    bias[v] = p.bias ? p.bias[r.col + v] : C(0);
+  }
+  Seq q = seq_at(p, r.dense, r.t0);
+  const T* const x = p.x + r.dense * p.x_seq + r.col;
+  T* const y = p.y + r.at * p.dim + r.col;
+  auto look_back = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const auto o = input_at<K, V>(p, x, q, t - (K - 1) + j, r.col);
+#pragma unroll
+      for (int v = 0; v < V; ++v) past[j][v] = (C)o.v[v];
+    }
+  };
+  Pack<T, V> in[U];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      in[i] = *(const Pack<T, V>*)(x + min(t + i, r.t1 - 1) * p.x_step);
+  };
+  fetch(r.t0);
+  look_back(r.t0);
+  for (int64_t t = r.t0; t < r.t1; t += U) {
+    if (t > r.t0) fetch(t);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (t + i >= r.t1) break;
+      if (p.offsets && t + i == q.end) {
+        q = seq_at(p, r.dense, t + i);
+        look_back(t + i);
+      }
+      Pack<T, V> o;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const C now = (C)in[i].v[v];
+        C pre = bias[v];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) pre += w[k][v] * past[k][v];
+        pre += w[K - 1][v] * now;
+        o.v[v] = (T)(p.silu ? silu(pre) : pre);
+#pragma unroll
+        for (int k = 0; k + 1 < K - 1; ++k) past[k][v] = past[k + 1][v];
+        past[K - 2][v] = now;
+      }
+      *(Pack<T, V>*)(y + (t + i) * p.dim) = o;
+    }
+  }
+  if (p.inlined && p.last && r.t1 == p.steps) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      Pack<T, V> o;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o.v[v] = (T)past[j][v];
+      *(Pack<T, V>*)(p.last + (r.dense * (K - 1) + j) * p.dim + r.col) = o;
+    }
+  }
+}
+
+// The last states of all sequences; backward (BACK) the gradients of the states of
+// those without steps, which are the last states'.
+template <typename T, int K, int V, bool BACK>
+__global__ __launch_bounds__(kWG) void conv_last(ConvArgs<T> p) {
+  const int64_t per = p.dim / V, k = (p.before + blockIdx.x) * kWG + threadIdx.x;
+  if (k >= p.n_seq * per) return;
+  Seq q{k / per, 0, p.steps};
+  const int64_t col = k % per * V;
+  if (p.offsets) {
+    q.begin = min(max(p.offsets[q.s], (int64_t)0), p.steps);
+    q.end = min(max(p.offsets[q.s + 1], q.begin), p.steps);
+  }
+  const T* const x = p.x + (p.offsets ? 0 : q.s * p.x_seq) + col;
+  Pack<T, V> o[K - 1];
+  if constexpr (BACK) {
+    if (q.begin != q.end) return;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+      o[j] = p.grad_last
+                 ? *(const Pack<T, V>*)(p.grad_last + (q.s * (K - 1) + j) * p.dim + col)
+                 : Pack<T, V>{};
+  } else {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) o[j] = input_at<K, V>(p, x, q, q.end - (K - 1) + j, col);
+  }
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j)
+    *(Pack<T, V>*)((BACK ? p.grad_state : p.last) + (q.s * (K - 1) + j) * p.dim + col) = o[j];
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
+  using C = typename Compute<T>::type;
+  constexpr int U = 8;
+  __shared__ C red[kWaves - 1][kLanes * V];
+  const Run r = run_of<V>(p);
+  C dw[K + 1][V];  // the bias's last
+#pragma unroll
+  for (int k = 0; k <= K; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw[k][v] = C(0);
+  if (r.some) {
+    C w[K][V], bias[V], past[K - 1][V], sum[K][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k][v] = p.weight[(r.col + v) * K + k], sum[k][v] = C(0);
+      bias[v] = p.bias ? p.bias[r.col + v] : C(0);
+    }
+    Seq q = seq_at(p, r.dense, r.t0);
+    const T* const x = p.x + r.dense * p.x_seq + r.col;
+    const T* const gy = p.grad_y ? p.grad_y + r.dense * p.gy_seq + r.col : nullptr;
+    T* const gx = p.grad_x + r.at * p.dim + r.col;
+    auto look_back = [&](int64_t t) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const auto o = input_at<K, V>(p, x, q, t - (K - 1) + j, r.col);
+#pragma unroll
+        for (int v = 0; v < V; ++v) past[j][v] = (C)o.v[v];
+      }
+    };
+    // The gradient at time t of sequence q, if this thread is the one to write it: its
+    // run holds the step, or for the state the sequence's first.
+    auto emit = [&](int64_t t, const C (&g)[V]) {
+      T* to;
+      if (t >= q.begin) {
+        if (t < r.t0 || t >= r.t1) return;
+        to = gx + t * p.dim;
+      } else {
+        const int64_t j = t - q.begin + K - 1;
+        if (!p.grad_state || q.begin < r.t0 || q.begin >= r.t1 || j < 0) return;
+        to = p.grad_state + (q.s * (K - 1) + j) * p.dim + r.col;
+      }
+      Pack<T, V> o;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o.v[v] = (T)g[v];
+      *(Pack<T, V>*)to = o;
+    };
+    // what is left at the end of a sequence
+    auto finish = [&]() {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        if (p.grad_last) {
+          const auto o =
+              *(const Pack<T, V>*)(p.grad_last + (q.s * (K - 1) + j) * p.dim + r.col);
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[j][v] += (C)o.v[v];
+        }
+        emit(q.end - (K - 1) + j, sum[j]);
+      }
+    };
+    const int64_t stop = min(r.t1 + K - 1, p.steps);
+    Pack<T, V> in[U], up[U];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t at = min(t + i, stop - 1);
+        in[i] = *(const Pack<T, V>*)(x + at * p.x_step);
+        if (gy) up[i] = *(const Pack<T, V>*)(gy + at * p.gy_step);
+        else up[i] = Pack<T, V>{};
+      }
+    };
+    fetch(r.t0);
+    look_back(r.t0);
+    bool done = false;
+    for (int64_t t = r.t0; t < stop && !done; t += U) {
+      if (t > r.t0) fetch(t);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t at = t + i;
+        if (done || at >= stop) break;
+        if (p.offsets && at == q.end) {
+          finish();
+          if (at >= r.t1) {
+            done = true;
+            break;
+          }
+          q = seq_at(p, r.dense, at);
+          look_back(at);
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum[k][v] = C(0);
+        }
+        const bool own = at < r.t1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const C now = (C)in[i].v[v];
+          C pre = bias[v], g = (C)up[i].v[v];
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) pre += w[k][v] * past[k][v];
+          pre += w[K - 1][v] * now;
+          if (p.silu) {
+            C slope;
+            silu(pre, slope);
+            g *= slope;
+          }
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            sum[k][v] += w[k][v] * g;
+            if (own) dw[k][v] += g * (k < K - 1 ? past[k < K - 1 ? k : 0][v] : now);
+          }
+          if (own) dw[K][v] += g;
+#pragma unroll
+          for (int k = 0; k + 1 < K - 1; ++k) past[k][v] = past[k + 1][v];
+          past[K - 2][v] = now;
+        }
+        emit(at - (K - 1), sum[0]);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[k][v] = k + 1 < K ? sum[k + 1 < K ? k + 1 : k][v] : C(0);
+      }
+    }
+    if (!done && stop == q.end) finish();
+  }
+  // over the workgroup's runs, and one row of parts for it
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  C* const to = p.part + (p.before + blockIdx.x) / p.blocks * (K + 1) * p.dim + r.col;
+#pragma unroll
+  for (int k = 0; k <= K; ++k) {
+    if (wave)
+#pragma unroll
+      for (int v = 0; v < V; ++v) red[wave - 1][v * kLanes + lane] = dw[k][v];
+    __syncthreads();
+    if (!wave && r.col < p.dim) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        C s = dw[k][v];
+#pragma unroll
+        for (int o = 0; o < kWaves - 1; ++o) s += red[o][v * kLanes + lane];
+        to[k * p.dim + v] = s;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The parts of the weights' gradients summed: 64 channels of a tap a workgroup,
+// the waves taking a part of the rows each.
+template <typename C>
+__global__ __launch_bounds__(kSumWaves * 64) void conv_sum(const C* part, int64_t rows,
+                                                           int64_t dim, int width, C* grad_w,
+                                                           C* grad_b) {
+  __shared__ C red[kSumWaves][kLanes];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t col = (int64_t)blockIdx.x * kLanes + lane;
+  const int k = blockIdx.y;
+  const int64_t each = (rows + kSumWaves - 1) / kSumWaves;
+  const int64_t r0 = wave * each, r1 = min(r0 + each, rows);
+  const int64_t step = (width + 1) * dim;
+  C s = C(0);
+  if (col < dim) {
+    const C* const from = part + k * dim + col;
+#pragma unroll 8
+    for (int64_t r = r0; r < r1; ++r) s += from[r * step];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave || col >= dim) return;
+#pragma unroll
+  for (int o = 1; o < kSumWaves; ++o) s += red[o][lane];
+  if (k < width) grad_w[col * width + k] = s;
+  else if (grad_b) grad_b[col] = s;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+sla_status refuse(const char* msg) {
+  set_error(msg);
+  return SLA_ERR_INVALID_ARG;
+}
+
+sla_status check_shape(const sla_conv_shape* q) {
+  if (!q) return refuse("shape is NULL");
+  if (q->n_seq < 0 || q->steps < 0 || q->dim < 0) return refuse("negative size");
+  if (q->dtype != SLA_F64 && q->dtype != SLA_F32 && q->dtype != SLA_BF16 && q->dtype != SLA_F16)
+    return refuse("unknown dtype");
+  if (q->act != SLA_ACT_NONE && q->act != SLA_ACT_SILU) return refuse("unknown activation");
+  if (q->width < 2 || q->width > 4) {
+    set_error("a convolution has 2 to 4 taps");
+    return SLA_ERR_UNSUPPORTED;
+  }
+  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 28) || q->steps >= ((int64_t)1 << 40) ||
+      (__int128)(q->d_offsets ? 1 : q->n_seq) * (q->steps + 64) * (q->dim + 64) >=
+          ((__int128)1 << 58) ||
+      (__int128)q->n_seq * q->dim >= ((__int128)1 << 58)) {
+    set_error("sizes beyond what a call can index");
+    return SLA_ERR_UNSUPPORTED;
+  }
+  return SLA_OK;
+}
+
+bool empty(const sla_conv_shape& q) { return q.n_seq == 0 || q.dim == 0; }
+
+// Channels of a thread: what 16 bytes hold forward, 8 backward.
+template <typename T>
+constexpr int most_v(bool backward) {
+  return std::max(1, (backward ? 8 : 16) / (int)sizeof(T));
+}
+
+struct Cut {
+  int run;
+  int64_t runs, all, rows;
+  int blocks;
+};
+Cut cut_of(const sla_conv_shape& q, int v, bool backward) {
+  Cut c;
+  c.blocks = (int)((q.dim + kLanes * v - 1) / (kLanes * v));
+  const int64_t seqs = q.d_offsets ? 1 : q.n_seq;
+  // waves that fill the device a few times over, of runs that look back seldom
+  const int64_t want = std::max<int64_t>(1, 8192 / ((int64_t)c.blocks * seqs));
+  const int64_t run = (q.steps + want - 1) / want;
+  c.run = (int)std::min<int64_t>(std::max<int64_t>((run + 7) / 8 * 8, 8), backward ? 128 : 64);
+  c.runs = (q.steps + c.run - 1) / c.run;
+  c.all = c.runs * seqs;
+  c.rows = (c.all + kWaves - 1) / kWaves;
+  return c;
+}
+
+bool packs(const void* p, int64_t seq, int64_t step, size_t bytes, int v, bool one_seq,
+           bool one_step) {
+  return (uintptr_t)p % (v * bytes) == 0 && (seq % v == 0 || one_seq) &&
+         (step % v == 0 || one_step);
+}
+
+size_t work_bytes_of(const sla_conv_shape& q) {
+  if (empty(q) || q.steps == 0) return 0;
+  // whichever number of channels a thread takes
+  int64_t rows = 0;
+  const int most = q.dtype == SLA_F64 || q.dtype == SLA_F32 ? (q.dtype == SLA_F64 ? 1 : 2) : 4;
+  for (int v : {1, most}) rows = std::max(rows, cut_of(q, v, true).rows);
+  return align_up((size_t)rows * (q.width + 1) * q.dim * (q.dtype == SLA_F64 ? 8 : 4));
+}
+
+template <typename T, typename F>
+sla_status in_launches(ConvArgs<T>& p, int64_t groups, F&& launch) {
+  constexpr int64_t kMost = ((int64_t)1 << 32) / kWG - 1;
+  for (int64_t at = 0; at < groups; at += kMost) {
+    p.before = at;
+    launch(dim3((unsigned)std::min(groups - at, kMost)));
+    SLA_HIP(hipGetLastError());
+  }
+  return SLA_OK;
+}
+
+// Calls f(type, taps, channels of a thread).
+template <typename F>
+sla_status with_types(const sla_conv_shape& q, F&& f) {
+  auto taps = [&](auto t) {
+    return q.width == 2   ? f(t, std::integral_constant<int, 2>{})
+           : q.width == 3 ? f(t, std::integral_constant<int, 3>{})
+                          : f(t, std::integral_constant<int, 4>{});
+  };
+  switch (q.dtype) {
+    case SLA_F64: return taps(double{});
+    case SLA_F32: return taps(float{});
+    case SLA_BF16: return taps(bf16_t{});
+    default: return taps(f16_t{});
+  }
+}
+
+template <typename T>
+ConvArgs<T> args_of(const sla_conv_shape& q, const void* x, int64_t xs, int64_t xt, const void* w,
+                    const void* b, const void* state) {
+  using C = typename Compute<T>::type;
+  ConvArgs<T> p{};
+  p.x = (const T*)x, p.x_seq = q.d_offsets ? 0 : xs, p.x_step = xt;
+  p.weight = (const C*)w, p.bias = (const C*)b, p.state = (const T*)state;
+  p.offsets = q.d_offsets;
+  p.n_seq = q.n_seq, p.steps = q.steps, p.dim = q.dim;
+  p.silu = q.act == SLA_ACT_SILU;
+  return p;
+}
+template <typename T>
+void set_cut(ConvArgs<T>& p, const Cut& c) {
+  p.blocks = c.blocks, p.run = c.run, p.runs = c.runs, p.all = c.all;
+}
+
+}  // namespace
+}  // namespace sla
+
+using namespace sla;
+
+extern "C" {
+
+sla_status sla_conv_sizes(const sla_conv_shape* shape, size_t* work_bytes) {
+  const sla_status st = check_shape(shape);
+  if (st != SLA_OK) return st;
+  if (!work_bytes) return refuse("NULL result");
+  *work_bytes = work_bytes_of(*shape);
+  return SLA_OK;
+}
+
+sla_status sla_conv_forward(const sla_conv_shape* shape, const void* d_x, int64_t x_seq_stride,
+                            int64_t x_step_stride, const void* d_weight, const void* d_bias,
+                            const void* d_state, void* d_y, void* d_last, void* stream) {
+  sla_status st = check_shape(shape);
+  if (st != SLA_OK) return st;
+  const sla_conv_shape& q = *shape;
+  if (x_seq_stride < 0 || x_step_stride < 0) return refuse("negative stride");
+  if (empty(q)) return SLA_OK;
+  if (q.steps && (!d_x || !d_weight || !d_y)) return refuse("x, weight or y is NULL");
+  if (q.steps && (d_y == d_x || d_y == d_state || d_y == d_last || d_last == d_x))
+    return refuse("an output must not be an input");
+  TraceRange tr("sla_conv_forward");
+  return with_types(q, [&](auto t, auto taps) -> sla_status {
+    using T = decltype(t);
+    constexpr int K = decltype(taps)::value, M = most_v<T>(false);
+    const hipStream_t s = (hipStream_t)stream;
+    ConvArgs<T> p = args_of<T>(q, d_x, x_seq_stride, x_step_stride, d_weight, d_bias, d_state);
+    p.y = (T*)d_y, p.last = (T*)d_last;
+    const size_t b = sizeof(T);
+    const bool wide =
+        q.dim % M == 0 && q.dim >= kLanes * M &&
+        packs(d_x, x_seq_stride, x_step_stride, b, M, q.d_offsets || q.n_seq == 1, q.steps == 1) &&
+        packs(d_y, 0, 0, b, M, true, true) && packs(d_state, 0, 0, b, M, true, true) &&
+        packs(d_last, 0, 0, b, M, true, true);
+    const Cut c = cut_of(q, wide ? M : 1, false);
+    set_cut(p, c);
+    // A state updated in place is read by a sequence's first run and written by its
+    // last: by one thread if they are one, else when all have read it.
+    p.inlined = !q.d_offsets && q.steps && (d_last != d_state || c.runs == 1);
+    sla_status e = SLA_OK;
+    if (q.steps)
+      e = in_launches(p, c.rows * c.blocks, [&](dim3 grid) {
+        if (wide) conv_forward<T, K, M><<<grid, kWG, 0, s>>>(p);
+        else conv_forward<T, K, 1><<<grid, kWG, 0, s>>>(p);
+      });
+    if (e != SLA_OK || !d_last || p.inlined) return e;
+    return in_launches(p, (q.n_seq * (q.dim / (wide ? M : 1)) + kWG - 1) / kWG, [&](dim3 grid) {
+      if (wide) conv_last<T, K, M, false><<<grid, kWG, 0, s>>>(p);
+      else conv_last<T, K, 1, false><<<grid, kWG, 0, s>>>(p);
+    });
+  });
+}
+
+sla_status sla_conv_backward(const sla_conv_shape* shape, const void* d_x, int64_t x_seq_stride,
+                             int64_t x_step_stride, const void* d_weight, const void* d_bias,
+                             const void* d_state, const void* d_grad_y, int64_t grad_seq_stride,
+                             int64_t grad_step_stride, const void* d_grad_last, void* d_grad_x,
+                             void* d_grad_weight, void* d_grad_bias, void* d_grad_state,
+                             void* d_work, size_t work_bytes, void* stream) {
+  sla_status st = check_shape(shape);
+  if (st != SLA_OK) return st;
+  const sla_conv_shape& q = *shape;
+  if (x_seq_stride < 0 || x_step_stride < 0 || grad_seq_stride < 0 || grad_step_stride < 0)
+    return refuse("negative stride");
+  if (q.dim == 0) return SLA_OK;
+  if (!d_grad_weight) return refuse("the weight's gradient is NULL");
+  const bool work = !empty(q) && q.steps;
+  if (work && (!d_x || !d_weight || !d_grad_x)) return refuse("x, weight or grad_x is NULL");
+  if (work)
+    for (const void* a : {d_x, d_state, d_grad_y, d_grad_last})
+      if (a && (a == d_grad_x || a == d_grad_state))
+        return refuse("a gradient must not be an input");
+  if (d_grad_state && d_grad_state == d_grad_x)
+    return refuse("the gradients must be distinct arrays");
+  const size_t need = work_bytes_of(q);
+  if (need && (!d_work || work_bytes < need)) return refuse("workspace too small");
+  if ((uintptr_t)d_work & 255) return refuse("the workspace must be 256-byte aligned");
+  TraceRange tr("sla_conv_backward");
+  return with_types(q, [&](auto t, auto taps) -> sla_status {
+    using T = decltype(t);
+    using C = typename Compute<T>::type;
+    constexpr int K = decltype(taps)::value, M = most_v<T>(true);
+    const hipStream_t s = (hipStream_t)stream;
+    ConvArgs<T> p = args_of<T>(q, d_x, x_seq_stride, x_step_stride, d_weight, d_bias, d_state);
+    p.grad_y = (const T*)d_grad_y, p.grad_last = (const T*)d_grad_last;
+    p.gy_seq = q.d_offsets ? 0 : grad_seq_stride, p.gy_step = grad_step_stride;
+    p.grad_x = (T*)d_grad_x, p.grad_state = (T*)d_grad_state, p.part = (C*)d_work;
+    const size_t b = sizeof(T);
+    const bool one = q.d_offsets || q.n_seq == 1;
+    const bool wide =
+        q.dim % M == 0 && q.dim >= kLanes * M &&
+        packs(d_x, x_seq_stride, x_step_stride, b, M, one, q.steps == 1) &&
+        packs(d_grad_y, grad_seq_stride, grad_step_stride, b, M, one, q.steps == 1) &&
+        packs(d_grad_x, 0, 0, b, M, true, true) && packs(d_state, 0, 0, b, M, true, true) &&
+        packs(d_grad_last, 0, 0, b, M, true, true) && packs(d_grad_state, 0, 0, b, M, true, true);
+    Cut c{};
+    sla_status e = SLA_OK;
+    if (work) {
+      c = cut_of(q, wide ? M : 1, true);
+      set_cut(p, c);
+      e = in_launches(p, c.rows * c.blocks, [&](dim3 grid) {
+        if (wide) conv_backward<T, K, M><<<grid, kWG, 0, s>>>(p);
+        else conv_backward<T, K, 1><<<grid, kWG, 0, s>>>(p);
+      });
+    }
+    if (e == SLA_OK && d_grad_state && q.n_seq && (q.d_offsets || !q.steps))
+      e = in_launches(p, (q.n_seq * q.dim + kWG - 1) / kWG, [&](dim3 grid) {
+        conv_last<T, K, 1, true><<<grid, kWG, 0, s>>>(p);
+      });
+    if (e != SLA_OK) return e;
+    const dim3 grid((unsigned)((q.dim + kLanes - 1) / kLanes), (unsigned)q.width + 1);
+    conv_sum<C><<<grid, kSumWaves * 64, 0, s>>>(p.part, c.rows, q.dim, (int)q.width, (C*)d_grad_weight,
+                                     (C*)d_grad_bias);
+    SLA_HIP(hipGetLastError());
+    return SLA_OK;
+  });
+}
+
+}  // extern "C"

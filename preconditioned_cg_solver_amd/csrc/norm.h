@@ -1,0 +1,345 @@
+// Kernels of the norms before (IN) and after a block, forward and backward.
+//
+// Bound by bytes: each element is read once and kept in registers between the sum
+// over its row and what follows.  A team of waves has a row; it walks many rows, so
+// that a lane's weights stay in registers, and backward so do the sums over rows
+// that are the weights' gradients.  Rows too wide for that, or not in packs, are
+// read again (from the caches) where they are needed a second time.
+#pragma once
+
+#include <algorithm>
+
+#include "rowsum.h"
+
+namespace sla {
+namespace norm {
+
+template <typename T, typename R>
+struct Args {
+  using C = typename Compute<T>::type;
+  const T *x, *gate, *grad_y;       // grad_y: IN
+  const R *residual, *grad_r;       // grad_r: IN, of r; OUT, of out
+  const C *scale, *weight;
+  T *y, *grad_x, *grad_gate;
+  R *r, *grad_residual;             // r: OUT, out
+  C *rstd, *part_weight, *part_scale;
+  int64_t rows, dim, x_row, gate_row, residual_row;
+  C eps;
+  bool norm_first;
+};
+
+// The sum over a team of W waves, in every lane.
+template <int W, typename C>
+__device__ __forceinline__ C team_sum(C v, C (&red)[2][16], int& turn) {
+  v += from_lane<kXor1>(v);
+  v += from_lane<kXor2>(v);
+  v += from_lane<kRor4>(v);
+  v += from_lane<kRor8>(v);
+  v = fold_rows(v, v);
+  v = fold_halves(v, v);
+  if constexpr (W > 1) {
+    // two buffers in turn: one barrier a sum
+    if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[turn][0];
+#pragma unroll
+    for (int o = 1; o < W; ++o) v += red[turn][o];
+    turn ^= 1;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float inverse_root(float v) { return __builtin_amdgcn_rsqf(v); }
+__device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
+
+// The elements of a row that a lane takes together.
+template <typename T, typename R, int V>
+struct Cells {
+  Pack<T, V> x, g;  // g: the gate, or IN backward dL/dy
+  Pack<R, V> res, gr;
+};
+template <typename C, int V>
+struct Weights {
+  C weight[V], scale[V];
+};
+
+// W waves a row; NP packs of V elements a lane (0: as many as there are, not kept).
+template <typename T, typename R, bool IN, bool BACK, int V, int W, int NP>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(Args<T, R> p) {
+  using C = typename Compute<T>::type;
+  using Cell = Cells<T, R, V>;
+  constexpr int TEAMS = W == 1 ? 4 : 1, N = NP ? NP : 1, STEP = 64 * W * V;
+  __shared__ C red[2][16];
+  int turn = 0;
+  const int team = W == 1 ? threadIdx.x >> 6 : 0;
+  const int first = (int)(threadIdx.x - team * 64 * W) * V;
+  const bool kept = NP > 0;
+  const int64_t slot = (int64_t)blockIdx.x * TEAMS + team, slots = (int64_t)gridDim.x * TEAMS;
+
+  auto weights_at = [&](int64_t col) {
+    Weights<C, V> w;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w.weight[v] = p.weight[col + v];
+      w.scale[v] = p.scale ? p.scale[col + v] : C(1);
+    }
+    return w;
+  };
+  auto load = [&](int64_t row, int64_t col) {
+    Cell c{};
+    c.x = *(const Pack<T, V>*)(p.x + row * p.x_row + col);
+    if (IN && p.residual) c.res = *(const Pack<R, V>*)(p.residual + row * p.residual_row + col);
+    if (!IN && p.gate) c.g = *(const Pack<T, V>*)(p.gate + row * p.gate_row + col);
+    if (BACK) {
+      if (IN) c.g = *(const Pack<T, V>*)(p.grad_y + row * p.dim + col);
+      if (p.grad_r) c.gr = *(const Pack<R, V>*)(p.grad_r + row * p.dim + col);
+    } else if (!IN && p.residual) {
+      c.res = *(const Pack<R, V>*)(p.residual + row * p.residual_row + col);
+    }
+    return c;
+  };
+  // what is normed
+  auto under = [&](const Cell& c, const Weights<C, V>& w, int v) {
+    C u = (C)c.x.v[v];
+    if constexpr (IN) {
+      if (p.scale) u *= w.scale[v];
+      if (p.residual) u += (C)c.res.v[v];
+    } else {
+      if (p.gate && !p.norm_first) u *= silu((C)c.g.v[v]);
+    }
+    return u;
+  };
+  // backward: dL/d(u / rms), and the factor of the weight's gradient with u / rms
+  auto pull = [&](const Cell& c, const Weights<C, V>& w, int v, C& factor) {
+    if constexpr (IN) {
+      factor = (C)c.g.v[v];
+    } else {
+      factor = (C)c.gr.v[v] * w.scale[v];
+      if (p.gate && p.norm_first) factor *= silu((C)c.g.v[v]);
+    }
+    return factor * w.weight[v];
+  };
+
+  Weights<C, V> wr[N];
+  C dw[N][V], ds[N][V];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (kept && first + k * STEP < p.dim) wr[k] = weights_at(first + k * STEP);
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw[k][v] = ds[k][v] = C(0);
+  }
+  // Calls f(pack, cells, weights) for each of the lane's packs of a row.
+  auto each = [&](int64_t row, Cell (&held)[N], auto&& f) {
+    if constexpr (kept) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (first + k * STEP < p.dim) f(k, (int64_t)first + k * STEP, held[k], wr[k]);
+    } else {
+      for (int64_t col = first; col < p.dim; col += STEP)
+        f(0, col, load(row, col), weights_at(col));
+    }
+  };
+  C* const pw = BACK ? p.part_weight + slot * p.dim : nullptr;
+  C* const ps = BACK && p.part_scale ? p.part_scale + slot * p.dim : nullptr;
+  if (BACK && !kept)
+    for (int64_t col = first; col < p.dim; col += STEP)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        pw[col + v] = C(0);
+        if (ps) ps[col + v] = C(0);
+      }
+
+  for (int64_t row = slot; row < p.rows; row += slots) {
+    Cell held[N];
+    if constexpr (kept) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (first + k * STEP < p.dim) held[k] = load(row, first + k * STEP);
+    }
+    C sum = C(0);
+    if constexpr (!BACK) {
+      each(row, held, [&](int, int64_t, const Cell& c, const Weights<C, V>& w) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const C u = under(c, w, v);
+          sum += u * u;
+        }
+      });
+      sum = team_sum<W>(sum, red, turn);
+      const C rstd = inverse_root(sum / (C)p.dim + p.eps);
+      if (first == 0 && p.rstd) p.rstd[row] = rstd;
+      each(row, held, [&](int, int64_t col, const Cell& c, const Weights<C, V>& w) {
+        Pack<T, V> oy;
+        Pack<R, V> orr;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const C u = under(c, w, v);
+          C n = u * rstd * w.weight[v];
+          if constexpr (IN) {
+            oy.v[v] = (T)n;
+            orr.v[v] = (R)u;
+          } else {
+            if (p.gate && p.norm_first) n *= silu((C)c.g.v[v]);
+            if (p.scale) n *= w.scale[v];
+            if (p.residual) n += (C)c.res.v[v];
+            orr.v[v] = (R)n;
+          }
+        }
+        if (IN) *(Pack<T, V>*)(p.y + row * p.dim + col) = oy;
+        if (p.r) *(Pack<R, V>*)(p.r + row * p.dim + col) = orr;
+      });
+    } else {
+      const C rstd = p.rstd[row];
+      each(row, held, [&](int, int64_t, const Cell& c, const Weights<C, V>& w) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          C factor;
+          sum += pull(c, w, v, factor) * (under(c, w, v) * rstd);
+        }
+      });
+      const C mean = team_sum<W>(sum, red, turn) / (C)p.dim;
+      each(row, held, [&](int k, int64_t col, const Cell& c, const Weights<C, V>& w) {
+        Pack<T, V> ox, og;
+        Pack<R, V> orr;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          C factor;
+          const C g = pull(c, w, v, factor), xv = (C)c.x.v[v];
+          const C hat = under(c, w, v) * rstd;
+          C du = rstd * (g - hat * mean);
+          C aw = factor * hat, as;
+          if constexpr (IN) {
+            if (p.grad_r) du += (C)c.gr.v[v];
+            orr.v[v] = (R)du;
+            as = du * xv;
+            ox.v[v] = (T)(p.scale ? du * w.scale[v] : du);
+          } else {
+            C slope = C(0), s = C(1);
+            if (p.gate) s = silu((C)c.g.v[v], slope);
+            as = (C)c.gr.v[v] * hat * w.weight[v];
+            if (p.norm_first) {
+              as *= s;
+              og.v[v] = (T)((C)c.gr.v[v] * w.scale[v] * hat * w.weight[v] * slope);
+              ox.v[v] = (T)du;
+            } else {
+              og.v[v] = (T)(du * xv * slope);
+              ox.v[v] = (T)(du * s);
+            }
+          }
+          if constexpr (kept) {
+            dw[k][v] += aw;
+            ds[k][v] += as;
+          } else {
+            pw[col + v] += aw;
+            if (ps) ps[col + v] += as;
+          }
+        }
+        *(Pack<T, V>*)(p.grad_x + row * p.dim + col) = ox;
+        if (IN && p.grad_residual)
+          *(Pack<R, V>*)(p.grad_residual + row * p.dim + col) = orr;
+        if (!IN && p.gate) *(Pack<T, V>*)(p.grad_gate + row * p.dim + col) = og;
+      });
+    }
+  }
+  if constexpr (BACK && kept) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (first + k * STEP < p.dim)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          pw[first + k * STEP + v] = dw[k][v];
+          if (ps) ps[first + k * STEP + v] = ds[k][v];
+        }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+sla_status refuse(const char* msg);
+sla_status check_shape(const sla_norm_shape* q);
+// Workgroups at most.
+constexpr int kMostGroups = 1024;
+size_t work_bytes_of(const sla_norm_shape& q);
+bool packs(const void* p, int64_t row, size_t bytes, int v, bool one);
+
+// How a row is taken: elements of a pack, waves, packs of a lane (0: read again).
+struct Way {
+  int v, w, np;
+};
+template <typename T>
+Way way_of(int64_t dim, bool wide) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (wide) {
+    if (dim <= 64 * V) return {V, 1, 1};
+    if (dim <= 256 * V) return {V, 4, 1};
+    if (dim <= 512 * V) return {V, 4, 2};
+    if (dim <= 1024 * V) return {V, 16, 1};
+    if (dim <= 2048 * V) return {V, 16, 2};
+    return {V, 16, 0};
+  }
+  if (dim <= 1024) return {1, 4, 4};
+  if (dim <= 4096) return {1, 16, 4};
+  return {1, 16, 0};
+}
+// Workgroups, and teams (rows of the gradients' parts).
+inline int64_t groups_of(const Way& w, int64_t rows) {
+  const int64_t teams = w.w == 1 ? 4 : 1;
+  return std::min<int64_t>((rows + teams - 1) / teams, w.w == 16 ? kMostGroups / 2 : kMostGroups);
+}
+
+template <typename T, typename R, bool IN, bool BACK>
+sla_status run(Args<T, R>& p, const Way& way, hipStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const unsigned grid = (unsigned)groups_of(way, p.rows);
+#define SLA_NORM_CASE(v_, w_, np_)                                                          \
+  if (way.v == v_ && way.w == w_ && way.np == np_)                                          \
+    norm_rows<T, R, IN, BACK, v_, w_, np_><<<grid, w_ == 1 ? 256 : w_ * 64, 0, s>>>(p)
+  SLA_NORM_CASE(V, 1, 1);
+  else SLA_NORM_CASE(V, 4, 1);
+  else SLA_NORM_CASE(V, 4, 2);
+  else SLA_NORM_CASE(V, 16, 1);
+  else SLA_NORM_CASE(V, 16, 2);
+  else SLA_NORM_CASE(V, 16, 0);
+  else SLA_NORM_CASE(1, 4, 4);
+  else SLA_NORM_CASE(1, 16, 4);
+  else SLA_NORM_CASE(1, 16, 0);
+#undef SLA_NORM_CASE
+  SLA_HIP(hipGetLastError());
+  return SLA_OK;
+}
+
+// Calls f with the types of elements and of the residual stream.
+template <typename F>
+sla_status with_types(const sla_norm_shape& q, F&& f) {
+  switch (q.dtype) {
+    case SLA_F64: return f(double{}, double{});
+    case SLA_F32: return f(float{}, float{});
+    case SLA_BF16: return q.stream == SLA_F32 ? f(bf16_t{}, float{}) : f(bf16_t{}, bf16_t{});
+    default: return q.stream == SLA_F32 ? f(f16_t{}, float{}) : f(f16_t{}, f16_t{});
+  }
+}
+
+// Runs the backward kernel, then sums the parts of the gradients of weight and scale.
+template <typename T, typename R, bool IN>
+sla_status run_back(const sla_norm_shape& q, Args<T, R>& p, bool wide, void* work, void* weight,
+                    void* scale, hipStream_t s) {
+  using C = typename Compute<T>::type;
+  RowSums<C> r{};
+  if (q.rows) {
+    const Way way = way_of<T>(q.dim, wide);
+    r.rows = groups_of(way, q.rows) * (way.w == 1 ? 4 : 1);
+    p.part_weight = (C*)work;
+    p.part_scale = scale ? p.part_weight + r.rows * q.dim : nullptr;
+    const sla_status st = run<T, R, IN, true>(p, way, s);
+    if (st != SLA_OK) return st;
+  }
+  r.part[0] = p.part_weight, r.part[1] = p.part_scale;
+  r.out[0] = (C*)weight, r.out[1] = (C*)scale;
+  r.n[0] = r.n[1] = r.stride[0] = r.stride[1] = q.dim;
+  return sum_of_rows(r, s);
+}
+
+}  // namespace norm
+}  // namespace sla

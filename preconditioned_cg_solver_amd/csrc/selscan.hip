@@ -1,0 +1,476 @@
+// Selective scans, forward: h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t per
+// channel and state, y_t = C_t . h_t + D x_t, gated by z.
+//
+// Per state and step the scan takes a product, an exponential, a product and two
+// fused sums, so with 16 states it is bound by arithmetic, not bytes.  A lane keeps
+// its states in registers through all steps; what depends on the channel alone
+// (softplus, the gate) is worked out once per element in another sharing of the
+// tile among the lanes, and handed over through LDS of the wave.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "selscan.h"
+
+namespace sla {
+namespace selscan {
+namespace {
+
+template <typename C>
+struct Drive {
+  C delta, dx;  // delta_t, delta_t x_t
+};
+
+// FULL writes the outputs from the state that enters the chunk; otherwise what
+// the chunk leaves from nothing, for the joining.
+template <typename T, int NS, bool PAD, bool FULL>
+__global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
+  using C = typename Compute<T>::type;
+  using R = Rows<C>;
+  constexpr int TS = R::TS, EL = R::EL;
+  __shared__ Drive<C> s_drive[kWavesOf][TS][kChannels];
+  __shared__ C s_b[kWavesOf][TS][4 * NS], s_c[FULL ? kWavesOf : 1][TS][4 * NS];
+  __shared__ C s_sum[FULL ? kWavesOf : 1][TS][kChannels];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const Place w = place_of<T, kWavesOf>(p);
+  if (w.some <= 0) return;
+  auto& drive = s_drive[wave];
+  auto& bs = s_b[wave];
+  auto& cs = s_c[FULL ? wave : 0];
+  auto& sums = s_sum[FULL ? wave : 0];
+
+  // the lane's channel and states
+  const int q = lane >> 4, c = lane & 15;
+  const bool live = c < w.some;
+  const int64_t channel = w.channel + c;
+  C a2[NS], h[NS], total = C(0);
+  get_states<NS, PAD>(a2, p.a, channel, p.states, q, live);
+#pragma unroll
+  for (int j = 0; j < NS; ++j) a2[j] *= C(1.4426950408889634);
+  bool cut = false;
+  {
+    const bool first = !p.offsets && w.t0 == 0;
+    const C* from = FULL ? (p.chunks > 1 ? p.ends : first ? p.h0 : nullptr)
+                         : (first ? p.h0 : nullptr);
+    const int64_t row = FULL && p.chunks > 1 ? w.row : w.seq;
+    get_states<NS, PAD>(h, from, row * p.dim + channel, p.states, q, live);
+    cut = first;
+  }
+
+  // its share of the rows
+  const int r = lane / R::PER, cc = lane % R::PER * EL, some = w.some - cc;
+  const int64_t col = w.channel + (some > 0 ? cc : 0);
+  C bias[EL], dd[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) {
+    bias[e] = p.bias && e < some ? p.bias[col + e] : C(0);
+    dd[e] = FULL && p.d && e < some ? p.d[col + e] : C(0);
+  }
+  const T* const x0 = p.x + w.seq * p.x_seq + col;
+  const T* const u0 = p.dt + w.seq * p.dt_seq + col;
+  const T* const z0 = p.z ? p.z + w.seq * p.z_seq + col : nullptr;
+  const T* const b0 = p.b + w.seq * p.b_seq + w.group * p.states;
+  const T* const c0 = p.c + w.seq * p.c_seq + w.group * p.states;
+  Pack<T, EL> xr, ur, zr{};
+  Pack<T, Shared<C, NS>::BL> br, cr{};
+  auto fetch = [&](int64_t t0) {
+    const int n = (int)min((int64_t)TS, w.t1 - t0);
+    const int64_t t = t0 + (r < n ? r : 0);
+    xr = load_some<EL>(x0 + t * p.x_step, some, p.vec);
+    ur = load_some<EL>(u0 + t * p.dt_step, some, p.vec);
+    br = load_shared<C, NS>(p, b0 + t0 * p.b_step, p.b_step, n);
+    if constexpr (FULL) {
+      if (z0) zr = load_some<EL>(z0 + t * p.z_step, some, p.vec);
+      cr = load_shared<C, NS>(p, c0 + t0 * p.c_step, p.c_step, n);
+    }
+  };
+  fetch(w.t0);
+  Span now = p.offsets ? span_of(p, w, w.t0) : Span{};
+
+  for (int64_t t0 = w.t0; t0 < w.t1; t0 += TS) {
+    const int n = (int)min((int64_t)TS, w.t1 - t0);
+    const Pack<T, EL> x = xr, z = zr;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      C slope, delta = (C)ur.v[e] + bias[e];
+      if (p.softplus) delta = softplus(delta, slope);
+      drive[r][cc + e] = {delta, delta * (C)x.v[e]};
+    }
+    keep_shared<C, NS>(bs, br);
+    if constexpr (FULL) keep_shared<C, NS>(cs, cr);
+    if (t0 + TS < w.t1) fetch(t0 + TS);
+    unsigned starts, ends;
+    edges_of<TS>(p, w, now, t0, n, starts, ends);
+    if (!p.offsets) starts = 0;  // h holds what enters
+    auto begin = [&](int i) {
+      const int64_t s = span_of(p, w, t0 + i).seq;
+      get_states<NS, PAD>(h, p.h0, s * p.dim + channel, p.states, q, live);
+      cut = true;
+    };
+    if (starts & 1) begin(0);
+    if (FULL && p.saved)
+      put_states<NS, PAD>(h, p.saved + ((p.offsets ? 0 : w.seq * p.tiles) + t0 / TS) * p.dim *
+                                           p.states,
+                          channel, p.states, q, live);
+    wave_sync();
+    C sum = C(0);
+    auto step = [&](int i) {
+      const Drive<C> d = drive[i][c];
+      C s = C(0);
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        h[j] = pow2(d.delta * a2[j]) * h[j] + d.dx * bs[i][q * NS + j];
+        if constexpr (FULL) {
+          const C v = cs[i][q * NS + j] * h[j];
+          s += !PAD || q * NS + j < p.states ? v : C(0);
+        }
+      }
+      if constexpr (!FULL) sum += d.delta;
+      return s;
+    };
+    if (n == TS && !starts && !ends) {
+#pragma unroll
+      for (int i = 0; i < TS; i += 4) {
+        C s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = step(i + k);
+        if constexpr (FULL)
+          sums[i + ((q >> 1) | ((q & 1) << 1))][c] =
+              fold_rows(fold_halves(s[0], s[1]), fold_halves(s[2], s[3]));
+      }
+    } else {
+      for (int i = 0; i < n; ++i) {
+        if (i > 0 && (starts >> i & 1)) begin(i);
+        C s = step(i);
+        if constexpr (FULL) {
+          s = fold_halves(s, s);
+          sums[i][c] = fold_rows(s, s);
+          if (ends >> i & 1) {
+            const int64_t at = span_of(p, w, t0 + i).seq;
+            put_states<NS, PAD>(h, p.h_last, at * p.dim + channel, p.states, q, live);
+          }
+        }
+      }
+    }
+    total += sum;
+    wave_sync();
+    if constexpr (FULL) {
+      if (r < n) {
+        Pack<T, EL> y;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          C v = sums[r][cc + e];
+          if (p.d) v += dd[e] * (C)x.v[e];
+          if (z0) v *= silu((C)z.v[e]);
+          y.v[e] = (T)v;
+        }
+        store_some<EL>(p.y + (w.at + t0 + r) * p.dim + col, y, some, p.vec);
+      }
+      wave_sync();
+    }
+  }
+  if constexpr (!FULL) {
+    put_states<NS, PAD>(h, p.ends, w.row * p.dim + channel, p.states, q, live);
+    if (q == 0 && live) p.deltas[w.row * p.dim + channel] = total;
+    if (threadIdx.x == 0 && w.block == 0) p.cuts[w.row] = cut;
+  }
+}
+
+// h e^(a sum), for exponents whose power leaves the range where the product does
+// not: in four factors, none of them 0, so that a state that is not finite
+// stays so; one that is 0 stays 0.
+template <typename C>
+__device__ __forceinline__ C carried(C h, C a, C sum) {
+  constexpr C kLow = sizeof(C) == 8 ? C(-1022) : C(-126);
+  const C e = a == C(0) ? C(0) : a * sum * C(1.4426950408889634 / 4);
+  const C f = pow2(max(e, kLow));
+  return h == C(0) ? C(0) : h * f * f * f * f;
+}
+
+// Follows each state through the chunks, in place: what a chunk leaves from
+// nothing becomes what enters it.  A thread has one state of a sequence (packed: of
+// all); the loads of eight chunks are on their way together.
+template <typename T, bool BACKWARD>
+__global__ __launch_bounds__(kWG) void scan_join(Args<T> p) {
+  using C = typename Compute<T>::type;
+  const int64_t per = p.dim * p.states;
+  const int64_t k = (p.before + blockIdx.x) * kWG + threadIdx.x;
+  const int64_t seq = k / per, at = k % per;
+  if (seq >= (p.offsets ? 1 : p.n_seq)) return;
+  const int64_t channel = at / p.states;
+  const C a = p.a[at];
+  const C* start = BACKWARD ? p.grad_last : p.h0;
+  C h = !p.offsets && start ? start[seq * per + at] : C(0);
+  constexpr int U = 8;
+  for (int i = 0; i < p.chunks; i += U) {
+    C end[U], sum[U];
+    bool cut[U];
+    int64_t row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(i + u, p.chunks - 1);
+      row[u] = seq * p.chunks + (BACKWARD ? p.chunks - 1 - j : j);
+      end[u] = p.ends[row[u] * per + at];
+      sum[u] = p.deltas[row[u] * p.dim + channel];
+      cut[u] = p.cuts[row[u]];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= p.chunks) break;
+      p.ends[row[u] * per + at] = h;
+      h = cut[u] ? end[u] : carried(h, a, sum[u]) + end[u];
+    }
+  }
+}
+
+// Sequences without steps leave the state that they began with.
+template <typename C>
+__global__ __launch_bounds__(kWG) void scan_empty(const int64_t* offsets, int64_t n_seq,
+                                                  int64_t per, const C* from, C* to) {
+  for (int64_t s = blockIdx.x; s < n_seq; s += gridDim.x) {
+    if (offsets && offsets[s + 1] > offsets[s]) continue;
+    for (int64_t i = threadIdx.x; i < per; i += kWG)
+      to[s * per + i] = from ? from[s * per + i] : C(0);
+  }
+}
+
+}  // namespace
+
+sla_status refuse(const char* msg) {
+  set_error(msg);
+  return SLA_ERR_INVALID_ARG;
+}
+bool empty(const sla_selscan_shape& q) { return q.n_seq == 0 || q.dim == 0; }
+bool no_steps(const sla_selscan_shape& q) { return empty(q) || q.steps == 0; }
+
+sla_status check_shape(const sla_selscan_shape* q) {
+  if (!q) return refuse("shape is NULL");
+  if (q->n_seq < 0 || q->steps < 0 || q->dim < 0) return refuse("negative size");
+  if (q->dtype != SLA_F64 && q->dtype != SLA_F32 && q->dtype != SLA_BF16 && q->dtype != SLA_F16)
+    return refuse("unknown dtype");
+  if (q->softplus != 0 && q->softplus != 1) return refuse("softplus must be 0 or 1");
+  if (q->groups < 1 || q->dim % q->groups) return refuse("the groups must divide the channels");
+  if (q->n_state < 1) return refuse("a channel needs a state");
+  const int64_t seqs = q->d_offsets ? 1 : q->n_seq;
+  if (q->n_state > 16) {
+    set_error("at most 16 states a channel");
+    return SLA_ERR_UNSUPPORTED;
+  }
+  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 26) || q->steps >= ((int64_t)1 << 40) ||
+      (__int128)seqs * (q->steps + 16) * (q->dim + 64) * 16 >= ((__int128)1 << 59) ||
+      (__int128)q->n_seq * q->dim * 16 >= ((__int128)1 << 59)) {
+    set_error("sizes beyond what a call can index");
+    return SLA_ERR_UNSUPPORTED;
+  }
+  return SLA_OK;
+}
+
+Plan plan_of(const sla_selscan_shape& q, bool backward) {
+  Plan p;
+  if (no_steps(q)) return p;
+  const int64_t per = q.dim / q.groups, seqs = q.d_offsets ? 1 : q.n_seq;
+  const int ts = tile_steps(q);
+  p.blocks = (int)(q.groups * ((per + kChannels * kWavesOf - 1) / (kChannels * kWavesOf)));
+  p.tiles = (q.steps + ts - 1) / ts;
+  const int64_t waves = seqs * q.groups * ((per + kChannels - 1) / kChannels);
+  // TODO measure
+  (void)backward;
+  int64_t chunks = 1;
+  if (waves < 512) chunks = std::min((2048 + waves - 1) / waves, (p.tiles + 3) / 4);
+  // 2^31 steps of a chunk are more than any chunk has, also of one a sequence
+  const int64_t least = (q.steps >> 30) + 1;
+  chunks = std::max(chunks, least);
+  const int64_t tiles = (p.tiles + chunks - 1) / chunks;
+  p.chunk = (int)(tiles * ts);
+  p.chunks = (int)((p.tiles + tiles - 1) / tiles);
+  p.rows = seqs * p.chunks;
+  return p;
+}
+
+Work work_of(const sla_selscan_shape& q, bool backward) {
+  Work w;
+  if (no_steps(q)) return w;
+  const Plan p = plan_of(q, backward);
+  const size_t size = q.dtype == SLA_F64 ? 8 : 4, rows = (size_t)p.rows;
+  const size_t states = align_up(rows * q.dim * q.n_state * size);
+  const size_t channels = align_up(rows * q.dim * size);
+  if (p.chunks > 1) {
+    w.deltas_at = states;
+    w.cuts_at = w.deltas_at + channels;
+    w.bytes = w.cuts_at + align_up(rows * sizeof(int));
+  }
+  if (backward) {
+    const size_t all = (size_t)(q.d_offsets ? 1 : q.n_seq) * q.steps;
+    w.a_at = w.bytes;
+    w.d_at = w.a_at + states;
+    w.bias_at = w.d_at + channels;
+    w.bc_at = w.bias_at + channels;
+    w.bytes = w.bc_at + align_up((size_t)p.blocks * all * 2 * q.n_state * size);
+  }
+  return w;
+}
+
+bool packs(const void* p, int64_t seq, int64_t step, size_t bytes, int v, bool one_seq,
+           bool one_step) {
+  return (uintptr_t)p % (v * bytes) == 0 && (seq % v == 0 || one_seq) &&
+         (step % v == 0 || one_step);
+}
+
+template <typename T>
+Args<T> args_of(const sla_selscan_shape& q, const sla_selscan_in& in, const Plan& plan,
+                const Work& w, void* work) {
+  using C = typename Compute<T>::type;
+  Args<T> p{};
+  const bool packed = q.d_offsets != nullptr;
+  p.x = (const T*)in.d_x, p.x_seq = packed ? 0 : in.x_seq, p.x_step = in.x_step;
+  p.dt = (const T*)in.d_dt, p.dt_seq = packed ? 0 : in.dt_seq, p.dt_step = in.dt_step;
+  p.z = (const T*)in.d_z, p.z_seq = packed ? 0 : in.z_seq, p.z_step = in.z_step;
+  p.b = (const T*)in.d_b, p.b_seq = packed ? 0 : in.b_seq, p.b_step = in.b_step;
+  p.c = (const T*)in.d_c, p.c_seq = packed ? 0 : in.c_seq, p.c_step = in.c_step;
+  p.a = (const C*)in.d_a, p.d = (const C*)in.d_d, p.bias = (const C*)in.d_dt_bias;
+  p.h0 = (const C*)in.d_h0;
+  p.offsets = q.d_offsets;
+  p.n_seq = q.n_seq, p.steps = q.steps, p.dim = q.dim;
+  p.states = (int)q.n_state, p.groups = (int)q.groups, p.group_dim = q.dim / q.groups;
+  p.blocks = plan.blocks, p.chunk = plan.chunk, p.chunks = plan.chunks, p.tiles = plan.tiles;
+  p.softplus = q.softplus;
+  const bool one = packed || q.n_seq == 1, step = q.steps == 1;
+  const int el = tile_steps(q) * kChannels / kLanes, ns = q.n_state <= 4 ? 1 : q.n_state <= 8 ? 2 : 4;
+  const int bl = std::max(1, 4 * ns * tile_steps(q) / kLanes);
+  const size_t b = sizeof(T);
+  p.vec = p.group_dim % el == 0 && packs(in.d_x, in.x_seq, in.x_step, b, el, one, step) &&
+          packs(in.d_dt, in.dt_seq, in.dt_step, b, el, one, step) &&
+          (!in.d_z || packs(in.d_z, in.z_seq, in.z_step, b, el, one, step));
+  p.bc_vec = p.states == 4 * ns && packs(in.d_b, in.b_seq, in.b_step, b, bl, one, step) &&
+             packs(in.d_c, in.c_seq, in.c_step, b, bl, one, step);
+  char* base = (char*)work;
+  p.ends = (C*)base, p.deltas = (C*)(base + w.deltas_at), p.cuts = (int*)(base + w.cuts_at);
+  p.part_a = (C*)(base + w.a_at), p.part_d = (C*)(base + w.d_at);
+  p.part_bias = (C*)(base + w.bias_at), p.part_bc = (C*)(base + w.bc_at);
+  return p;
+}
+
+template <typename T>
+sla_status join(const Args<T>& p, const Plan& plan, bool backward, hipStream_t s) {
+  if (plan.chunks < 2) return SLA_OK;
+  Args<T> a = p;
+  const int64_t n = (p.offsets ? 1 : p.n_seq) * p.dim * p.states;
+  return in_launches(a, (n + kWG - 1) / kWG, [&](dim3 grid) {
+    if (backward) scan_join<T, true><<<grid, kWG, 0, s>>>(a);
+    else scan_join<T, false><<<grid, kWG, 0, s>>>(a);
+  });
+}
+
+template <typename C>
+sla_status leave_empty(const sla_selscan_shape& q, const void* from, void* to, hipStream_t s) {
+  const unsigned grid = (unsigned)std::min<int64_t>(q.n_seq, 4096);
+  scan_empty<C><<<grid, kWG, 0, s>>>(q.d_offsets, q.n_seq, q.dim * q.n_state, (const C*)from,
+                                     (C*)to);
+  SLA_HIP(hipGetLastError());
+  return SLA_OK;
+}
+template sla_status leave_empty<float>(const sla_selscan_shape&, const void*, void*, hipStream_t);
+template sla_status leave_empty<double>(const sla_selscan_shape&, const void*, void*, hipStream_t);
+
+#define SLA_SELSCAN_TYPES(T)                                                                   \
+  template Args<T> args_of<T>(const sla_selscan_shape&, const sla_selscan_in&, const Plan&,    \
+                              const Work&, void*);                                             \
+  template sla_status join<T>(const Args<T>&, const Plan&, bool, hipStream_t);
+SLA_SELSCAN_TYPES(double)
+SLA_SELSCAN_TYPES(float)
+SLA_SELSCAN_TYPES(bf16_t)
+SLA_SELSCAN_TYPES(f16_t)
+
+sla_status check_in(const sla_selscan_shape& q, const sla_selscan_in* in) {
+  if (!in) return refuse("inputs are NULL");
+  for (int64_t s : {in->x_seq, in->x_step, in->dt_seq, in->dt_step, in->z_seq, in->z_step,
+                    in->b_seq, in->b_step, in->c_seq, in->c_step})
+    if (s < 0) return refuse("negative stride");
+  if (!no_steps(q) && (!in->d_x || !in->d_dt || !in->d_a || !in->d_b || !in->d_c))
+    return refuse("x, dt, A, B or C is NULL");
+  return SLA_OK;
+}
+
+sla_status check_work(size_t need, const void* work, size_t bytes) {
+  if (need && (!work || bytes < need)) return refuse("workspace too small");
+  if ((uintptr_t)work & 255) return refuse("the workspace must be 256-byte aligned");
+  return SLA_OK;
+}
+
+}  // namespace selscan
+}  // namespace sla
+
+using namespace sla;
+using namespace sla::selscan;
+
+extern "C" {
+
+sla_status sla_selscan_sizes(const sla_selscan_shape* shape, size_t* saved_bytes,
+                             size_t* forward_bytes, size_t* backward_bytes) {
+  const sla_status st = check_shape(shape);
+  if (st != SLA_OK) return st;
+  if (!saved_bytes || !forward_bytes || !backward_bytes) return refuse("NULL result");
+  const sla_selscan_shape& q = *shape;
+  const size_t tiles = no_steps(q) ? 0 : (size_t)(q.d_offsets ? 1 : q.n_seq) *
+                                             plan_of(q, false).tiles;
+  *saved_bytes = tiles * q.dim * q.n_state * (q.dtype == SLA_F64 ? 8 : 4);
+  *forward_bytes = work_of(q, false).bytes;
+  *backward_bytes = work_of(q, true).bytes;
+  return SLA_OK;
+}
+
+sla_status sla_selscan_forward(const sla_selscan_shape* shape, const sla_selscan_in* in, void* d_y,
+                               void* d_h_last, void* d_saved, void* d_work, size_t work_bytes,
+                               void* stream) {
+  sla_status st = check_shape(shape);
+  if (st != SLA_OK) return st;
+  const sla_selscan_shape& q = *shape;
+  if ((st = check_in(q, in)) != SLA_OK) return st;
+  if (empty(q)) return SLA_OK;
+  if (!no_steps(q)) {
+    if (!d_y) return refuse("y is NULL");
+    for (const void* a : {in->d_x, in->d_dt, in->d_z, in->d_b, in->d_c})
+      if (a == d_y) return refuse("y must not be an input");
+  }
+  if (q.d_offsets && d_h_last && d_h_last == in->d_h0)
+    return refuse("packed sequences' states cannot be updated in place");
+  const Work w = work_of(q, false);
+  if ((st = check_work(w.bytes, d_work, work_bytes)) != SLA_OK) return st;
+  TraceRange tr("sla_selscan_forward");
+  const hipStream_t s = (hipStream_t)stream;
+  if (d_h_last && (q.d_offsets || q.steps == 0) && d_h_last != in->d_h0) {
+    st = q.dtype == SLA_F64 ? leave_empty<double>(q, in->d_h0, d_h_last, s)
+                            : leave_empty<float>(q, in->d_h0, d_h_last, s);
+    if (st != SLA_OK) return st;
+  }
+  if (no_steps(q)) return SLA_OK;
+  const Plan plan = plan_of(q, false);
+  return with_type(q, [&](auto t) {
+    using T = decltype(t);
+    using C = typename Compute<T>::type;
+    Args<T> p = args_of<T>(q, *in, plan, w, d_work);
+    p.y = (T*)d_y;
+    p.vec = p.vec && packs(d_y, 0, 0, sizeof(T), tile_steps(q) / 4, true, true);
+    p.h_last = (C*)d_h_last;
+    p.saved = (C*)d_saved;
+    return with_states(q.n_state, [&](auto ns, auto pad) -> sla_status {
+      constexpr int NS = decltype(ns)::value;
+      constexpr bool PAD = decltype(pad)::value;
+      const int64_t groups = plan.rows * plan.blocks;
+      if (plan.chunks > 1) {
+        sla_status e = in_launches(p, groups, [&](dim3 grid) {
+          scan_forward<T, NS, PAD, false><<<grid, kWG, 0, s>>>(p);
+        });
+        if (e == SLA_OK) e = join(p, plan, false, s);
+        if (e != SLA_OK) return e;
+      }
+      return in_launches(p, groups, [&](dim3 grid) {
+        scan_forward<T, NS, PAD, true><<<grid, kWG, 0, s>>>(p);
+      });
+    });
+  });
+}
+
+}  // extern "C"

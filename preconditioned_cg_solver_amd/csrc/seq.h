@@ -1,0 +1,134 @@
+// Parts shared by the operators along sequences: where packed sequences begin,
+// the activations and their slopes, and sums over lanes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "elem.h"
+#include "internal.h"
+
+namespace sla {
+
+// The sequence of step t: the last one that begins at t or before (the first if
+// none does), so a valid index whatever the offsets hold.
+__device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t n, int64_t t) {
+  int64_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (offsets[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Orders a wave's LDS accesses before and after it: its lanes exchange data
+// without a barrier, for LDS serves a wave's accesses in their order.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// 2^v; in fp32 results under 2^-126 are 0.
+__device__ __forceinline__ float pow2(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ double pow2(double v) { return exp2(v); }
+
+// 1 / (1 + e^-v).
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+}
+__device__ __forceinline__ double sigmoid(double v) { return 1.0 / (1.0 + exp(-v)); }
+
+// v sigmoid(v), which goes to -0 at -infinity, where the product would be NaN.
+template <typename C>
+__device__ __forceinline__ C silu(C v) {
+  return v == -C(INFINITY) ? -C(0) : v * sigmoid(v);
+}
+// The same and its slope, s (1 + v (1 - s)).
+template <typename C>
+__device__ __forceinline__ C silu(C v, C& slope) {
+  const C s = sigmoid(v);
+  const bool inf = fabs(v) == C(INFINITY);
+  slope = inf ? (v > C(0) ? C(1) : C(0)) : s + v * s * (C(1) - s);
+  return v == -C(INFINITY) ? -C(0) : v * s;
+}
+
+// log(1 + e^v), and the slope sigmoid(v).  log(w) e / (w - 1) with w = 1 + e as
+// rounded has the accuracy of log(1 + e) for every e; above 30 (fp64: 40) the sum
+// is v to the last place.
+__device__ __forceinline__ float softplus(float v, float& slope) {
+  const float e = __builtin_amdgcn_exp2f(1.44269504f * v), w = 1.0f + e;
+  const float r = __builtin_amdgcn_rcpf(w);
+  const float d = w - 1.0f;
+  const float l = 0.693147181f * __builtin_amdgcn_logf(w);
+  const float small = d == 0.0f ? e : l * (e * __builtin_amdgcn_rcpf(d));
+  const bool big = v > 30.0f;
+  slope = big ? 1.0f : e * r;
+  return big ? v : small;
+}
+__device__ __forceinline__ double softplus(double v, double& slope) {
+  const double e = exp(v);
+  const bool big = v > 40.0;
+  slope = big ? 1.0 : e / (1.0 + e);
+  return big ? v : log1p(e);
+}
+
+// Lane exchanges of either width: with the halves (the 16-lane rows) of a wave
+// swapped between two values, their sum holds in each half (row) one of the two
+// sums over a lane and its partner.
+__device__ __forceinline__ void swap_halves(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_rows(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_halves(double& a, double& b) {
+  const auto lo = __builtin_amdgcn_permlane32_swap(__double2loint(a), __double2loint(b), false,
+                                                   false);
+  const auto hi = __builtin_amdgcn_permlane32_swap(__double2hiint(a), __double2hiint(b), false,
+                                                   false);
+  a = __hiloint2double((int)hi[0], (int)lo[0]);
+  b = __hiloint2double((int)hi[1], (int)lo[1]);
+}
+__device__ __forceinline__ void swap_rows(double& a, double& b) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(__double2loint(a), __double2loint(b), false,
+                                                   false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(__double2hiint(a), __double2hiint(b), false,
+                                                   false);
+  a = __hiloint2double((int)hi[0], (int)lo[0]);
+  b = __hiloint2double((int)hi[1], (int)lo[1]);
+}
+// Both sums over pairs of lanes, 32 apart: of a in the lower half, of b in the upper.
+template <typename C>
+__device__ __forceinline__ C fold_halves(C a, C b) {
+  swap_halves(a, b);
+  return a + b;
+}
+// Both sums over pairs of lanes, 16 apart: of a in the even rows, of b in the odd.
+template <typename C>
+__device__ __forceinline__ C fold_rows(C a, C b) {
+  swap_rows(a, b);
+  return a + b;
+}
+// The value of another lane of the 16-lane row (a DPP pattern).
+template <int CTRL>
+__device__ __forceinline__ float from_lane(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double from_lane(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf, 0xf, false);
+  return __hiloint2double(hi, lo);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;             // within a quad
+constexpr int kRor4 = 0x124, kRor8 = 0x128, kRor12 = 0x12C;  // rotations of a row
+
+}  // namespace sla
