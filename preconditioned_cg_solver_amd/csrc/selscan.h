@@ -45,8 +45,7 @@ struct Args {
   int64_t tiles;      // of a sequence (packed: of all)
   int64_t before;     // workgroups of earlier launches of the call
   bool softplus;
-  bool vec;           // channels can be read and written four (fp64: two) at a time
-  bool bc_vec;        // and B and C by what a lane takes of them
+  bool fast;          // whole packs, 4, 8 or 16 states: see with_states
   // joining the chunks, [row][channel][state] and [row][channel]: what a chunk
   // leaves from nothing, then what enters it; the sum of its deltas; whether
   // what enters it does not reach its end
@@ -124,22 +123,30 @@ struct Rows {
   static constexpr int PER = kChannels / EL;  // lanes of a row
 };
 
-// EL elements from p, of which `some` exist.
-template <int EL, typename T>
-__device__ __forceinline__ Pack<T, EL> load_some(const T* p, int some, bool vec) {
+// Waits for loads of values here, and not where they are used: in a loop that would
+// be a wait for whatever was loaded last, the next tile.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(double& v) { asm volatile("" : "+v"(v)); }
+template <int N, typename C>
+__device__ __forceinline__ void settle(C (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) settle(v[j]);
+}
+
+// EL elements from p, of which `some` exist.  FAST: all of them or none, in a pack; p
+// is then valid in any case, and what is read where none exist is not used.
+template <bool FAST, int EL, typename T>
+__device__ __forceinline__ Pack<T, EL> load_some(const T* p, int some) {
+  if constexpr (FAST) return *(const Pack<T, EL>*)p;
   Pack<T, EL> r;
-  if (vec) {
-    if (some >= EL) return *(const Pack<T, EL>*)p;
-    some = 0;
-  }
 #pragma unroll
   for (int e = 0; e < EL; ++e) r.v[e] = e < some ? p[e] : T(0);
   return r;
 }
-template <int EL, typename T>
-__device__ __forceinline__ void store_some(T* p, const Pack<T, EL>& v, int some, bool vec) {
-  if (vec) {
-    if (some >= EL) *(Pack<T, EL>*)p = v;
+template <bool FAST, int EL, typename T>
+__device__ __forceinline__ void store_some(T* p, const Pack<T, EL>& v, int some) {
+  if constexpr (FAST) {
+    if (some > 0) *(Pack<T, EL>*)p = v;
     return;
   }
 #pragma unroll
@@ -155,15 +162,6 @@ struct Shared {
   static constexpr int PER = 4 * NS / BL;  // lanes of a step
 };
 template <typename C, int NS, typename T>
-__device__ __forceinline__ Pack<T, Shared<C, NS>::BL> load_shared(const Args<T>& p, const T* row,
-                                                                  int64_t step, int n) {
-  using S = Shared<C, NS>;
-  const int lane = threadIdx.x & 63, t = lane / S::PER, at = lane % S::PER * S::BL;
-  const int some = t < n ? p.states - at : 0;
-  return load_some<S::BL>(row + (int64_t)(t < n ? t : 0) * step + (some > 0 ? at : 0), some,
-                          p.bc_vec);
-}
-template <typename C, int NS, typename T>
 __device__ __forceinline__ void keep_shared(C (*to)[4 * NS], const Pack<T, Shared<C, NS>::BL>& v) {
   using S = Shared<C, NS>;
   const int lane = threadIdx.x & 63, t = lane / S::PER, at = lane % S::PER * S::BL;
@@ -172,8 +170,34 @@ __device__ __forceinline__ void keep_shared(C (*to)[4 * NS], const Pack<T, Share
   for (int e = 0; e < S::BL; ++e) to[t][at + e] = (C)v.v[e];
 }
 
+// A lane's place in the rows of an array of steps; it moves from tile to tile.  In a
+// tile of n < TS steps, lanes of the others read the last.
+template <bool FAST, int EL, typename T>
+struct Stream {
+  const T* at;
+  int64_t step, hop;
+  int row, some;
+  // `base`: the lane's first element of step 0; t0: the first tile's step.
+  __device__ __forceinline__ Stream(const T* base, int64_t step_, int64_t t0, int row_, int some_,
+                                    int hop_)
+      : at(base + (t0 + row_) * step_), step(step_), hop(hop_ * step_), row(row_), some(some_) {}
+  __device__ __forceinline__ Pack<T, EL> load(int n, int ts) const {
+    const T* p = at;
+    if (n < ts) p -= max(row - (n - 1), 0) * step;
+    return load_some<FAST, EL>(p, some);
+  }
+  __device__ __forceinline__ void move() { at += hop; }
+};
+template <bool FAST, typename C, int NS, typename T>
+__device__ __forceinline__ Stream<FAST, Shared<C, NS>::BL, T> shared_stream(
+    const Args<T>& p, const T* base, int64_t step, int64_t t0, int hop) {
+  using S = Shared<C, NS>;
+  const int lane = threadIdx.x & 63, at = lane % S::PER * S::BL, some = p.states - at;
+  return {base + (some > 0 ? at : 0), step, t0, min(lane / S::PER, S::TS - 1), some, hop};
+}
+
 // A lane's NS states in an array [..][channel][state].
-template <int NS, bool PAD, typename C>
+template <int NS, bool FAST, typename C>
 __device__ __forceinline__ void get_states(C (&h)[NS], const C* base, int64_t channel, int states,
                                            int q, bool live) {
 #pragma unroll
@@ -182,16 +206,23 @@ __device__ __forceinline__ void get_states(C (&h)[NS], const C* base, int64_t ch
   const C* at = base + channel * states + q * NS;
 #pragma unroll
   for (int j = 0; j < NS; ++j)
-    if (!PAD || q * NS + j < states) h[j] = at[j];
+    if (FAST || q * NS + j < states) h[j] = at[j];
 }
-template <int NS, bool PAD, typename C>
+// The same, waited for.
+template <int NS, bool FAST, typename C>
+__device__ __forceinline__ void enter_states(C (&h)[NS], const C* base, int64_t channel,
+                                             int states, int q, bool live) {
+  get_states<NS, FAST>(h, base, channel, states, q, live);
+  settle(h);
+}
+template <int NS, bool FAST, typename C>
 __device__ __forceinline__ void put_states(const C (&h)[NS], C* base, int64_t channel, int states,
                                            int q, bool live) {
   if (!base || !live) return;
   C* at = base + channel * states + q * NS;
 #pragma unroll
   for (int j = 0; j < NS; ++j)
-    if (!PAD || q * NS + j < states) at[j] = h[j];
+    if (FAST || q * NS + j < states) at[j] = h[j];
 }
 
 sla_status check_shape(const sla_selscan_shape* q);
@@ -228,8 +259,10 @@ sla_status in_launches(Args<T>& p, int64_t groups, F&& launch) {
   return SLA_OK;
 }
 
-// Calls f with the storage type, then with the states of a lane and whether some
-// of them do not exist.
+// Calls f with the storage type, then with the states of a lane and whether all of
+// them exist and every array can be read in packs, as most models' can: then no
+// lane asks what exists, and the loads of the next tile stay on their way through
+// the present one.
 template <typename F>
 sla_status with_type(const sla_selscan_shape& q, F&& f) {
   switch (q.dtype) {
@@ -240,13 +273,13 @@ sla_status with_type(const sla_selscan_shape& q, F&& f) {
   }
 }
 template <typename F>
-sla_status with_states(int64_t n, F&& f) {
-  auto pad = [&](auto ns) {
-    return n == 4 * decltype(ns)::value ? f(ns, std::false_type{}) : f(ns, std::true_type{});
+sla_status with_states(int64_t n, bool fast, F&& f) {
+  auto pick = [&](auto ns) {
+    return fast ? f(ns, std::true_type{}) : f(ns, std::false_type{});
   };
-  if (n <= 4) return pad(std::integral_constant<int, 1>{});
-  if (n <= 8) return pad(std::integral_constant<int, 2>{});
-  return pad(std::integral_constant<int, 4>{});
+  if (n <= 4) return pick(std::integral_constant<int, 1>{});
+  if (n <= 8) return pick(std::integral_constant<int, 2>{});
+  return pick(std::integral_constant<int, 4>{});
 }
 
 bool packs(const void* p, int64_t seq, int64_t step, size_t bytes, int v, bool one_seq,

@@ -25,7 +25,7 @@ struct Drive {
 
 // FULL writes the outputs from the state that enters the chunk; otherwise what
 // the chunk leaves from nothing, for the joining.
-template <typename T, int NS, bool PAD, bool FULL>
+template <typename T, int NS, bool FAST, bool FULL>
 __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   using C = typename Compute<T>::type;
   using R = Rows<C>;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   const bool live = c < w.some;
   const int64_t channel = w.channel + c;
   C a2[NS], h[NS], total = C(0);
-  get_states<NS, PAD>(a2, p.a, channel, p.states, q, live);
+  enter_states<NS, FAST>(a2, p.a, channel, p.states, q, live);
 #pragma unroll
   for (int j = 0; j < NS; ++j) a2[j] *= C(1.4426950408889634);
   bool cut = false;
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
     const C* from = FULL ? (p.chunks > 1 ? p.ends : first ? p.h0 : nullptr)
                          : (first ? p.h0 : nullptr);
     const int64_t row = FULL && p.chunks > 1 ? w.row : w.seq;
-    get_states<NS, PAD>(h, from, row * p.dim + channel, p.states, q, live);
+    enter_states<NS, FAST>(h, from, row * p.dim + channel, p.states, q, live);
     cut = first;
   }
 
@@ -68,88 +68,126 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
     bias[e] = p.bias && e < some ? p.bias[col + e] : C(0);
     dd[e] = FULL && p.d && e < some ? p.d[col + e] : C(0);
   }
-  const T* const x0 = p.x + w.seq * p.x_seq + col;
-  const T* const u0 = p.dt + w.seq * p.dt_seq + col;
-  const T* const z0 = p.z ? p.z + w.seq * p.z_seq + col : nullptr;
-  const T* const b0 = p.b + w.seq * p.b_seq + w.group * p.states;
-  const T* const c0 = p.c + w.seq * p.c_seq + w.group * p.states;
+  settle(bias);
+  settle(dd);
+  using Row = Stream<FAST, EL, T>;
+  Row xs(p.x + w.seq * p.x_seq + col, p.x_step, w.t0, r, some, TS);
+  Row us(p.dt + w.seq * p.dt_seq + col, p.dt_step, w.t0, r, some, TS);
+  Row zs(p.z + w.seq * p.z_seq + col, p.z_step, w.t0, r, some, TS);
+  auto bt = shared_stream<FAST, C, NS>(p, p.b + w.seq * p.b_seq + w.group * p.states, p.b_step,
+                                       w.t0, TS);
+  auto ct = shared_stream<FAST, C, NS>(p, p.c + w.seq * p.c_seq + w.group * p.states, p.c_step,
+                                       w.t0, TS);
+  const bool gated = FULL && p.z;
+  T* y = FULL ? p.y + (w.at + w.t0 + r) * p.dim + col : nullptr;
+  const int64_t tile = p.dim * p.states;
+  C* saved = FULL && p.saved ? p.saved + ((p.offsets ? 0 : w.seq * p.tiles) + w.t0 / TS) * tile
+                             : nullptr;
   Pack<T, EL> xr, ur, zr{};
   Pack<T, Shared<C, NS>::BL> br, cr{};
-  auto fetch = [&](int64_t t0) {
-    const int n = (int)min((int64_t)TS, w.t1 - t0);
-    const int64_t t = t0 + (r < n ? r : 0);
-    xr = load_some<EL>(x0 + t * p.x_step, some, p.vec);
-    ur = load_some<EL>(u0 + t * p.dt_step, some, p.vec);
-    br = load_shared<C, NS>(p, b0 + t0 * p.b_step, p.b_step, n);
+  auto fetch = [&](int n) {
+    xr = xs.load(n, TS);
+    ur = us.load(n, TS);
+    br = bt.load(n, TS);
+    xs.move(), us.move(), bt.move();
     if constexpr (FULL) {
-      if (z0) zr = load_some<EL>(z0 + t * p.z_step, some, p.vec);
-      cr = load_shared<C, NS>(p, c0 + t0 * p.c_step, p.c_step, n);
+      if (gated) zr = zs.load(n, TS);
+      cr = ct.load(n, TS);
+      zs.move(), ct.move();
     }
   };
-  fetch(w.t0);
+  int left = (int)(w.t1 - w.t0);  // steps
+  fetch(min(left, TS));
   Span now = p.offsets ? span_of(p, w, w.t0) : Span{};
 
-  for (int64_t t0 = w.t0; t0 < w.t1; t0 += TS) {
-    const int n = (int)min((int64_t)TS, w.t1 - t0);
+  for (int64_t t0 = w.t0; left > 0; t0 += TS, left -= TS) {
+    const int n = min(left, TS);
     const Pack<T, EL> x = xr, z = zr;
+    C delta[EL], slope;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) {
-      C slope, delta = (C)ur.v[e] + bias[e];
-      if (p.softplus) delta = softplus(delta, slope);
-      drive[r][cc + e] = {delta, delta * (C)x.v[e]};
-    }
+    for (int e = 0; e < EL; ++e) delta[e] = (C)ur.v[e] + bias[e];
+    if (p.softplus)
+#pragma unroll
+      for (int e = 0; e < EL; ++e) delta[e] = softplus(delta[e], slope);
+#pragma unroll
+    for (int e = 0; e < EL; ++e) drive[r][cc + e] = {delta[e], delta[e] * (C)x.v[e]};
     keep_shared<C, NS>(bs, br);
     if constexpr (FULL) keep_shared<C, NS>(cs, cr);
-    if (t0 + TS < w.t1) fetch(t0 + TS);
+    if (left > TS) fetch(min(left - TS, TS));
     unsigned starts, ends;
     edges_of<TS>(p, w, now, t0, n, starts, ends);
     if (!p.offsets) starts = 0;  // h holds what enters
     auto begin = [&](int i) {
       const int64_t s = span_of(p, w, t0 + i).seq;
-      get_states<NS, PAD>(h, p.h0, s * p.dim + channel, p.states, q, live);
+      enter_states<NS, FAST>(h, p.h0, s * p.dim + channel, p.states, q, live);
       cut = true;
     };
     if (starts & 1) begin(0);
-    if (FULL && p.saved)
-      put_states<NS, PAD>(h, p.saved + ((p.offsets ? 0 : w.seq * p.tiles) + t0 / TS) * p.dim *
-                                           p.states,
-                          channel, p.states, q, live);
+    if (FULL && saved) {
+      put_states<NS, FAST>(h, saved, channel, p.states, q, live);
+      saved += tile;
+    }
     wave_sync();
     C sum = C(0);
-    auto step = [&](int i) {
-      const Drive<C> d = drive[i][c];
+    struct Step {
+      Drive<C> d;
+      C b[NS], c[FULL ? NS : 1];
+    };
+    auto read = [&](int i) {
+      Step v;
+      v.d = drive[i][c];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        v.b[j] = bs[i][q * NS + j];
+        if constexpr (FULL) v.c[j] = cs[i][q * NS + j];
+      }
+      return v;
+    };
+    auto step = [&](const Step& v) {
       C s = C(0);
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        h[j] = pow2(d.delta * a2[j]) * h[j] + d.dx * bs[i][q * NS + j];
+        h[j] = pow2(v.d.delta * a2[j]) * h[j] + v.d.dx * v.b[j];
         if constexpr (FULL) {
-          const C v = cs[i][q * NS + j] * h[j];
-          s += !PAD || q * NS + j < p.states ? v : C(0);
+          const C m = v.c[j] * h[j];
+          s += FAST || q * NS + j < p.states ? m : C(0);
         }
       }
-      if constexpr (!FULL) sum += d.delta;
+      if constexpr (!FULL) sum += v.d.delta;
       return s;
     };
     if (n == TS && !starts && !ends) {
+      // groups of steps, the next one's operands on their way from LDS
+      constexpr int G = 4;
+      Step ahead[G];
 #pragma unroll
-      for (int i = 0; i < TS; i += 4) {
-        C s[4];
+      for (int k = 0; k < G; ++k) ahead[k] = read(k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = step(i + k);
+      for (int i = 0; i < TS; i += G) {
+        Step at[G];
+        C s[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) at[k] = ahead[k];
+        if (i + G < TS)
+#pragma unroll
+          for (int k = 0; k < G; ++k) ahead[k] = read(i + G + k);
+#pragma unroll
+        for (int k = 0; k < G; ++k) s[k] = step(at[k]);
         if constexpr (FULL)
           sums[i + ((q >> 1) | ((q & 1) << 1))][c] =
               fold_rows(fold_halves(s[0], s[1]), fold_halves(s[2], s[3]));
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       for (int i = 0; i < n; ++i) {
         if (i > 0 && (starts >> i & 1)) begin(i);
-        C s = step(i);
+        C s = step(read(i));
         if constexpr (FULL) {
           s = fold_halves(s, s);
           sums[i][c] = fold_rows(s, s);
           if (ends >> i & 1) {
             const int64_t at = span_of(p, w, t0 + i).seq;
-            put_states<NS, PAD>(h, p.h_last, at * p.dim + channel, p.states, q, live);
+            put_states<NS, FAST>(h, p.h_last, at * p.dim + channel, p.states, q, live);
           }
         }
       }
@@ -158,21 +196,26 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
     wave_sync();
     if constexpr (FULL) {
       if (r < n) {
-        Pack<T, EL> y;
+        C v[EL];
+        Pack<T, EL> o;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) {
-          C v = sums[r][cc + e];
-          if (p.d) v += dd[e] * (C)x.v[e];
-          if (z0) v *= silu((C)z.v[e]);
-          y.v[e] = (T)v;
-        }
-        store_some<EL>(p.y + (w.at + t0 + r) * p.dim + col, y, some, p.vec);
+        for (int e = 0; e < EL; ++e) v[e] = sums[r][cc + e];
+        if (p.d)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) v[e] += dd[e] * (C)x.v[e];
+        if (gated)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) v[e] *= silu((C)z.v[e]);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o.v[e] = (T)v[e];
+        store_some<FAST, EL>(y, o, some);
       }
+      y += TS * p.dim;
       wave_sync();
     }
   }
   if constexpr (!FULL) {
-    put_states<NS, PAD>(h, p.ends, w.row * p.dim + channel, p.states, q, live);
+    put_states<NS, FAST>(h, p.ends, w.row * p.dim + channel, p.states, q, live);
     if (q == 0 && live) p.deltas[w.row * p.dim + channel] = total;
     if (threadIdx.x == 0 && w.block == 0) p.cuts[w.row] = cut;
   }
@@ -278,7 +321,8 @@ Plan plan_of(const sla_selscan_shape& q, bool backward) {
   // TODO measure
   (void)backward;
   int64_t chunks = 1;
-  if (waves < 512) chunks = std::min((2048 + waves - 1) / waves, (p.tiles + 3) / 4);
+  {const char*e1=getenv("SC_MAX"),*e2=getenv("SC_WANT"); int64_t mx=e1?atoll(e1):512, wt=e2?atoll(e2):2048;
+  if (waves < mx) chunks = std::min((wt + waves - 1) / waves, (p.tiles + 3) / 4);}
   // 2^31 steps of a chunk are more than any chunk has, also of one a sequence
   const int64_t least = (q.steps >> 30) + 1;
   chunks = std::max(chunks, least);
@@ -340,11 +384,11 @@ Args<T> args_of(const sla_selscan_shape& q, const sla_selscan_in& in, const Plan
   const int el = tile_steps(q) * kChannels / kLanes, ns = q.n_state <= 4 ? 1 : q.n_state <= 8 ? 2 : 4;
   const int bl = std::max(1, 4 * ns * tile_steps(q) / kLanes);
   const size_t b = sizeof(T);
-  p.vec = p.group_dim % el == 0 && packs(in.d_x, in.x_seq, in.x_step, b, el, one, step) &&
+  p.fast = p.group_dim % el == 0 && packs(in.d_x, in.x_seq, in.x_step, b, el, one, step) &&
           packs(in.d_dt, in.dt_seq, in.dt_step, b, el, one, step) &&
           (!in.d_z || packs(in.d_z, in.z_seq, in.z_step, b, el, one, step));
-  p.bc_vec = p.states == 4 * ns && packs(in.d_b, in.b_seq, in.b_step, b, bl, one, step) &&
-             packs(in.d_c, in.c_seq, in.c_step, b, bl, one, step);
+  p.fast = p.fast && p.states == 4 * ns && packs(in.d_b, in.b_seq, in.b_step, b, bl, one, step) &&
+           packs(in.d_c, in.c_seq, in.c_step, b, bl, one, step);
   char* base = (char*)work;
   p.ends = (C*)base, p.deltas = (C*)(base + w.deltas_at), p.cuts = (int*)(base + w.cuts_at);
   p.part_a = (C*)(base + w.a_at), p.part_d = (C*)(base + w.d_at);
@@ -452,22 +496,22 @@ sla_status sla_selscan_forward(const sla_selscan_shape* shape, const sla_selscan
     using C = typename Compute<T>::type;
     Args<T> p = args_of<T>(q, *in, plan, w, d_work);
     p.y = (T*)d_y;
-    p.vec = p.vec && packs(d_y, 0, 0, sizeof(T), tile_steps(q) / 4, true, true);
+    p.fast = p.fast && packs(d_y, 0, 0, sizeof(T), tile_steps(q) / 4, true, true);
     p.h_last = (C*)d_h_last;
     p.saved = (C*)d_saved;
-    return with_states(q.n_state, [&](auto ns, auto pad) -> sla_status {
+    return with_states(q.n_state, p.fast, [&](auto ns, auto fast) -> sla_status {
       constexpr int NS = decltype(ns)::value;
-      constexpr bool PAD = decltype(pad)::value;
+      constexpr bool FAST = decltype(fast)::value;
       const int64_t groups = plan.rows * plan.blocks;
       if (plan.chunks > 1) {
         sla_status e = in_launches(p, groups, [&](dim3 grid) {
-          scan_forward<T, NS, PAD, false><<<grid, kWG, 0, s>>>(p);
+          scan_forward<T, NS, FAST, false><<<grid, kWG, 0, s>>>(p);
         });
         if (e == SLA_OK) e = join(p, plan, false, s);
         if (e != SLA_OK) return e;
       }
       return in_launches(p, groups, [&](dim3 grid) {
-        scan_forward<T, NS, PAD, true><<<grid, kWG, 0, s>>>(p);
+        scan_forward<T, NS, FAST, true><<<grid, kWG, 0, s>>>(p);
       });
     });
   });

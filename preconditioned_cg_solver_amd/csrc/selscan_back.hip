@@ -28,8 +28,10 @@ sla_status leave_empty(const sla_selscan_shape& q, const void* from, void* to, h
 
 namespace {
 
-// Steps whose instructions are scheduled together; over more of them the compiler
-// moves so many loads ahead that the states leave the registers.
+// Steps whose instructions may mix, while the operands of as many more are on their
+// way from LDS: the barriers to the scheduler put those loads first, where it would
+// put them last, and keep it from taking so many ahead that the states leave the
+// registers.
 constexpr int kAhead = 2;
 
 template <typename C>
@@ -42,7 +44,7 @@ struct Pull {
 };
 
 // What a chunk leaves to the one before it, from nothing.
-template <typename T, int NS, bool PAD>
+template <typename T, int NS, bool FAST>
 __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
   using C = typename Compute<T>::type;
   using R = Rows<C>;
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
   const bool live = c < w.some;
   const int64_t channel = w.channel + c;
   C a2[NS], mu[NS], total = C(0);
-  get_states<NS, PAD>(a2, p.a, channel, p.states, q, live);
+  enter_states<NS, FAST>(a2, p.a, channel, p.states, q, live);
 #pragma unroll
   for (int j = 0; j < NS; ++j) a2[j] *= C(1.4426950408889634), mu[j] = C(0);
   bool cut = false;
@@ -68,81 +70,114 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
   C bias[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) bias[e] = p.bias && e < some ? p.bias[col + e] : C(0);
-  const T* const u0 = p.dt + w.seq * p.dt_seq + col;
-  const T* const z0 = p.z ? p.z + w.seq * p.z_seq + col : nullptr;
-  const T* const g0 = p.grad_y + w.seq * p.gy_seq + col;
-  const T* const c0 = p.c + w.seq * p.c_seq + w.group * p.states;
+  settle(bias);
+  const int64_t last = w.t0 + (w.t1 - 1 - w.t0) / TS * TS;
+  using Row = Stream<FAST, EL, T>;
+  Row us(p.dt + w.seq * p.dt_seq + col, p.dt_step, last, r, some, -TS);
+  Row zs(p.z + w.seq * p.z_seq + col, p.z_step, last, r, some, -TS);
+  Row gs(p.grad_y + w.seq * p.gy_seq + col, p.gy_step, last, r, some, -TS);
+  auto ct = shared_stream<FAST, C, NS>(p, p.c + w.seq * p.c_seq + w.group * p.states, p.c_step,
+                                       last, -TS);
+  const bool gated = p.z != nullptr;
   Pack<T, EL> ur, zr{}, gr;
   Pack<T, Shared<C, NS>::BL> cr;
-  auto fetch = [&](int64_t t0) {
-    const int n = (int)min((int64_t)TS, w.t1 - t0);
-    const int64_t t = t0 + (r < n ? r : 0);
-    ur = load_some<EL>(u0 + t * p.dt_step, some, p.vec);
-    gr = load_some<EL>(g0 + t * p.gy_step, some, p.vec);
-    if (z0) zr = load_some<EL>(z0 + t * p.z_step, some, p.vec);
-    cr = load_shared<C, NS>(p, c0 + t0 * p.c_step, p.c_step, n);
+  auto fetch = [&](int n) {
+    ur = us.load(n, TS);
+    gr = gs.load(n, TS);
+    if (gated) zr = zs.load(n, TS);
+    cr = ct.load(n, TS);
+    us.move(), gs.move(), zs.move(), ct.move();
   };
-  const int64_t last = w.t0 + (w.t1 - 1 - w.t0) / TS * TS;
-  fetch(last);
+  fetch((int)(w.t1 - last));
   Span now = p.offsets ? span_of(p, w, last) : Span{};
   for (int64_t t0 = last; t0 >= w.t0; t0 -= TS) {
     const int n = (int)min((int64_t)TS, w.t1 - t0);
+    C delta[EL], ds[EL], slope;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) {
-      C slope, delta = (C)ur.v[e] + bias[e], ds = (C)gr.v[e];
-      if (p.softplus) delta = softplus(delta, slope);
-      if (z0) ds *= silu((C)zr.v[e]);
-      pull[r][cc + e] = {delta, ds};
-    }
+    for (int e = 0; e < EL; ++e) delta[e] = (C)ur.v[e] + bias[e], ds[e] = (C)gr.v[e];
+    if (p.softplus)
+#pragma unroll
+      for (int e = 0; e < EL; ++e) delta[e] = softplus(delta[e], slope);
+    if (gated)
+#pragma unroll
+      for (int e = 0; e < EL; ++e) ds[e] *= silu((C)zr.v[e]);
+#pragma unroll
+    for (int e = 0; e < EL; ++e) pull[r][cc + e] = {delta[e], ds[e]};
     keep_shared<C, NS>(cs, cr);
-    if (t0 > w.t0) fetch(t0 - TS);
+    if (t0 > w.t0) fetch(TS);
     unsigned starts, ends;
     edges_of<TS>(p, w, now, t0, n, starts, ends);
     wave_sync();
     C sum = C(0);
-    auto step = [&](int i) {
-      const Pull<C> d = pull[i][c];
+    struct Step {
+      Pull<C> d;
+      C c[NS];
+    };
+    auto read = [&](int i) {
+      Step v;
+      v.d = pull[i][c];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) v.c[j] = cs[i][q * NS + j];
+      return v;
+    };
+    auto step = [&](const Step& v) {
 #pragma unroll
       for (int j = 0; j < NS; ++j)
-        mu[j] = pow2(d.delta * a2[j]) * (d.ds * cs[i][q * NS + j] + mu[j]);
-      sum += d.delta;
+        mu[j] = pow2(v.d.delta * a2[j]) * (v.d.ds * v.c[j] + mu[j]);
+      sum += v.d.delta;
     };
     if (n == TS && !ends) {
+      constexpr int G = 4;
+      Step ahead[G];
 #pragma unroll
-      for (int i = TS - 1; i >= 0; --i) step(i);
+      for (int k = 0; k < G; ++k) ahead[k] = read(TS - 1 - k);
+#pragma unroll
+      for (int i = TS - 1; i >= 0; i -= G) {
+        Step at[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) at[k] = ahead[k];
+        if (i >= G)
+#pragma unroll
+          for (int k = 0; k < G; ++k) ahead[k] = read(i - G - k);
+#pragma unroll
+        for (int k = 0; k < G; ++k) step(at[k]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
       for (int i = n - 1; i >= 0; --i) {
         if (ends >> i & 1) {
           const int64_t s = span_of(p, w, t0 + i).seq;
-          get_states<NS, PAD>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
+          enter_states<NS, FAST>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
           cut = true;
         }
-        step(i);
+        step(read(i));
       }
     }
     total += sum;
     wave_sync();
   }
-  put_states<NS, PAD>(mu, p.ends, w.row * p.dim + channel, p.states, q, live);
+  put_states<NS, FAST>(mu, p.ends, w.row * p.dim + channel, p.states, q, live);
   if (q == 0 && live) p.deltas[w.row * p.dim + channel] = total;
   if (threadIdx.x == 0 && w.block == 0) p.cuts[w.row] = cut;
 }
 
-template <typename T, int NS, bool PAD>
+template <typename T, int NS, bool FAST>
 __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
   using C = typename Compute<T>::type;
   using R = Rows<C>;
   constexpr int TS = R::TS, EL = R::EL, N4 = 4 * NS;
   __shared__ Drive<C> s_drive[kWavesOf][TS][kChannels];
-  __shared__ C s_ds[kWavesOf][TS][kChannels];
+  __shared__ C s_ds[kWavesOf][TS][kChannels], s_slope[kWavesOf][TS][kChannels];
+  __shared__ C s_bias[kWavesOf][kChannels], s_d[kWavesOf][kChannels];
   __shared__ C s_b[kWavesOf][TS][N4], s_c[kWavesOf][TS][N4];
-  __shared__ C s_sum[kWavesOf][TS][3][kChannels];  // over states: C h, g B, mu h A
+  __shared__ C s_sum[kWavesOf][TS][3][kChannels];  // over states: C h, g B, mu h A / ln 2
   __shared__ C s_bc[2][kWavesOf][TS][2][N4];       // over a wave's channels: of dB, of dC
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place w = place_of<T, kWavesOf>(p);
   const bool idle = w.some <= 0;  // its workgroup's sums want it all the same
   auto& drive = s_drive[wave];
   auto& dss = s_ds[wave];
+  auto& slopes = s_slope[wave];
   auto& bs = s_b[wave];
   auto& cs = s_c[wave];
   auto& sums = s_sum[wave];
@@ -152,50 +187,56 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
   const int q = lane >> 2 & 3, c = (lane & 3) | (lane >> 4) << 2;
   const bool live = c < w.some;
   const int64_t channel = w.channel + (idle ? 0 : c);
-  C a[NS], a2[NS], mu[NS], da[NS];
-  get_states<NS, PAD>(a, p.a, channel, p.states, q, live);
+  C a2[NS], mu[NS], da[NS];
+  enter_states<NS, FAST>(a2, p.a, channel, p.states, q, live);
   {
     // what enters from the chunk that follows
     const bool end = !p.offsets && w.t1 == p.steps;
     const C* from = p.chunks > 1 && !end ? p.ends : nullptr;
-    get_states<NS, PAD>(mu, from, w.row * p.dim + channel, p.states, q, live);
+    enter_states<NS, FAST>(mu, from, w.row * p.dim + channel, p.states, q, live);
   }
 #pragma unroll
-  for (int j = 0; j < NS; ++j) a2[j] = a[j] * C(1.4426950408889634), da[j] = C(0);
+  for (int j = 0; j < NS; ++j) a2[j] *= C(1.4426950408889634), da[j] = C(0);
 
   const int r = lane / R::PER, cc = lane % R::PER * EL, some = w.some - cc;
   const int64_t col = idle ? 0 : w.channel + (some > 0 ? cc : 0);
-  C bias[EL], dd[EL], dbias[EL], ddd[EL];
+  C dbias[EL], ddd[EL];
 #pragma unroll
-  for (int e = 0; e < EL; ++e) {
-    bias[e] = p.bias && e < some ? p.bias[col + e] : C(0);
-    dd[e] = p.d && e < some ? p.d[col + e] : C(0);
-    dbias[e] = ddd[e] = C(0);
+  for (int e = 0; e < EL; ++e) dbias[e] = ddd[e] = C(0);
+  if (lane < kChannels) {
+    s_bias[wave][lane] = p.bias && lane < w.some ? p.bias[w.channel + lane] : C(0);
+    s_d[wave][lane] = p.d && lane < w.some ? p.d[w.channel + lane] : C(0);
   }
-  const T* const x0 = p.x + w.seq * p.x_seq + col;
-  const T* const u0 = p.dt + w.seq * p.dt_seq + col;
-  const T* const z0 = p.z ? p.z + w.seq * p.z_seq + col : nullptr;
-  const T* const g0 = p.grad_y + w.seq * p.gy_seq + col;
-  const T* const b0 = p.b + w.seq * p.b_seq + w.group * p.states;
-  const T* const c0 = p.c + w.seq * p.c_seq + w.group * p.states;
-  const int64_t tile0 = p.offsets ? 0 : w.seq * p.tiles;
+  wave_sync();
+  const int64_t last = w.t0 + (w.t1 - 1 - w.t0) / TS * TS;
+  using Row = Stream<FAST, EL, T>;
+  Row xs(p.x + w.seq * p.x_seq + col, p.x_step, last, r, some, -TS);
+  Row us(p.dt + w.seq * p.dt_seq + col, p.dt_step, last, r, some, -TS);
+  Row zs(p.z + w.seq * p.z_seq + col, p.z_step, last, r, some, -TS);
+  Row gs(p.grad_y + w.seq * p.gy_seq + col, p.gy_step, last, r, some, -TS);
+  auto bt = shared_stream<FAST, C, NS>(p, p.b + w.seq * p.b_seq + w.group * p.states, p.b_step,
+                                       last, -TS);
+  auto ct = shared_stream<FAST, C, NS>(p, p.c + w.seq * p.c_seq + w.group * p.states, p.c_step,
+                                       last, -TS);
+  const bool gated = p.z != nullptr;
+  const int64_t tile = p.dim * p.states;
+  const C* saved = (const C*)p.saved + ((p.offsets ? 0 : w.seq * p.tiles) + last / TS) * tile;
+  int64_t to = (w.at + last + r) * p.dim + col;
   Pack<T, EL> xr, ur, zr{}, gr;
   Pack<T, Shared<C, NS>::BL> br, cr;
   C enter[NS];  // the state at the tile's start
-  auto fetch = [&](int64_t t0) {
-    const int n = (int)min((int64_t)TS, w.t1 - t0);
-    const int64_t t = t0 + (r < n ? r : 0);
-    xr = load_some<EL>(x0 + t * p.x_step, some, p.vec);
-    ur = load_some<EL>(u0 + t * p.dt_step, some, p.vec);
-    gr = load_some<EL>(g0 + t * p.gy_step, some, p.vec);
-    if (z0) zr = load_some<EL>(z0 + t * p.z_step, some, p.vec);
-    br = load_shared<C, NS>(p, b0 + t0 * p.b_step, p.b_step, n);
-    cr = load_shared<C, NS>(p, c0 + t0 * p.c_step, p.c_step, n);
-    get_states<NS, PAD>(enter, (const C*)p.saved + (tile0 + t0 / TS) * p.dim * p.states, channel,
-                        p.states, q, live);
+  auto fetch = [&](int n) {
+    xr = xs.load(n, TS);
+    ur = us.load(n, TS);
+    gr = gs.load(n, TS);
+    if (gated) zr = zs.load(n, TS);
+    br = bt.load(n, TS);
+    cr = ct.load(n, TS);
+    get_states<NS, FAST>(enter, saved, channel, p.states, q, live);
+    xs.move(), us.move(), gs.move(), zs.move(), bt.move(), ct.move();
+    saved -= tile;
   };
-  const int64_t last = w.t0 + (w.t1 - 1 - w.t0) / TS * TS;
-  if (!idle) fetch(last);
+  if (!idle) fetch((int)(w.t1 - last));
   else {
     for (int i = lane; i < TS * 2 * N4; i += kLanes)
       (&s_bc[0][wave][0][0][0])[i] = (&s_bc[1][wave][0][0][0])[i] = C(0);
@@ -206,170 +247,218 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
   for (int64_t t0 = last; t0 >= w.t0; t0 -= TS, turn ^= 1) {
     const int n = (int)min((int64_t)TS, w.t1 - t0);
     if (!idle) {
-      const Pack<T, EL> x = xr, z = zr, gy = gr, u = ur;
-      C delta[EL], slope[EL], ds[EL];
+      const Pack<T, EL> x = xr, z = zr, gy = gr;
+      {
+        C delta[EL], slope[EL], ds[EL];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        slope[e] = C(1);
-        delta[e] = (C)u.v[e] + bias[e];
-        if (p.softplus) delta[e] = softplus(delta[e], slope[e]);
-        ds[e] = (C)gy.v[e];
-        if (z0) ds[e] *= silu((C)z.v[e]);
-        drive[r][cc + e] = {delta[e], delta[e] * (C)x.v[e]};
-        dss[r][cc + e] = ds[e];
+        for (int e = 0; e < EL; ++e)
+          slope[e] = C(1), delta[e] = (C)ur.v[e] + s_bias[wave][cc + e], ds[e] = (C)gy.v[e];
+        if (p.softplus)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) delta[e] = softplus(delta[e], slope[e]);
+        if (gated)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) ds[e] *= silu((C)z.v[e]);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          // channels that do not exist add nothing to the sums over channels
+          const bool exists = !FAST || some > 0;
+          drive[r][cc + e] = {exists ? delta[e] : C(0), exists ? delta[e] * (C)x.v[e] : C(0)};
+          dss[r][cc + e] = exists ? ds[e] : C(0);
+          slopes[r][cc + e] = slope[e];
+        }
       }
       keep_shared<C, NS>(bs, br);
       keep_shared<C, NS>(cs, cr);
       C h0[NS];
 #pragma unroll
       for (int j = 0; j < NS; ++j) h0[j] = enter[j];
-      if (t0 > w.t0) fetch(t0 - TS);
+      settle(h0);
+      if (t0 > w.t0) fetch(TS);
       unsigned starts, ends;
       edges_of<TS>(p, w, now, t0, n, starts, ends);
       wave_sync();
 
-      auto tile = [&](auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
-        C coef[TS][NS], hs[TS][NS];
-        // forward again
+      struct Step {
+        Drive<C> d;
+        C ds, b[NS], c[NS];
+      };
+      auto read = [&](int i) {
+        Step v;
+        v.d = drive[i][c];
+        v.ds = dss[i][c];
 #pragma unroll
-        for (int i = 0; i < TS; ++i) {
-          if (WHOLE || i < n) {
-            C before[NS];
+        for (int j = 0; j < NS; ++j) v.b[j] = bs[i][q * NS + j], v.c[j] = cs[i][q * NS + j];
+        return v;
+      };
+      // A step forward, from `before` to `now`, and back.
+      auto advance = [&](const Step& v, int i, const C (&before)[NS], C (&now)[NS]) {
+        C s = C(0);
 #pragma unroll
-            for (int j = 0; j < NS; ++j) before[j] = i ? hs[i ? i - 1 : 0][j] : h0[j];
-            if (!WHOLE && i > 0 && (starts >> i & 1))
-              get_states<NS, PAD>(before, p.h0, span_of(p, w, t0 + i).seq * p.dim + channel,
-                                  p.states, q, live);
-            const Drive<C> d = drive[i][c];
-            C s = C(0);
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              coef[i][j] = pow2(d.delta * a2[j]);
-              hs[i][j] = coef[i][j] * before[j] + d.dx * bs[i][q * NS + j];
-              const C v = cs[i][q * NS + j] * hs[i][j];
-              s += !PAD || q * NS + j < p.states ? v : C(0);
-            }
-            s += from_lane<kRor8>(s);
-            s += from_lane<kRor4>(s);
-            sums[i][0][c] = s;
-          } else {
-#pragma unroll
-            for (int j = 0; j < NS; ++j) coef[i][j] = hs[i][j] = C(0);
-          }
-          if (i % kAhead == kAhead - 1) __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < NS; ++j) {
+          now[j] = pow2(v.d.delta * a2[j]) * before[j] + v.d.dx * v.b[j];
+          const C m = v.c[j] * now[j];
+          s += FAST || q * NS + j < p.states ? m : C(0);
         }
-        // and back
+        s += from_lane<kRor8>(s);
+        s += from_lane<kRor4>(s);
+        sums[i][0][c] = s;
+      };
+      auto retreat = [&](const Step& v, int i, const C (&before)[NS], const C (&now)[NS]) {
+        C gb = C(0), qa = C(0), db[NS], dc[NS];
 #pragma unroll
-        for (int i = TS - 1; i >= 0; --i) {
-          if (WHOLE || i < n) {
-            C before[NS];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) before[j] = i ? hs[i ? i - 1 : 0][j] : h0[j];
-            if (!WHOLE) {
-              const bool begins = starts >> i & 1;
-              if ((ends >> i & 1) || (begins && i > 0)) {
-                const int64_t s = span_of(p, w, t0 + i).seq;
-                if (ends >> i & 1)
-                  get_states<NS, PAD>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
-                if (begins && i > 0)
-                  get_states<NS, PAD>(before, p.h0, s * p.dim + channel, p.states, q, live);
-              }
-            }
-            const Drive<C> d = drive[i][c];
-            const C dsv = dss[i][c];
-            C gb = C(0), qa = C(0), db[NS], dc[NS];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              const C g = dsv * cs[i][q * NS + j] + mu[j];
-              dc[j] = dsv * hs[i][j];
-              db[j] = g * d.dx;
-              const C v = g * bs[i][q * NS + j];
-              gb += !PAD || q * NS + j < p.states ? v : C(0);
-              mu[j] = coef[i][j] * g;
-              const C mh = mu[j] * before[j];
-              const C va = mh * a[j];
-              qa += !PAD || q * NS + j < p.states ? va : C(0);
-              da[j] += mh * d.delta;
-            }
-            if (!WHOLE && (starts >> i & 1) && p.grad_h0)
-              put_states<NS, PAD>(mu, p.grad_h0, span_of(p, w, t0 + i).seq * p.dim + channel,
-                                  p.states, q, live);
-            gb += from_lane<kRor8>(gb);
-            qa += from_lane<kRor8>(qa);
-            gb += from_lane<kRor4>(gb);
-            qa += from_lane<kRor4>(qa);
-            sums[i][1 + (q & 1)][c] = q & 1 ? qa : gb;
-            // over the channels
-            const int odd = lane >> 4 & 1, high = lane >> 5;
-            if constexpr (NS == 4) {
-              C vb = fold_rows(fold_halves(db[0], db[1]), fold_halves(db[2], db[3]));
-              C vc = fold_rows(fold_halves(dc[0], dc[1]), fold_halves(dc[2], dc[3]));
-              vb += from_lane<kXor1>(vb);
-              vc += from_lane<kXor1>(vc);
-              C v = lane & 1 ? vc : vb;
-              v += from_lane<kXor2>(v);
-              if ((lane & 2) == 0) s_bc[turn][wave][i][lane & 1][q * NS + 2 * odd + high] = v;
-            } else if constexpr (NS == 2) {
-              C v = fold_rows(fold_halves(db[0], db[1]), fold_halves(dc[0], dc[1]));
-              v += from_lane<kXor1>(v);
-              v += from_lane<kXor2>(v);
-              if ((lane & 3) == 0) s_bc[turn][wave][i][odd][q * NS + high] = v;
-            } else {
-              C v = fold_halves(db[0], dc[0]);
-              v = fold_rows(v, v);
-              v += from_lane<kXor1>(v);
-              v += from_lane<kXor2>(v);
-              if ((lane & 3) == 0 && !odd) s_bc[turn][wave][i][high][q] = v;
-            }
-          }
-          if (i % kAhead == 0) __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < NS; ++j) {
+          const C g = v.ds * v.c[j] + mu[j];
+          dc[j] = v.ds * now[j];
+          db[j] = g * v.d.dx;
+          const C m = g * v.b[j];
+          gb += FAST || q * NS + j < p.states ? m : C(0);
+          mu[j] = pow2(v.d.delta * a2[j]) * g;
+          const C mh = mu[j] * before[j];
+          const C ma = mh * a2[j];
+          qa += FAST || q * NS + j < p.states ? ma : C(0);
+          da[j] += mh * v.d.delta;
+        }
+        gb += from_lane<kRor8>(gb);
+        qa += from_lane<kRor8>(qa);
+        gb += from_lane<kRor4>(gb);
+        qa += from_lane<kRor4>(qa);
+        sums[i][1 + (q & 1)][c] = q & 1 ? qa : gb;
+        // over the channels (lanes that hold the same sum write it to the same place)
+        const int odd = lane >> 4 & 1, high = lane >> 5;
+        if constexpr (NS == 4) {
+          C vb = fold_rows(fold_halves(db[0], db[1]), fold_halves(db[2], db[3]));
+          C vc = fold_rows(fold_halves(dc[0], dc[1]), fold_halves(dc[2], dc[3]));
+          vb += from_lane<kXor1>(vb);
+          vc += from_lane<kXor1>(vc);
+          C o = lane & 1 ? vc : vb;
+          o += from_lane<kXor2>(o);
+          s_bc[turn][wave][i][lane & 1][q * NS + 2 * odd + high] = o;
+        } else if constexpr (NS == 2) {
+          C o = fold_rows(fold_halves(db[0], db[1]), fold_halves(dc[0], dc[1]));
+          o += from_lane<kXor1>(o);
+          o += from_lane<kXor2>(o);
+          s_bc[turn][wave][i][odd][q * NS + high] = o;
+        } else {
+          C o = fold_halves(db[0], dc[0]);
+          o = fold_rows(o, o);
+          o += from_lane<kXor1>(o);
+          o += from_lane<kXor2>(o);
+          s_bc[turn][wave][i][high][q] = o;
         }
       };
-      if (n == TS && !starts && !ends) tile(std::true_type{});
-      else tile(std::false_type{});
+      if (n == TS && !starts && !ends) {
+        constexpr int G = kAhead;
+        C hs[TS][NS];
+        Step at[G], ahead[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) ahead[k] = read(k);
+#pragma unroll
+        for (int i = 0; i < TS; i += G) {
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            at[k] = ahead[k];
+            if (i + G < TS) ahead[k] = read(i + G + k);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < G; ++k)
+            advance(at[k], i + k, i + k ? hs[i + k ? i + k - 1 : 0] : h0, hs[i + k]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int k = 0; k < G; ++k) ahead[k] = read(TS - 1 - k);
+#pragma unroll
+        for (int i = TS - 1; i >= 0; i -= G) {
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            at[k] = ahead[k];
+            if (i >= G) ahead[k] = read(i - G - k);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < G; ++k)
+            retreat(at[k], i - k, i - k ? hs[i - k ? i - k - 1 : 0] : h0, hs[i - k]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        // Tiles in which a sequence begins or ends, step by step; the states are in memory.
+        C hs[TS + 1][NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) hs[0][j] = h0[j];
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          C before[NS], now[NS];
+#pragma unroll
+          for (int j = 0; j < NS; ++j) before[j] = hs[i][j];
+          if (i > 0 && (starts >> i & 1))
+            enter_states<NS, FAST>(before, p.h0, span_of(p, w, t0 + i).seq * p.dim + channel,
+                                   p.states, q, live);
+          advance(read(i), i, before, now);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) hs[i + 1][j] = now[j];
+        }
+#pragma unroll 1
+        for (int i = n - 1; i >= 0; --i) {
+          const bool begins = starts >> i & 1, stops = ends >> i & 1;
+          const int64_t s = begins || stops ? span_of(p, w, t0 + i).seq : 0;
+          C before[NS], now[NS];
+#pragma unroll
+          for (int j = 0; j < NS; ++j) before[j] = hs[i][j], now[j] = hs[i + 1][j];
+          if (stops)
+            enter_states<NS, FAST>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
+          if (begins && i > 0)
+            enter_states<NS, FAST>(before, p.h0, s * p.dim + channel, p.states, q, live);
+          retreat(read(i), i, before, now);
+          if (begins && p.grad_h0)
+            put_states<NS, FAST>(mu, p.grad_h0, s * p.dim + channel, p.states, q, live);
+        }
+      }
       wave_sync();
 
       if (r < n) {
-        Pack<T, EL> ox, ou, oz;
+        C gx[EL];
+        Pack<T, EL> ox, ou, oz{};
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-          const C xv = (C)x.v[e], gb = sums[r][1][cc + e], qa = sums[r][2][cc + e];
-          const C du = (qa + xv * gb) * slope[e];
+          const C xv = (C)x.v[e], gb = sums[r][1][cc + e], ds = dss[r][cc + e];
+          const C du = (sums[r][2][cc + e] * C(0.69314718055994531) + xv * gb) * slopes[r][cc + e];
           ou.v[e] = (T)du;
           dbias[e] += du;
-          C gx = delta[e] * gb;
-          if (p.d) gx += dd[e] * ds[e];
-          ddd[e] += ds[e] * xv;
-          ox.v[e] = (T)gx;
-          if (z0) {
+          gx[e] = drive[r][cc + e].delta * gb;
+          if (p.d) gx[e] += s_d[wave][cc + e] * ds;
+          ddd[e] += ds * xv;
+          ox.v[e] = (T)gx[e];
+        }
+        if (gated)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
             C zs, s = sums[r][0][cc + e];
-            if (p.d) s += dd[e] * xv;
+            if (p.d) s += s_d[wave][cc + e] * (C)x.v[e];
             silu((C)z.v[e], zs);
             oz.v[e] = (T)((C)gy.v[e] * s * zs);
           }
-        }
-        const int64_t to = (w.at + t0 + r) * p.dim + col;
-        store_some<EL>(p.grad_x + to, ox, some, p.vec);
-        store_some<EL>(p.grad_dt + to, ou, some, p.vec);
-        if (z0) store_some<EL>(p.grad_z + to, oz, some, p.vec);
+        store_some<FAST, EL>(p.grad_x + to, ox, some);
+        store_some<FAST, EL>(p.grad_dt + to, ou, some);
+        if (gated) store_some<FAST, EL>(p.grad_z + to, oz, some);
       }
+      to -= TS * p.dim;
     }
     // One barrier a tile: the other half of s_bc is written next, and read by a
     // wave only after the barrier that follows.
-    __syncthreads();
-    C* const to = p.part_bc + ((int64_t)w.block * (p.offsets ? p.steps : p.n_seq * p.steps) +
-                               w.at + t0) * 2 * p.states;
+    lds_barrier();
+    C* const out = p.part_bc + ((int64_t)w.block * (p.offsets ? p.steps : p.n_seq * p.steps) +
+                                w.at + t0) * 2 * p.states;
     for (int k = threadIdx.x; k < n * 2 * N4; k += kWG) {
       const int i = k / (2 * N4), of = k / N4 & 1, st = k % N4;
       C v = s_bc[turn][0][i][of][st];
 #pragma unroll
       for (int o = 1; o < kWavesOf; ++o) v += s_bc[turn][o][i][of][st];
-      if (st < p.states) to[(i * 2 + of) * p.states + st] = v;
+      if (st < p.states) out[(i * 2 + of) * p.states + st] = v;
     }
   }
   if (idle) return;
-  put_states<NS, PAD>(da, p.part_a, w.row * p.dim + channel, p.states, q, live);
+  put_states<NS, FAST>(da, p.part_a, w.row * p.dim + channel, p.states, q, live);
   // over the rows' lanes
 #pragma unroll
   for (int e = 0; e < EL; ++e) {
@@ -457,25 +546,25 @@ extern "C" sla_status sla_selscan_backward(const sla_selscan_shape* shape, const
     p.grad_x = (T*)o.d_x, p.grad_dt = (T*)o.d_dt, p.grad_z = (T*)o.d_z;
     p.grad_h0 = (C*)h0;
     const int el = tile_steps(q) / 4;
-    p.vec = p.vec && packs(d_grad_y, grad_seq, grad_step, sizeof(T), el, q.d_offsets || q.n_seq == 1,
+    p.fast = p.fast && packs(d_grad_y, grad_seq, grad_step, sizeof(T), el, q.d_offsets || q.n_seq == 1,
                            q.steps == 1) &&
             packs(o.d_x, 0, 0, sizeof(T), el, true, true) &&
             packs(o.d_dt, 0, 0, sizeof(T), el, true, true) &&
             (!in->d_z || packs(o.d_z, 0, 0, sizeof(T), el, true, true));
     if (!no_steps(q)) {
       const int64_t groups = plan.rows * plan.blocks;
-      sla_status e = with_states(q.n_state, [&](auto ns, auto pad) -> sla_status {
+      sla_status e = with_states(q.n_state, p.fast, [&](auto ns, auto fast) -> sla_status {
         constexpr int NS = decltype(ns)::value;
-        constexpr bool PAD = decltype(pad)::value;
+        constexpr bool FAST = decltype(fast)::value;
         if (plan.chunks > 1) {
           sla_status e = in_launches(p, groups, [&](dim3 grid) {
-            scan_back_local<T, NS, PAD><<<grid, kWG, 0, s>>>(p);
+            scan_back_local<T, NS, FAST><<<grid, kWG, 0, s>>>(p);
           });
           if (e == SLA_OK) e = join(p, plan, true, s);
           if (e != SLA_OK) return e;
         }
         return in_launches(p, groups, [&](dim3 grid) {
-          scan_backward<T, NS, PAD><<<grid, kWG, 0, s>>>(p);
+          scan_backward<T, NS, FAST><<<grid, kWG, 0, s>>>(p);
         });
       });
       if (e != SLA_OK) return e;

@@ -29,6 +29,12 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A barrier that waits for a wave's LDS accesses but not, as __syncthreads does, for
+// its stores to memory.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // 2^v; in fp32 results under 2^-126 are 0.
 __device__ __forceinline__ float pow2(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ double pow2(double v) { return exp2(v); }
