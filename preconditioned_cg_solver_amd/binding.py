@@ -712,12 +712,12 @@ def _enter(dev: torch.device, stream):
     that their memory is not reused before the call's work is done.  A stream
     given by its raw pointer (or as ExternalStream) may not live that long: there
     the caller keeps the tensors until then."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    current = torch.cuda.current_device()
+    if dev.index is not None and dev.index != current:
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{current}")
     if stream is None:
         # current_stream() would make an object of it: 2.5 us of a serving step's 17
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _SAME_STREAM, None
+        return torch._C._cuda_getCurrentRawStream(current), _SAME_STREAM, None
     if not hasattr(stream, "cuda_stream"):
         raw = stream.value if isinstance(stream, ctypes.c_void_p) else stream
         stream = torch.cuda.ExternalStream(raw or 0, device=dev)
@@ -1138,7 +1138,6 @@ def sla_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     ps, pl = _dense(state, "state", held, x.dtype), _dense(last, "last", held, x.dtype)
     dev = _device_of((("x", x), ("weight", weight), ("bias", bias), ("state", state),
                       ("offsets", offsets), ("last", last)))
-    _conv_sizes(q)
     raw, ctx, used = _enter(dev, stream)
     given = last
     with ctx:
@@ -1196,6 +1195,7 @@ def _shared_in(t, name: str, x, q):
 
 class _Selscan:
     """The checked arguments of a selective scan."""
+    __slots__ = ("q", "pt", "held", "given", "tensors")
 
     def __init__(self, x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus):
         n, t, d = _sequences(x, offsets)
@@ -1213,19 +1213,25 @@ class _Selscan:
             _dense(A, "A", (d, q.n_state), pt), _dense(D, "D", (d,), pt),
             _dense(dt_bias, "dt_bias", (d,), pt), _dense(h0, "h0", self.held, pt))
         self.tensors = (x, dt, A, B, C, D, z, dt_bias, h0, offsets)
-        self.named = tuple(zip(("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0", "offsets"),
-                               self.tensors))
+
+    def device(self, *more):
+        return _device_of((*zip(_Selscan.NAMES, self.tensors), *more))
+
+    def sizes(self):
         s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
-        _check(lib().sla_selscan_sizes(ctypes.byref(q), ctypes.byref(s), ctypes.byref(f),
+        _check(lib().sla_selscan_sizes(ctypes.byref(self.q), ctypes.byref(s), ctypes.byref(f),
                                        ctypes.byref(b)))
-        self.sizes = s.value, f.value, b.value
+        return s.value, f.value, b.value
+
+
+_Selscan.NAMES = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0", "offsets")
 
 
 def sla_selscan_sizes(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, offsets=None,
                       softplus: bool = True) -> Tuple[int, int, int]:
     """Bytes of (the states kept for the backward pass, the forward pass's workspace, the
     backward pass's)."""
-    return _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus).sizes
+    return _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus).sizes()
 
 
 def sla_selscan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -1248,8 +1254,9 @@ def sla_selscan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
     `saved` (None unless save) is what the backward pass needs."""
     a = _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
     pl = _dense(h_last, "h_last", a.held, a.pt)
-    dev = _device_of(a.named + (("h_last", h_last),))
-    n_saved, n_work, _ = a.sizes
+    dev = a.device(("h_last", h_last))
+    # a step or two need neither
+    n_saved, n_work, _ = a.sizes() if save or a.q.steps > 2 else (0, 0, 0)
     raw, ctx, used = _enter(dev, stream)
     given = h_last
     with ctx:
@@ -1281,8 +1288,8 @@ def sla_selscan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: 
     a = _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
     pd = _steps_in(grad_y, "grad_y", x)
     pl = _dense(grad_last, "grad_last", a.held, a.pt)
-    dev = _device_of(a.named + (("saved", saved), ("grad_y", grad_y), ("grad_last", grad_last)))
-    n_saved, _, n_work = a.sizes
+    dev = a.device(("saved", saved), ("grad_y", grad_y), ("grad_last", grad_last))
+    n_saved, _, n_work = a.sizes()
     if saved.dtype != a.pt or not saved.is_contiguous() or \
             saved.numel() * a.pt.itemsize != n_saved:
         raise ValueError("saved must be the forward call's")
@@ -1367,7 +1374,6 @@ def sla_norm_in_forward(x: torch.Tensor, weight: torch.Tensor,
     px, pr = _rows_of(x, "x", q.dim), _rows_of(residual, "residual", q.dim)
     pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
     dev = _device_of((("x", x), ("weight", weight), ("residual", residual), ("scale", scale)))
-    _norm_sizes(q)
     raw, ctx, used = _enter(dev, stream)
     same = residual is None and scale is None
     with ctx:
@@ -1436,7 +1442,6 @@ def sla_norm_out_forward(x: torch.Tensor, weight: torch.Tensor,
     pw, ps = _dense(weight, "weight", (q.dim,), pt), _dense(scale, "scale", (q.dim,), pt)
     dev = _device_of((("x", x), ("weight", weight), ("gate", gate), ("residual", residual),
                       ("scale", scale)))
-    _norm_sizes(q)
     raw, ctx, used = _enter(dev, stream)
     with ctx:
         out = torch.empty(x.shape, dtype=rt, device=dev)

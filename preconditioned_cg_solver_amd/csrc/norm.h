@@ -40,7 +40,7 @@ __device__ __forceinline__ C team_sum(C v, C (&red)[2][16], int& turn) {
   if constexpr (W > 1) {
     // two buffers in turn: one barrier a sum
     if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     v = red[turn][0];
 #pragma unroll
     for (int o = 1; o < W; ++o) v += red[turn][o];
@@ -52,96 +52,100 @@ __device__ __forceinline__ C team_sum(C v, C (&red)[2][16], int& turn) {
 __device__ __forceinline__ float inverse_root(float v) { return __builtin_amdgcn_rsqf(v); }
 __device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
 
-// The elements of a row that a lane takes together.
+// The elements of a row that a lane takes together, as they were read, and what is
+// worked out of them once: the normed values and the gate's sigmoid.
 template <typename T, typename R, int V>
 struct Cells {
   Pack<T, V> x, g;  // g: the gate, or IN backward dL/dy
   Pack<R, V> res, gr;
 };
 template <typename C, int V>
+struct Made {
+  C u[V], sig[V];
+};
+template <typename C, int V>
 struct Weights {
   C weight[V], scale[V];
 };
 
-// W waves a row; NP packs of V elements a lane (0: as many as there are, not kept).
-template <typename T, typename R, bool IN, bool BACK, int V, int W, int NP>
+// W waves a row; NP packs of V elements a lane (0: as many as there are, not kept).  STREAM:
+// what is written goes past the caches.
+template <typename T, typename R, bool IN, bool BACK, int V, int W, int NP, bool STREAM>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(Args<T, R> p) {
   using C = typename Compute<T>::type;
   using Cell = Cells<T, R, V>;
+  using Make = Made<C, V>;
+  using Weight = Weights<C, V>;
   constexpr int TEAMS = W == 1 ? 4 : 1, N = NP ? NP : 1, STEP = 64 * W * V;
+  constexpr bool KEPT = NP > 0;
   __shared__ C red[2][16];
   int turn = 0;
   const int team = W == 1 ? threadIdx.x >> 6 : 0;
   const int first = (int)(threadIdx.x - team * 64 * W) * V;
-  const bool kept = NP > 0;
   const int64_t slot = (int64_t)blockIdx.x * TEAMS + team, slots = (int64_t)gridDim.x * TEAMS;
 
   auto weights_at = [&](int64_t col) {
-    Weights<C, V> w;
+    Weight w;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      w.weight[v] = p.weight[col + v];
-      w.scale[v] = p.scale ? p.scale[col + v] : C(1);
-    }
+    for (int v = 0; v < V; ++v) w.weight[v] = p.weight[col + v], w.scale[v] = C(1);
+    if (p.scale)
+#pragma unroll
+      for (int v = 0; v < V; ++v) w.scale[v] = p.scale[col + v];
     return w;
   };
   auto load = [&](int64_t row, int64_t col) {
     Cell c{};
     c.x = *(const Pack<T, V>*)(p.x + row * p.x_row + col);
-    if (IN && p.residual) c.res = *(const Pack<R, V>*)(p.residual + row * p.residual_row + col);
-    if (!IN && p.gate) c.g = *(const Pack<T, V>*)(p.gate + row * p.gate_row + col);
-    if (BACK) {
-      if (IN) c.g = *(const Pack<T, V>*)(p.grad_y + row * p.dim + col);
-      if (p.grad_r) c.gr = *(const Pack<R, V>*)(p.grad_r + row * p.dim + col);
-    } else if (!IN && p.residual) {
+    if ((IN || !BACK) && p.residual)
       c.res = *(const Pack<R, V>*)(p.residual + row * p.residual_row + col);
-    }
+    if (!IN && p.gate) c.g = *(const Pack<T, V>*)(p.gate + row * p.gate_row + col);
+    if (IN && BACK) c.g = *(const Pack<T, V>*)(p.grad_y + row * p.dim + col);
+    if (BACK && p.grad_r) c.gr = *(const Pack<R, V>*)(p.grad_r + row * p.dim + col);
     return c;
   };
-  // what is normed
-  auto under = [&](const Cell& c, const Weights<C, V>& w, int v) {
-    C u = (C)c.x.v[v];
+  const bool gated = !IN && p.gate, gate_first = gated && !p.norm_first;
+  auto make = [&](const Cell& c, const Weight& w) {
+    Make m;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m.u[v] = (C)c.x.v[v], m.sig[v] = C(1);
     if constexpr (IN) {
-      if (p.scale) u *= w.scale[v];
-      if (p.residual) u += (C)c.res.v[v];
-    } else {
-      if (p.gate && !p.norm_first) u *= silu((C)c.g.v[v]);
+      if (p.scale)
+#pragma unroll
+        for (int v = 0; v < V; ++v) m.u[v] *= w.scale[v];
+      if (p.residual)
+#pragma unroll
+        for (int v = 0; v < V; ++v) m.u[v] += (C)c.res.v[v];
+    } else if (gated) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) m.sig[v] = sigmoid((C)c.g.v[v]);
+      if (gate_first)
+#pragma unroll
+        for (int v = 0; v < V; ++v) m.u[v] *= silu_of((C)c.g.v[v], m.sig[v]);
     }
-    return u;
+    return m;
   };
   // backward: dL/d(u / rms), and the factor of the weight's gradient with u / rms
-  auto pull = [&](const Cell& c, const Weights<C, V>& w, int v, C& factor) {
+  auto pull = [&](const Cell& c, const Make& m, const Weight& w, int v, C& factor) {
     if constexpr (IN) {
       factor = (C)c.g.v[v];
     } else {
       factor = (C)c.gr.v[v] * w.scale[v];
-      if (p.gate && p.norm_first) factor *= silu((C)c.g.v[v]);
+      if (gated && !gate_first) factor *= silu_of((C)c.g.v[v], m.sig[v]);
     }
     return factor * w.weight[v];
   };
 
-  Weights<C, V> wr[N];
+  Weight wr[N];
   C dw[N][V], ds[N][V];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    if (kept && first + k * STEP < p.dim) wr[k] = weights_at(first + k * STEP);
+    if (KEPT && first + k * STEP < p.dim) wr[k] = weights_at(first + k * STEP);
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = ds[k][v] = C(0);
   }
-  // Calls f(pack, cells, weights) for each of the lane's packs of a row.
-  auto each = [&](int64_t row, Cell (&held)[N], auto&& f) {
-    if constexpr (kept) {
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (first + k * STEP < p.dim) f(k, (int64_t)first + k * STEP, held[k], wr[k]);
-    } else {
-      for (int64_t col = first; col < p.dim; col += STEP)
-        f(0, col, load(row, col), weights_at(col));
-    }
-  };
   C* const pw = BACK ? p.part_weight + slot * p.dim : nullptr;
   C* const ps = BACK && p.part_scale ? p.part_scale + slot * p.dim : nullptr;
-  if (BACK && !kept)
+  if (BACK && !KEPT)
     for (int64_t col = first; col < p.dim; col += STEP)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -149,99 +153,129 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(Args<T, R> p)
         if (ps) ps[col + v] = C(0);
       }
 
+  // A row's packs, the next row's on their way.
+  Cell ahead[N];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (first + k * STEP < p.dim) ahead[k] = load(row, first + k * STEP);
+  };
+  if (KEPT && slot < p.rows) fetch(slot);
+
   for (int64_t row = slot; row < p.rows; row += slots) {
     Cell held[N];
-    if constexpr (kept) {
+    Make made[N];
+    if constexpr (KEPT) {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (first + k * STEP < p.dim) held[k] = load(row, first + k * STEP);
+      for (int k = 0; k < N; ++k) held[k] = ahead[k];
+      if (row + slots < p.rows) fetch(row + slots);
+#pragma unroll
+      for (int k = 0; k < N; ++k) made[k] = make(held[k], wr[k]);
     }
+    // Calls f(pack, column, cells, made, weights) for each of the lane's packs.
+    auto each = [&](auto&& f) {
+      if constexpr (KEPT) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (first + k * STEP < p.dim) f(k, (int64_t)first + k * STEP, held[k], made[k], wr[k]);
+      } else {
+        for (int64_t col = first; col < p.dim; col += STEP) {
+          const Cell c = load(row, col);
+          const Weight w = weights_at(col);
+          f(0, col, c, make(c, w), w);
+        }
+      }
+    };
     C sum = C(0);
     if constexpr (!BACK) {
-      each(row, held, [&](int, int64_t, const Cell& c, const Weights<C, V>& w) {
+      each([&](int, int64_t, const Cell&, const Make& m, const Weight&) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const C u = under(c, w, v);
-          sum += u * u;
-        }
+        for (int v = 0; v < V; ++v) sum += m.u[v] * m.u[v];
       });
       sum = team_sum<W>(sum, red, turn);
       const C rstd = inverse_root(sum / (C)p.dim + p.eps);
       if (first == 0 && p.rstd) p.rstd[row] = rstd;
-      each(row, held, [&](int, int64_t col, const Cell& c, const Weights<C, V>& w) {
+      each([&](int, int64_t col, const Cell& c, const Make& m, const Weight& w) {
         Pack<T, V> oy;
         Pack<R, V> orr;
+        C n[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const C u = under(c, w, v);
-          C n = u * rstd * w.weight[v];
-          if constexpr (IN) {
-            oy.v[v] = (T)n;
-            orr.v[v] = (R)u;
-          } else {
-            if (p.gate && p.norm_first) n *= silu((C)c.g.v[v]);
-            if (p.scale) n *= w.scale[v];
-            if (p.residual) n += (C)c.res.v[v];
-            orr.v[v] = (R)n;
-          }
+        for (int v = 0; v < V; ++v) n[v] = m.u[v] * rstd * w.weight[v];
+        if constexpr (IN) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) oy.v[v] = (T)n[v], orr.v[v] = (R)m.u[v];
+          put_pack<STREAM, V>(p.y + row * p.dim + col, oy);
+        } else {
+          if (gated && !gate_first)
+#pragma unroll
+            for (int v = 0; v < V; ++v) n[v] *= silu_of((C)c.g.v[v], m.sig[v]);
+          if (p.scale)
+#pragma unroll
+            for (int v = 0; v < V; ++v) n[v] *= w.scale[v];
+          if (p.residual)
+#pragma unroll
+            for (int v = 0; v < V; ++v) n[v] += (C)c.res.v[v];
+#pragma unroll
+          for (int v = 0; v < V; ++v) orr.v[v] = (R)n[v];
         }
-        if (IN) *(Pack<T, V>*)(p.y + row * p.dim + col) = oy;
-        if (p.r) *(Pack<R, V>*)(p.r + row * p.dim + col) = orr;
+        if (p.r) put_pack<STREAM, V>(p.r + row * p.dim + col, orr);
       });
     } else {
       const C rstd = p.rstd[row];
-      each(row, held, [&](int, int64_t, const Cell& c, const Weights<C, V>& w) {
+      each([&](int, int64_t, const Cell& c, const Make& m, const Weight& w) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           C factor;
-          sum += pull(c, w, v, factor) * (under(c, w, v) * rstd);
+          sum += pull(c, m, w, v, factor) * m.u[v];
         }
       });
-      const C mean = team_sum<W>(sum, red, turn) / (C)p.dim;
-      each(row, held, [&](int k, int64_t col, const Cell& c, const Weights<C, V>& w) {
+      // rstd (g - hat mean(g hat)), hat = u rstd
+      const C mean = team_sum<W>(sum, red, turn) / (C)p.dim * rstd * rstd;
+      each([&](int k, int64_t col, const Cell& c, const Make& m, const Weight& w) {
         Pack<T, V> ox, og;
         Pack<R, V> orr;
+        C aw[V], as[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           C factor;
-          const C g = pull(c, w, v, factor), xv = (C)c.x.v[v];
-          const C hat = under(c, w, v) * rstd;
-          C du = rstd * (g - hat * mean);
-          C aw = factor * hat, as;
+          const C g = pull(c, m, w, v, factor), xv = (C)c.x.v[v];
+          const C hat = m.u[v] * rstd;
+          C du = rstd * (g - m.u[v] * mean);
+          aw[v] = factor * hat;
           if constexpr (IN) {
             if (p.grad_r) du += (C)c.gr.v[v];
             orr.v[v] = (R)du;
-            as = du * xv;
+            as[v] = du * xv;
             ox.v[v] = (T)(p.scale ? du * w.scale[v] : du);
           } else {
-            C slope = C(0), s = C(1);
-            if (p.gate) s = silu((C)c.g.v[v], slope);
-            as = (C)c.gr.v[v] * hat * w.weight[v];
-            if (p.norm_first) {
-              as *= s;
-              og.v[v] = (T)((C)c.gr.v[v] * w.scale[v] * hat * w.weight[v] * slope);
-              ox.v[v] = (T)du;
-            } else {
-              og.v[v] = (T)(du * xv * slope);
-              ox.v[v] = (T)(du * s);
+            const C gv = (C)c.g.v[v], s = gated ? silu_of(gv, m.sig[v]) : C(1);
+            const C n = hat * w.weight[v];
+            as[v] = (C)c.gr.v[v] * (gate_first ? n : n * s);
+            ox.v[v] = (T)(gate_first ? du * s : du);
+            if (gated) {
+              const C to = gate_first ? du * xv : (C)c.gr.v[v] * w.scale[v] * n;
+              og.v[v] = (T)(to * silu_slope(gv, m.sig[v]));
             }
           }
-          if constexpr (kept) {
-            dw[k][v] += aw;
-            ds[k][v] += as;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if constexpr (KEPT) {
+            dw[k][v] += aw[v];
+            ds[k][v] += as[v];
           } else {
-            pw[col + v] += aw;
-            if (ps) ps[col + v] += as;
+            pw[col + v] += aw[v];
+            if (ps) ps[col + v] += as[v];
           }
         }
-        *(Pack<T, V>*)(p.grad_x + row * p.dim + col) = ox;
+        put_pack<STREAM, V>(p.grad_x + row * p.dim + col, ox);
         if (IN && p.grad_residual)
-          *(Pack<R, V>*)(p.grad_residual + row * p.dim + col) = orr;
-        if (!IN && p.gate) *(Pack<T, V>*)(p.grad_gate + row * p.dim + col) = og;
+          put_pack<STREAM, V>(p.grad_residual + row * p.dim + col, orr);
+        if (gated) put_pack<STREAM, V>(p.grad_gate + row * p.dim + col, og);
       });
     }
   }
-  if constexpr (BACK && kept) {
+  if constexpr (BACK && KEPT) {
 #pragma unroll
     for (int k = 0; k < N; ++k)
       if (first + k * STEP < p.dim)
@@ -274,7 +308,7 @@ Way way_of(int64_t dim, bool wide) {
   if (wide) {
     if (dim <= 64 * V) return {V, 1, 1};
     if (dim <= 256 * V) return {V, 4, 1};
-    if (dim <= 512 * V) return {V, 4, 2};
+    if (dim <= 512 * V) return {V, 8, 1};
     if (dim <= 1024 * V) return {V, 16, 1};
     if (dim <= 2048 * V) return {V, 16, 2};
     return {V, 16, 0};
@@ -292,19 +326,31 @@ inline int64_t groups_of(const Way& w, int64_t rows) {
 template <typename T, typename R, bool IN, bool BACK>
 sla_status run(Args<T, R>& p, const Way& way, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
+  const double bytes = (double)p.rows * p.dim *
+                       (sizeof(T) * (IN ? 2 + BACK : 1 + (p.gate ? 1 + BACK : 0) + BACK) +
+                        sizeof(R) * ((p.residual != nullptr) + 1 + (IN && BACK)));
+  // Beyond what the last-level cache holds (256 MB): 16384 x 4096 bf16 with a gate, after a
+  // block, forward 81 -> 66 us, backward 144 -> 132; reads past it gained nothing.
+  const bool streams = bytes >= kMallBytes;
   const unsigned grid = (unsigned)groups_of(way, p.rows);
-#define SLA_NORM_CASE(v_, w_, np_)                                                          \
-  if (way.v == v_ && way.w == w_ && way.np == np_)                                          \
-    norm_rows<T, R, IN, BACK, v_, w_, np_><<<grid, w_ == 1 ? 256 : w_ * 64, 0, s>>>(p)
-  SLA_NORM_CASE(V, 1, 1);
-  else SLA_NORM_CASE(V, 4, 1);
-  else SLA_NORM_CASE(V, 4, 2);
-  else SLA_NORM_CASE(V, 16, 1);
-  else SLA_NORM_CASE(V, 16, 2);
-  else SLA_NORM_CASE(V, 16, 0);
-  else SLA_NORM_CASE(1, 4, 4);
-  else SLA_NORM_CASE(1, 16, 4);
-  else SLA_NORM_CASE(1, 16, 0);
+#define SLA_NORM_CASE(v_, w_, np_, stream_)                                                 \
+  if (way.v == v_ && way.w == w_ && way.np == np_ && (!stream_ || streams))                 \
+    norm_rows<T, R, IN, BACK, v_, w_, np_, stream_>                                         \
+        <<<grid, w_ == 1 ? 256 : w_ * 64, 0, s>>>(p)
+  SLA_NORM_CASE(V, 1, 1, true);
+  else SLA_NORM_CASE(V, 4, 1, true);
+  else SLA_NORM_CASE(V, 8, 1, true);
+  else SLA_NORM_CASE(V, 16, 1, true);
+  else SLA_NORM_CASE(V, 16, 2, true);
+  else SLA_NORM_CASE(V, 1, 1, false);
+  else SLA_NORM_CASE(V, 4, 1, false);
+  else SLA_NORM_CASE(V, 8, 1, false);
+  else SLA_NORM_CASE(V, 16, 1, false);
+  else SLA_NORM_CASE(V, 16, 2, false);
+  else SLA_NORM_CASE(V, 16, 0, false);
+  else SLA_NORM_CASE(1, 4, 4, false);
+  else SLA_NORM_CASE(1, 16, 4, false);
+  else SLA_NORM_CASE(1, 16, 0, false);
 #undef SLA_NORM_CASE
   SLA_HIP(hipGetLastError());
   return SLA_OK;

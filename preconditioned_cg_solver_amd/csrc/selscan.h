@@ -60,6 +60,7 @@ struct Args {
 // Where a wave works: its row of chunks, sequence, steps and channels.
 struct Place {
   int64_t row, seq, t0, t1;  // steps t0 <= t < t1 (packed: of all sequences)
+  int64_t part;              // which chunk of the sequence (packed: of all)
   int64_t at;                // the step that x's row 0 of this sequence is (packed: 0)
   int64_t channel;           // the first of the wave
   int group, block, some;    // channels that exist, of the wave's 16
@@ -77,8 +78,8 @@ __device__ __forceinline__ Place place_of(const Args<T>& p) {
   w.some = (int)min(max(p.group_dim - first, (int64_t)0), (int64_t)kChannels);
   w.channel = w.group * p.group_dim + first;
   w.seq = p.offsets ? 0 : w.row / p.chunks;
-  const int64_t part = p.offsets ? w.row : w.row % p.chunks;
-  w.t0 = part * p.chunk;
+  w.part = p.offsets ? w.row : w.row % p.chunks;
+  w.t0 = w.part * p.chunk;
   w.t1 = min(w.t0 + p.chunk, p.steps);
   w.at = p.offsets ? 0 : w.seq * p.steps;
   return w;
@@ -122,16 +123,6 @@ struct Rows {
   static constexpr int EL = TS * kChannels / kLanes;
   static constexpr int PER = kChannels / EL;  // lanes of a row
 };
-
-// Waits for loads of values here, and not where they are used: in a loop that would
-// be a wait for whatever was loaded last, the next tile.
-__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
-__device__ __forceinline__ void settle(double& v) { asm volatile("" : "+v"(v)); }
-template <int N, typename C>
-__device__ __forceinline__ void settle(C (&v)[N]) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) settle(v[j]);
-}
 
 // EL elements from p, of which `some` exist.  FAST: all of them or none, in a pack; p
 // is then valid in any case, and what is read where none exist is not used.

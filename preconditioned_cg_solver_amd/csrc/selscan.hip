@@ -35,7 +35,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   __shared__ C s_sum[FULL ? kWavesOf : 1][TS][kChannels];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place w = place_of<T, kWavesOf>(p);
-  if (w.some <= 0) return;
+  if (w.some <= 0 || (!FULL && w.part == p.chunks - 1)) return;  // what the last leaves is not asked
   auto& drive = s_drive[wave];
   auto& bs = s_b[wave];
   auto& cs = s_c[FULL ? wave : 0];
@@ -221,6 +221,66 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   }
 }
 
+// Sequences of a few steps, a serving step above all: 4 lanes take a channel from the
+// first step to the last, its states among them, without LDS.  16 x 4096 x 16 states bf16,
+// one step: 3.4 us for 8.9 in tiles.
+constexpr int kFew = 4;
+template <typename T, int NS, bool FAST>
+__global__ __launch_bounds__(kWG) void scan_few(Args<T> p) {
+  using C = typename Compute<T>::type;
+  const int64_t k = (p.before + blockIdx.x) * kWG + threadIdx.x;
+  const int q = (int)(k & 3);
+  const int64_t s = (k >> 2) / p.dim, channel = (k >> 2) % p.dim;
+  if (s >= p.n_seq) return;
+  const int g = (int)(channel / p.group_dim), at = q * NS;
+  const T* x = p.x + s * p.x_seq + channel;
+  const T* u = p.dt + s * p.dt_seq + channel;
+  const T* z = p.z ? p.z + s * p.z_seq + channel : nullptr;
+  const T* b = p.b + s * p.b_seq + (int64_t)g * p.states + (FAST ? at : 0);
+  const T* c = p.c + s * p.c_seq + (int64_t)g * p.states + (FAST ? at : 0);
+  T* y = p.y + s * p.steps * p.dim + channel;
+  C a2[NS], h[NS];
+  get_states<NS, FAST>(a2, p.a, channel, p.states, q, true);
+  get_states<NS, FAST>(h, p.h0, s * p.dim + channel, p.states, q, true);
+#pragma unroll
+  for (int j = 0; j < NS; ++j) a2[j] *= C(1.4426950408889634);
+  const C bias = p.bias ? p.bias[channel] : C(0), d = p.d ? p.d[channel] : C(0);
+  for (int64_t t = 0; t < p.steps; ++t) {
+    C bv[NS], cv[NS];
+    if constexpr (FAST) {
+      const auto bp = *(const Pack<T, NS>*)b, cp = *(const Pack<T, NS>*)c;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) bv[j] = (C)bp.v[j], cv[j] = (C)cp.v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const bool in = at + j < p.states;
+        bv[j] = in ? (C)b[at + j] : C(0), cv[j] = in ? (C)c[at + j] : C(0);
+      }
+    }
+    const C xv = (C)*x;
+    C delta = (C)*u + bias, slope, sum = C(0);
+    if (p.softplus) delta = softplus(delta, slope);
+    const C dx = delta * xv;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      h[j] = pow2(delta * a2[j]) * h[j] + dx * bv[j];
+      const C m = cv[j] * h[j];
+      sum += FAST || at + j < p.states ? m : C(0);
+    }
+    sum += from_lane<kXor1>(sum);
+    sum += from_lane<kXor2>(sum);
+    if (p.d) sum += d * xv;
+    if (z) {
+      sum *= silu((C)*z);
+      z += p.z_step;
+    }
+    if (q == 0) *y = (T)sum;
+    x += p.x_step, u += p.dt_step, b += p.b_step, c += p.c_step, y += p.dim;
+  }
+  put_states<NS, FAST>(h, p.h_last, s * p.dim + channel, p.states, q, true);
+}
+
 // h e^(a sum), for exponents whose power leaves the range where the product does
 // not: in four factors, none of them 0, so that a state that is not finite
 // stays so; one that is 0 stays 0.
@@ -313,16 +373,21 @@ sla_status check_shape(const sla_selscan_shape* q) {
 Plan plan_of(const sla_selscan_shape& q, bool backward) {
   Plan p;
   if (no_steps(q)) return p;
-  const int64_t per = q.dim / q.groups, seqs = q.d_offsets ? 1 : q.n_seq;
+  const bool packed = q.d_offsets != nullptr;
+  const int64_t per = q.dim / q.groups, seqs = packed ? 1 : q.n_seq;
   const int ts = tile_steps(q);
   p.blocks = (int)(q.groups * ((per + kChannels * kWavesOf - 1) / (kChannels * kWavesOf)));
   p.tiles = (q.steps + ts - 1) / ts;
   const int64_t waves = seqs * q.groups * ((per + kChannels - 1) / kChannels);
-  // TODO measure
-  (void)backward;
+  // Waves that leave SIMDs idle have their sequences cut, which costs a pass over the
+  // steps that writes nothing.  With 16 states, us, whole and cut to 4096 waves: forward 2 x
+  // 2048 x 2048 bf16 (256 waves) 201 and 73, 4 x 2048 x 2048 200 and 128, 8 x 2048 x 2048 (a wave
+  // a SIMD) 215 and 239, 16 x 2048 x 2048 330 and 437; backward 695 and 176, 707 and 335, 717 and
+  // 628, 1026 and 1168.  Packed sequences make chunks of uneven work: 30011 x 1000 fp16 cut
+  // to 4096 355 and 720, to 8192 320 and 689.
   int64_t chunks = 1;
-  {const char*e1=getenv("SC_MAX"),*e2=getenv("SC_WANT"); int64_t mx=e1?atoll(e1):512, wt=e2?atoll(e2):2048;
-  if (waves < mx) chunks = std::min((wt + waves - 1) / waves, (p.tiles + 3) / 4);}
+  if (waves < (backward ? 1536 : 768))
+    chunks = std::min(((packed ? 8192 : 4096) + waves - 1) / waves, (p.tiles + 3) / 4);
   // 2^31 steps of a chunk are more than any chunk has, also of one a sequence
   const int64_t least = (q.steps >> 30) + 1;
   chunks = std::max(chunks, least);
@@ -382,7 +447,7 @@ Args<T> args_of(const sla_selscan_shape& q, const sla_selscan_in& in, const Plan
   p.softplus = q.softplus;
   const bool one = packed || q.n_seq == 1, step = q.steps == 1;
   const int el = tile_steps(q) * kChannels / kLanes, ns = q.n_state <= 4 ? 1 : q.n_state <= 8 ? 2 : 4;
-  const int bl = std::max(1, 4 * ns * tile_steps(q) / kLanes);
+  const int bl = ns;  // what a lane takes of B and C, or more
   const size_t b = sizeof(T);
   p.fast = p.group_dim % el == 0 && packs(in.d_x, in.x_seq, in.x_step, b, el, one, step) &&
           packs(in.d_dt, in.dt_seq, in.dt_step, b, el, one, step) &&
@@ -502,6 +567,12 @@ sla_status sla_selscan_forward(const sla_selscan_shape* shape, const sla_selscan
     return with_states(q.n_state, p.fast, [&](auto ns, auto fast) -> sla_status {
       constexpr int NS = decltype(ns)::value;
       constexpr bool FAST = decltype(fast)::value;
+      if (q.steps <= kFew && !q.d_offsets && !d_saved) {
+        const int64_t lanes = q.n_seq * q.dim * 4;
+        return in_launches(p, (lanes + kWG - 1) / kWG, [&](dim3 grid) {
+          scan_few<T, NS, FAST><<<grid, kWG, 0, s>>>(p);
+        });
+      }
       const int64_t groups = plan.rows * plan.blocks;
       if (plan.chunks > 1) {
         sla_status e = in_launches(p, groups, [&](dim3 grid) {

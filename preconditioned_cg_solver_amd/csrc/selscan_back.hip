@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
   __shared__ C s_c[kWavesOf][TS][4 * NS];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place w = place_of<T, kWavesOf>(p);
-  if (w.some <= 0) return;
+  if (w.some <= 0 || w.part == 0) return;  // what the first leaves is not asked
   auto& pull = s_pull[wave];
   auto& cs = s_c[wave];
   const int q = lane >> 4, c = lane & 15;
@@ -207,6 +207,9 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
     s_bias[wave][lane] = p.bias && lane < w.some ? p.bias[w.channel + lane] : C(0);
     s_d[wave][lane] = p.d && lane < w.some ? p.d[w.channel + lane] : C(0);
   }
+  if (FAST && some <= 0)
+#pragma unroll
+    for (int e = 0; e < EL; ++e) drive[r][cc + e] = {C(0), C(0)}, dss[r][cc + e] = C(0);
   wave_sync();
   const int64_t last = w.t0 + (w.t1 - 1 - w.t0) / TS * TS;
   using Row = Stream<FAST, EL, T>;
@@ -248,6 +251,7 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
     const int n = (int)min((int64_t)TS, w.t1 - t0);
     if (!idle) {
       const Pack<T, EL> x = xr, z = zr, gy = gr;
+      C zsig[EL];
       {
         C delta[EL], slope[EL], ds[EL];
 #pragma unroll
@@ -258,15 +262,17 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           for (int e = 0; e < EL; ++e) delta[e] = softplus(delta[e], slope[e]);
         if (gated)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) ds[e] *= silu((C)z.v[e]);
+          for (int e = 0; e < EL; ++e) {
+            zsig[e] = sigmoid((C)z.v[e]);
+            ds[e] *= silu_of((C)z.v[e], zsig[e]);
+          }
+        if (!FAST || some > 0)  // else they stay 0, as what does not exist adds nothing to sums
 #pragma unroll
-        for (int e = 0; e < EL; ++e) {
-          // channels that do not exist add nothing to the sums over channels
-          const bool exists = !FAST || some > 0;
-          drive[r][cc + e] = {exists ? delta[e] : C(0), exists ? delta[e] * (C)x.v[e] : C(0)};
-          dss[r][cc + e] = exists ? ds[e] : C(0);
-          slopes[r][cc + e] = slope[e];
-        }
+          for (int e = 0; e < EL; ++e) {
+            drive[r][cc + e] = {delta[e], delta[e] * (C)x.v[e]};
+            dss[r][cc + e] = ds[e];
+            slopes[r][cc + e] = slope[e];
+          }
       }
       keep_shared<C, NS>(bs, br);
       keep_shared<C, NS>(cs, cr);
@@ -319,11 +325,10 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           qa += FAST || q * NS + j < p.states ? ma : C(0);
           da[j] += mh * v.d.delta;
         }
-        gb += from_lane<kRor8>(gb);
-        qa += from_lane<kRor8>(qa);
-        gb += from_lane<kRor4>(gb);
-        qa += from_lane<kRor4>(qa);
-        sums[i][1 + (q & 1)][c] = q & 1 ? qa : gb;
+        // lanes of even q end with the sum of one, those of odd q with the other's
+        C two = (q & 1 ? qa : gb) + from_lane<kRor4>(q & 1 ? gb : qa);
+        two += from_lane<kRor8>(two);
+        sums[i][1 + (q & 1)][c] = two;
         // over the channels (lanes that hold the same sum write it to the same place)
         const int odd = lane >> 4 & 1, high = lane >> 5;
         if constexpr (NS == 4) {
@@ -433,10 +438,9 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
         if (gated)
 #pragma unroll
           for (int e = 0; e < EL; ++e) {
-            C zs, s = sums[r][0][cc + e];
+            C s = sums[r][0][cc + e];
             if (p.d) s += s_d[wave][cc + e] * (C)x.v[e];
-            silu((C)z.v[e], zs);
-            oz.v[e] = (T)((C)gy.v[e] * s * zs);
+            oz.v[e] = (T)((C)gy.v[e] * s * silu_slope((C)z.v[e], zsig[e]));
           }
         store_some<FAST, EL>(p.grad_x + to, ox, some);
         store_some<FAST, EL>(p.grad_dt + to, ou, some);

@@ -29,6 +29,16 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Waits for loads of values here, and not where they are used: in a loop that would
+// be a wait for whatever was loaded last, the next tile.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(double& v) { asm volatile("" : "+v"(v)); }
+template <int N, typename C>
+__device__ __forceinline__ void settle(C (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) settle(v[j]);
+}
+
 // A barrier that waits for a wave's LDS accesses but not, as __syncthreads does, for
 // its stores to memory.
 __device__ __forceinline__ void lds_barrier() {
@@ -45,32 +55,32 @@ __device__ __forceinline__ float sigmoid(float v) {
 }
 __device__ __forceinline__ double sigmoid(double v) { return 1.0 / (1.0 + exp(-v)); }
 
-// v sigmoid(v), which goes to -0 at -infinity, where the product would be NaN.
+// v sigmoid(v) from s = sigmoid(v): -infinity gives -0, where the plain product is NaN
+// (s is NaN if v is, which the maximum would hide).
+__device__ __forceinline__ float silu_of(float v, float s) { return fmaxf(v, -3e38f) * s; }
+__device__ __forceinline__ double silu_of(double v, double s) { return fmax(v, -1e308) * s; }
 template <typename C>
 __device__ __forceinline__ C silu(C v) {
-  return v == -C(INFINITY) ? -C(0) : v * sigmoid(v);
+  return silu_of(v, sigmoid(v));
 }
-// The same and its slope, s (1 + v (1 - s)).
-template <typename C>
-__device__ __forceinline__ C silu(C v, C& slope) {
-  const C s = sigmoid(v);
-  const bool inf = fabs(v) == C(INFINITY);
-  slope = inf ? (v > C(0) ? C(1) : C(0)) : s + v * s * (C(1) - s);
-  return v == -C(INFINITY) ? -C(0) : v * s;
+// Its slope, s (1 + v (1 - s)): s (1 - s) is 0 long before v reaches the bounds.
+__device__ __forceinline__ float silu_slope(float v, float s) {
+  return s + __builtin_amdgcn_fmed3f(v, -1e4f, 1e4f) * (s * (1.0f - s));
+}
+__device__ __forceinline__ double silu_slope(double v, double s) {
+  return s + fmin(fmax(v, -1e5), 1e5) * (s * (1.0 - s));
 }
 
-// log(1 + e^v), and the slope sigmoid(v).  log(w) e / (w - 1) with w = 1 + e as
-// rounded has the accuracy of log(1 + e) for every e; above 30 (fp64: 40) the sum
-// is v to the last place.
+// log(1 + e^v), and the slope sigmoid(v).  With w = 1 + e as rounded, log(w) + (e - (w -
+// 1)) / w has the accuracy of log(1 + e) for every e; above 30 (fp64: 40) the sum is v
+// to the last place.
 __device__ __forceinline__ float softplus(float v, float& slope) {
   const float e = __builtin_amdgcn_exp2f(1.44269504f * v), w = 1.0f + e;
   const float r = __builtin_amdgcn_rcpf(w);
-  const float d = w - 1.0f;
-  const float l = 0.693147181f * __builtin_amdgcn_logf(w);
-  const float small = d == 0.0f ? e : l * (e * __builtin_amdgcn_rcpf(d));
+  const float l = 0.693147181f * __builtin_amdgcn_logf(w) + (e - (w - 1.0f)) * r;
   const bool big = v > 30.0f;
   slope = big ? 1.0f : e * r;
-  return big ? v : small;
+  return big ? v : l;
 }
 __device__ __forceinline__ double softplus(double v, double& slope) {
   const double e = exp(v);
