@@ -30,11 +30,14 @@
   are learnt from the observations: the recurrence along time
   (autograd.linear_recurrence), the solves of all observed times at once,
   their adjoint, the recurrence's adjoint and an AdamW step over both
-  parameters, with states of ``--bits`` bits.
+  parameters, with states of ``--bits`` bits.  With ``--sources block`` nothing is
+  known of how the sources arise: a sequence block (norm, projection, causal
+  convolution, selective scan, gated norm onto the residual) makes them of
+  the driving signal, and all its parameters are learnt through the solves.
 
 Usage: ``python -m preconditioned_cg_solver_amd.studies
 jacobi|quality|trace|learn [--configs 0,1,2,3] [--rows N] [--iters N]
-[--bits 8|32]``.  jacobi and quality print one JSON line per configuration,
+[--bits 8|32] [--sources relax|block]``.  jacobi and quality print one JSON line per configuration,
 learn one for the run.
 """
 from __future__ import annotations
@@ -42,6 +45,7 @@ from __future__ import annotations
 import argparse
 import json
 import time
+from typing import Optional
 
 import numpy as np
 import torch
@@ -170,36 +174,86 @@ class _SolveColumns(torch.autograd.Function):
         return out[0], None, None, None, None, None
 
 
-def learn(iters: int = 300, bits: int = 32, steps: int = 256, snapshots: int = 16, lr: float = 0.05,
-          seed: int = 0):
-    """Learn relaxation rates and source strengths from observed fields."""
+def block_parameters(n: int, width: int = 64, states: int = 16, seed: int = 0):
+    """The parameters of `block_sources` for n nodes, float64."""
+    rng = np.random.default_rng([22, seed])
+
+    def normal(*shape, scale):
+        return scale * rng.standard_normal(shape)
+
+    rest = np.exp(rng.uniform(np.log(1e-2), np.log(0.5), width))  # first steps of the scan
+    p = {"lift": normal(2, width, scale=1.0), "norm": np.ones(width),
+         "split": normal(width, 2 * width, scale=width ** -0.5),
+         "conv": normal(width, 4, scale=0.5), "conv_bias": np.zeros(width),
+         "drive": normal(width, width + 2 * states, scale=0.5 * width ** -0.5),
+         "rate": np.log(np.tile(np.arange(1.0, states + 1), (width, 1))), "skip": np.ones(width),
+         "dt_bias": np.log(np.expm1(rest)), "gated": np.ones(width), "scale": np.ones(width),
+         "spread": normal(width, n, scale=width ** -0.5)}
+    return {k: _dev(v).requires_grad_() for k, v in p.items()}
+
+
+def block_sources(p, drive):
+    """Sources (steps, n) made of a driving signal (steps) by a sequence block."""
+    width, states = p["rate"].shape
+    stream = (drive[:, None] * p["lift"][0] + p["lift"][1])[None]
+    y, stream = AG.norm_in(stream, p["norm"])
+    x, gate = (y @ p["split"]).split(width, -1)
+    x, _ = AG.causal_conv(x, p["conv"], p["conv_bias"])
+    dt, b, c = (x @ p["drive"]).split([width, states, states], -1)
+    y, _ = AG.selective_scan(x, dt, -torch.exp(p["rate"]), b.unsqueeze(2), c.unsqueeze(2),
+                             D=p["skip"], dt_bias=p["dt_bias"])
+    stream = AG.norm_out(y, p["gated"], gate=gate, residual=stream, scale=p["scale"])
+    return stream[0] @ p["spread"]
+
+
+def learn(iters: int = 300, bits: int = 32, steps: int = 256, snapshots: int = 16,
+          lr: Optional[float] = None, seed: int = 0, sources: str = "relax"):
+    """Learn relaxation rates and source strengths, or a block that makes the
+    sources, from observed fields."""
     rng = np.random.default_rng([21, seed])
     M = I.heat2d(64, dt=1e-4)
     A, G = _handle(M), _handle(I.spai_factor(M, rng), transpose=True)
     n = M.n
+    lr = lr if lr is not None else 0.05 if sources == "relax" else 0.005
     drive = _dev(np.cumsum(rng.standard_normal(steps)) / 4.0)
     seen = _dev(np.linspace(steps // 8, steps - 1, snapshots).astype(np.int64))
     true_g = _dev(3.0 + 0.5 * rng.standard_normal(n))
     true_s = _dev(1.0 + 0.3 * rng.standard_normal(n))
 
-    def fields(g, s):
+    def relaxing(g, s):
         x = drive[None, :, None] * s
         h, _ = AG.linear_recurrence(x, g.expand(1, steps, n))
-        return _SolveColumns.apply(h[0, seen].t(), A, G, 3e-3, 1e-10, 500)
+        return h[0]
+
+    def fields(h):
+        return _SolveColumns.apply(h[seen].t(), A, G, 3e-3, 1e-10, 500)
 
     with torch.no_grad():
-        observed = fields(true_g, true_s)
+        observed = fields(relaxing(true_g, true_s))
     scale = float(observed.square().mean())
-    g = torch.full_like(true_g, 3.0, requires_grad=True)
-    s = torch.ones_like(true_s, requires_grad=True)
-    opt = B.sla_adamw_create([g, s], state_bits=bits)
+    if sources == "relax":
+        g = torch.full_like(true_g, 3.0, requires_grad=True)
+        s = torch.ones_like(true_s, requires_grad=True)
+        params = [g, s]
+
+        def made():
+            return relaxing(g, s)
+    elif sources == "block":
+        p = block_parameters(n, seed=seed)
+        params = list(p.values())
+
+        def made():
+            return block_sources(p, drive)
+    else:
+        raise ValueError(f"sources must be 'relax' or 'block', got {sources!r}")
+    opt = B.sla_adamw_create(params, state_bits=bits)
     losses, t0 = [], None
     for t in range(1, iters + 1):
         if t == 2:
             torch.cuda.synchronize()
             t0 = time.perf_counter()
-        loss = (fields(g, s) - observed).square().mean() / scale
-        grads = torch.autograd.grad(loss, [g, s])
+        loss = (fields(made()) - observed).square().mean() / scale
+        grads = torch.autograd.grad(loss, params)
         B.sla_adamw_step(opt, grads, step=t, lr=lr * (1 - (t - 1) / iters), weight_decay=0.0,
                          seed=seed)
         losses.append(loss.detach())
@@ -211,10 +265,13 @@ def learn(iters: int = 300, bits: int = 32, steps: int = 256, snapshots: int = 1
         return float((a - b).norm() / (b - start).norm())
 
     out = {"grid": "64x64", "n": n, "steps": steps, "snapshots": snapshots, "bits": bits,
-           "iterations": iters, "loss_first": float(losses[0]), "loss_last": float(losses[-1]),
-           "rate_error": off(g.detach(), true_g, 3.0),
-           "strength_error": off(s.detach(), true_s, 1.0),
-           "ms_per_iteration": None if each is None else round(each * 1e3, 3)}
+           "iterations": iters, "loss_first": float(losses[0]), "loss_last": float(losses[-1])}
+    if sources == "relax":
+        out.update(rate_error=off(g.detach(), true_g, 3.0),
+                   strength_error=off(s.detach(), true_s, 1.0))
+    else:
+        out.update(sources=sources, parameters=sum(p.numel() for p in params))
+    out["ms_per_iteration"] = None if each is None else round(each * 1e3, 3)
     for h in (A, G):
         h.destroy()
     opt.destroy()
@@ -228,6 +285,7 @@ def main():
     ap.add_argument("--rows", type=int, default=20000)
     ap.add_argument("--iters", type=int, default=300)
     ap.add_argument("--bits", type=int, default=32, choices=[8, 32])
+    ap.add_argument("--sources", default="relax", choices=["relax", "block"])
     args = ap.parse_args()
     configs = [int(c) for c in args.configs.split(",")]
     if args.study == "jacobi":
@@ -235,7 +293,7 @@ def main():
     elif args.study == "quality":
         quality(configs)
     elif args.study == "learn":
-        print(json.dumps(learn(args.iters, args.bits)), flush=True)
+        print(json.dumps(learn(args.iters, args.bits, sources=args.sources)), flush=True)
     else:
         trace_run(args.rows)
 

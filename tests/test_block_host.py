@@ -1,0 +1,384 @@
+"""The operators of a sequence block without a GPU: what the C entry points and the
+binding refuse, their sizes, the references that the GPU tests use, and where packed
+sequences' offsets lead."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from preconditioned_cg_solver_amd import binding as B
+import block_util as K
+
+OK, INVALID, UNSUPPORTED = 0, -1, -2
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(B.LIB_PATH):
+        from preconditioned_cg_solver_amd import build
+        build.build()
+    return B.lib()
+
+
+P = [ctypes.c_void_p(0x1000 * (k + 1)) for k in range(24)]  # never dereferenced
+
+
+def conv_shape(**kw):
+    q = dict(n_seq=2, steps=600, dim=96, width=4, d_offsets=None, dtype=B.SLA_BF16,
+             act=B.SLA_ACT_SILU)
+    q.update(kw)
+    return B.ConvShape(**q)
+
+
+def scan_shape(**kw):
+    q = dict(n_seq=2, steps=600, dim=96, n_state=16, groups=1, d_offsets=None, dtype=B.SLA_BF16,
+             softplus=1)
+    q.update(kw)
+    return B.SelscanShape(**q)
+
+
+def norm_shape(**kw):
+    q = dict(rows=30, dim=96, dtype=B.SLA_BF16, stream=B.SLA_F32, eps=1e-5)
+    q.update(kw)
+    return B.NormShape(**q)
+
+
+def conv_sizes(L, q):
+    n = ctypes.c_size_t()
+    return L.sla_conv_sizes(ctypes.byref(q), ctypes.byref(n)), n.value
+
+
+def scan_sizes(L, q):
+    n = [ctypes.c_size_t() for _ in range(3)]
+    return (L.sla_selscan_sizes(ctypes.byref(q), *(ctypes.byref(k) for k in n)),
+            *(k.value for k in n))
+
+
+def norm_sizes(L, q):
+    n = ctypes.c_size_t()
+    return L.sla_norm_sizes(ctypes.byref(q), ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_seq=-1), INVALID), (dict(steps=-1), INVALID), (dict(dim=-1), INVALID),
+    (dict(dtype=9), INVALID), (dict(act=2), INVALID), (dict(width=1), UNSUPPORTED),
+    (dict(width=5), UNSUPPORTED), (dict(steps=1 << 41), UNSUPPORTED),
+    (dict(dim=1 << 28), UNSUPPORTED), (dict(n_seq=1 << 30, steps=1 << 30), UNSUPPORTED)])
+def test_conv_shapes_refused(L, kw, want):
+    assert conv_sizes(L, conv_shape(**kw))[0] == want
+    assert L.sla_last_error()
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_seq=-1), INVALID), (dict(steps=-1), INVALID), (dict(dim=-1), INVALID),
+    (dict(dtype=9), INVALID), (dict(softplus=2), INVALID), (dict(groups=0), INVALID),
+    (dict(groups=5), INVALID), (dict(n_state=0), INVALID), (dict(n_state=17), UNSUPPORTED),
+    (dict(steps=1 << 41), UNSUPPORTED), (dict(dim=1 << 26), UNSUPPORTED),
+    (dict(n_seq=1 << 30, steps=1 << 30), UNSUPPORTED)])
+def test_scan_shapes_refused(L, kw, want):
+    assert scan_sizes(L, scan_shape(**kw))[0] == want
+    assert L.sla_last_error()
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INVALID), (dict(dim=-1), INVALID), (dict(dtype=9), INVALID),
+    (dict(stream=B.SLA_F16), INVALID), (dict(stream=B.SLA_F64), INVALID),
+    (dict(dtype=B.SLA_F64), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(dim=1 << 30), UNSUPPORTED),
+    (dict(rows=1 << 40, dim=1 << 29), UNSUPPORTED)])
+def test_norm_shapes_refused(L, kw, want):
+    assert norm_sizes(L, norm_shape(**kw))[0] == want
+    assert L.sla_last_error()
+
+
+def test_sizes(L):
+    assert conv_sizes(L, conv_shape(n_seq=0)) == (OK, 0)
+    assert conv_sizes(L, conv_shape(steps=0)) == (OK, 0)
+    assert conv_sizes(L, conv_shape())[1] > 0
+    assert scan_sizes(L, scan_shape(dim=0)) == (OK, 0, 0, 0)
+    assert scan_sizes(L, scan_shape(steps=1))[2] == 0  # a serving step needs no workspace
+    st, saved, fwd, back = scan_sizes(L, scan_shape())
+    assert st == OK and saved == 2 * 38 * 96 * 16 * 4 and back > fwd
+    assert scan_sizes(L, scan_shape(dtype=B.SLA_F64))[1] == 2 * 75 * 96 * 16 * 8
+    assert norm_sizes(L, norm_shape(rows=0)) == (OK, 0)
+    assert norm_sizes(L, norm_shape())[1] > 0
+    for f in (L.sla_conv_sizes, L.sla_norm_sizes):
+        assert f(None, None) == INVALID
+    assert L.sla_selscan_sizes(None, None, None, None) == INVALID
+    assert L.sla_conv_sizes(ctypes.byref(conv_shape()), None) == INVALID
+
+
+def conv_forward(L, q, x=P[0], xs=1, xt=1, w=P[1], b=P[2], st=P[3], y=P[4], last=P[5]):
+    return L.sla_conv_forward(ctypes.byref(q) if q else None, x, xs, xt, w, b, st, y, last, None)
+
+
+def conv_backward(L, q, x=P[0], xs=1, w=P[1], st=P[3], gy=P[4], gs=1, gl=P[5], dx=P[6], dw=P[7],
+                  dst=P[9], work=P[10], nw=1 << 40):
+    return L.sla_conv_backward(ctypes.byref(q) if q else None, x, xs, 1, w, P[2], st, gy, gs, 1, gl,
+                               dx, dw, P[8], dst, work, nw, None)
+
+
+def test_conv_arguments_refused(L):
+    q = conv_shape()
+    for bad in (dict(x=None), dict(w=None), dict(y=None), dict(xs=-1), dict(xt=-1), dict(y=P[0]),
+                dict(y=P[3]), dict(last=P[0]), dict(last=P[4])):
+        assert conv_forward(L, q, **bad) == INVALID, bad
+        assert L.sla_last_error()
+    assert conv_forward(L, None) == INVALID
+    for bad in (dict(x=None), dict(w=None), dict(dx=None), dict(dw=None), dict(xs=-1),
+                dict(gs=-1), dict(dx=P[0]), dict(dx=P[4]), dict(dst=P[3]), dict(dst=P[6]),
+                dict(work=None), dict(nw=8), dict(work=ctypes.c_void_p(0x1008))):
+        assert conv_backward(L, q, **bad) == INVALID, bad
+    assert conv_forward(L, conv_shape(n_seq=0), x=None, w=None, y=None) == OK
+
+
+def scan_in(**kw):
+    a = dict(d_x=P[0], d_dt=P[1], d_z=P[2], d_b=P[3], d_c=P[4], x_seq=1, x_step=1, dt_seq=1,
+             dt_step=1, z_seq=1, z_step=1, b_seq=1, b_step=1, c_seq=1, c_step=1, d_a=P[5],
+             d_d=P[6], d_dt_bias=P[7], d_h0=P[8])
+    a.update(kw)
+    return B.SelscanIn(**a)
+
+
+def scan_forward(L, q, a, y=P[9], last=P[10], work=P[11], nw=1 << 50):
+    return L.sla_selscan_forward(ctypes.byref(q) if q else None, ctypes.byref(a) if a else None, y,
+                                 last, None, work, nw, None)
+
+
+def scan_backward(L, q, a, saved=P[9], gy=P[10], gs=1, o=None, work=P[11], nw=1 << 50, **kw):
+    g = dict(d_x=P[12], d_dt=P[13], d_z=P[14], d_b=P[15], d_c=P[16], d_a=P[17], d_d=P[18],
+             d_dt_bias=P[19], d_h0=P[20])
+    g.update(kw)
+    o = B.SelscanGrads(**g) if o is None else o
+    return L.sla_selscan_backward(ctypes.byref(q), ctypes.byref(a), saved, gy, gs, 1, None,
+                                  ctypes.byref(o) if o else None, work, nw, None)
+
+
+def test_scan_arguments_refused(L):
+    q = scan_shape(steps=3000)
+    assert scan_sizes(L, q)[2] > 0  # cut into chunks
+    for k in ("d_x", "d_dt", "d_a", "d_b", "d_c"):
+        assert scan_forward(L, q, scan_in(**{k: None})) == INVALID
+        assert scan_backward(L, q, scan_in(**{k: None})) == INVALID
+    for k in ("x_seq", "dt_step", "z_seq", "b_step", "c_seq"):
+        assert scan_forward(L, q, scan_in(**{k: -1})) == INVALID
+    assert scan_forward(L, None, scan_in()) == INVALID
+    assert scan_forward(L, q, None) == INVALID
+    for bad in (dict(y=None), dict(y=P[0]), dict(y=P[2]), dict(y=P[4]), dict(work=None), dict(nw=8),
+                dict(work=ctypes.c_void_p(0x1008))):
+        assert scan_forward(L, q, scan_in(), **bad) == INVALID, bad
+    # packed states in place: who reads a sequence's first state and who writes its last differ
+    assert scan_forward(L, scan_shape(d_offsets=P[12]), scan_in(), last=P[8]) == INVALID
+    for bad in (dict(saved=None), dict(gy=None), dict(gs=-1), dict(d_x=None), dict(d_z=None),
+                dict(d_a=None), dict(d_b=P[0]), dict(d_x=P[10]), dict(d_c=P[15]), dict(work=None),
+                dict(nw=8)):
+        assert scan_backward(L, q, scan_in(), **bad) == INVALID, bad
+    empty = scan_in(d_x=None, d_dt=None, d_a=None, d_b=None, d_c=None)
+    assert scan_forward(L, scan_shape(n_seq=0), empty, y=None, work=None, nw=0) == OK
+
+
+def test_norm_arguments_refused(L):
+    q = norm_shape()
+    f, b = L.sla_norm_in_forward, L.sla_norm_in_backward
+
+    def fwd(x=P[0], xr=96, res=P[1], rr=96, sc=P[2], w=P[3], y=P[4], r=P[5]):
+        return f(ctypes.byref(q), x, xr, res, rr, sc, w, y, r, P[6], None)
+
+    for bad in (dict(x=None), dict(w=None), dict(y=None), dict(r=None), dict(xr=-1), dict(rr=-1),
+                dict(y=P[0]), dict(y=P[1]), dict(r=P[0]), dict(r=P[4]), dict(r=P[1], rr=200),
+                dict(res=None, sc=None)):
+        assert fwd(**bad) == INVALID, bad
+
+    def back(gy=P[0], gr=P[1], x=P[2], w=P[5], rstd=P[6], dx=P[7], dres=P[8], dw=P[9], work=P[11],
+             nw=1 << 40):
+        return b(ctypes.byref(q), gy, gr, x, 96, P[3], 96, P[4], w, rstd, dx, dres, dw, P[10], work,
+                 nw, None)
+
+    for bad in (dict(gy=None), dict(x=None), dict(w=None), dict(rstd=None), dict(dx=None),
+                dict(dw=None), dict(dx=P[0]), dict(dres=P[1]), dict(dres=P[7]), dict(work=None),
+                dict(nw=8), dict(work=ctypes.c_void_p(0x1008))):
+        assert back(**bad) == INVALID, bad
+
+    def out(order=0, x=P[0], xr=96, g=P[1], gr=96, res=P[2], rr=96, w=P[4], o=P[5]):
+        return L.sla_norm_out_forward(ctypes.byref(q), order, x, xr, g, gr, res, rr, P[3], w, o,
+                                      P[6], None)
+
+    for bad in (dict(order=2), dict(x=None), dict(w=None), dict(o=None), dict(xr=-1), dict(gr=-1),
+                dict(rr=-1), dict(o=P[0]), dict(o=P[1]), dict(o=P[2], rr=97)):
+        assert out(**bad) == INVALID, bad
+
+    def oback(order=1, go=P[0], x=P[1], g=P[2], gr=96, w=P[4], rstd=P[5], dx=P[6], dg=P[7], dw=P[8],
+              work=P[10], nw=1 << 40):
+        return L.sla_norm_out_backward(ctypes.byref(q), order, go, x, 96, g, gr, P[3], w, rstd, dx,
+                                       dg, dw, P[9], work, nw, None)
+
+    for bad in (dict(order=-1), dict(go=None), dict(x=None), dict(w=None), dict(rstd=None),
+                dict(dx=None), dict(dg=None), dict(dw=None), dict(gr=-1), dict(dx=P[0]),
+                dict(dg=P[2]), dict(dg=P[6]), dict(work=None), dict(nw=8)):
+        assert oback(**bad) == INVALID, bad
+
+
+def test_binding_refuses():
+    x = torch.zeros(2, 6, 8)
+    w = torch.zeros(8, 4)
+    for bad in (lambda: B.sla_conv_forward(x[0], w), lambda: B.sla_conv_forward(x, w[:4]),
+                lambda: B.sla_conv_forward(x, w, act="gelu"),
+                lambda: B.sla_conv_forward(x, w.double()),
+                lambda: B.sla_conv_forward(x, w, state=torch.zeros(2, 4, 8)),
+                lambda: B.sla_conv_forward(x, w, bias=torch.zeros(9)),
+                lambda: B.sla_conv_forward(x.transpose(1, 2), torch.zeros(6, 4)),
+                lambda: B.sla_conv_forward(x.long(), w),
+                lambda: B.sla_conv_forward(x, w)):  # not on the GPU
+        with pytest.raises(ValueError):
+            bad()
+    A, bc = torch.zeros(8, 4), torch.zeros(2, 6, 1, 4)
+    for bad in (lambda: B.sla_selscan_forward(x, x[:, :5], A, bc, bc),
+                lambda: B.sla_selscan_forward(x, x, A[:5], bc, bc),
+                lambda: B.sla_selscan_forward(x, x, A, bc[:, :, 0], bc),
+                lambda: B.sla_selscan_forward(x, x, A, bc, bc.half()),
+                lambda: B.sla_selscan_forward(x, x, A.double(), bc, bc),
+                lambda: B.sla_selscan_forward(x, x, A, bc.transpose(2, 3), bc),
+                lambda: B.sla_selscan_forward(x, x, A, bc, bc, h0=torch.zeros(2, 8)),
+                lambda: B.sla_selscan_forward(x, x, A, bc, bc, offsets=torch.zeros(3)),
+                lambda: B.sla_selscan_forward(x, x, A, bc, bc)):
+        with pytest.raises(ValueError):
+            bad()
+    v = torch.ones(8)
+    for bad in (lambda: B.sla_norm_in_forward(x, v[:7]),
+                lambda: B.sla_norm_in_forward(x, v, residual=x[:1]),
+                lambda: B.sla_norm_in_forward(x, v, scale=v.double()),
+                lambda: B.sla_norm_in_forward(x.transpose(1, 2), torch.ones(6)),
+                lambda: B.sla_norm_out_forward(x, v, order="first"),
+                lambda: B.sla_norm_out_forward(x, v, gate=x.half()),
+                lambda: B.sla_norm_out_forward(x, v)):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_rows_of_slices():
+    wide = torch.zeros(3, 5, 2, 8)
+    assert B._rows_of(wide[:, :, 0], "x", 8)[1:] == (15, 16)
+    assert B._rows_of(wide, "x", 8)[1:] == (30, 8)
+    assert B._rows_of(wide[:1, 2:3, 0], "x", 8)[1:] == (1, 8)
+    assert B._rows_of(wide[0, :, 1], "x", 8)[1:] == (5, 16)
+    with pytest.raises(ValueError):
+        B._rows_of(wide[:, :4, 0], "x", 8)  # the rows of two leading steps are apart
+    with pytest.raises(ValueError):
+        B._rows_of(wide.transpose(0, 1)[:, :, 0], "x", 8)
+
+
+def test_any_offsets_lead_to_a_sequence():
+    """The sequence of a step, for offsets that ascend and for arbitrary ones: always one
+    of the call's; where they ascend, the one that holds the step."""
+    rng = np.random.default_rng(4)
+    for case in range(500):
+        n, steps = int(rng.integers(1, 12)), int(rng.integers(1, 300))
+        ascend = case % 2 == 0
+        off = np.sort(rng.integers(0, steps + 1, n + 1)) if ascend else \
+            rng.integers(-400, 400, n + 1)
+        if ascend:
+            off[0], off[-1] = 0, steps
+        for t in range(steps):
+            lo, hi = 0, n
+            while hi - lo > 1:
+                mid = (lo + hi) >> 1
+                lo, hi = (mid, hi) if off[mid] <= t else (lo, mid)
+            assert 0 <= lo < n
+            if ascend:
+                assert off[lo] <= t < off[lo + 1]
+
+
+# ----- the references -----
+
+def directional(f, args, grads, rng, tol=2e-6):
+    """Each gradient against central differences along a random direction."""
+    for name, g in grads.items():
+        v = rng.standard_normal(args[name].shape)
+        h = 1e-6
+        up, down = dict(args), dict(args)
+        up[name], down[name] = args[name] + h * v, args[name] - h * v
+        diff = (f(up) - f(down)) / (2 * h)
+        assert abs(diff - (g * v).sum()) <= tol * (1 + abs(diff)), name
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("packed", [False, True])
+def test_scan_reference_against_differences(packed, softplus):
+    rng = np.random.default_rng(5)
+    off = np.array([0, 0, 4, 5, 9]) if packed else None
+    lead = (9,) if packed else (2, 5)
+    n, d, N, G = (4 if packed else 2), 4, 3, 2
+    s = rng.standard_normal
+    a = dict(x=s((*lead, d)), dt=s((*lead, d)), A=-np.abs(s((d, N))), B=s((*lead, G, N)),
+             C=s((*lead, G, N)), D=s(d), z=s((*lead, d)), bias=s(d), h0=s((n, d, N)))
+    dy, dl = s((*lead, d)), s((n, d, N))
+    kw = dict(offsets=off, softplus_=softplus, unit=K.U64, store="f64")
+
+    def loss(a):
+        o = K.scan(**a, **kw)
+        return (o["y"][0] * dy).sum() + (o["last"][0] * dl).sum()
+
+    o = K.scan(**a, **kw, dy=dy, dlast=dl)
+    directional(loss, a, {k: o["d" + k][0] for k in a}, rng)
+
+
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_conv_reference_against_differences(packed, act):
+    rng = np.random.default_rng(6)
+    off = np.array([0, 1, 1, 7, 9]) if packed else None
+    lead, n, d = ((9,), 4, 3) if packed else ((2, 5), 2, 3)
+    s = rng.standard_normal
+    a = dict(x=s((*lead, d)), w=s((d, 4)), bias=s(d), state=s((n, 3, d)))
+    dy, dl = s((*lead, d)), s((n, 3, d))
+
+    def loss(a):
+        o = K.conv(**a, offsets=off, act=act, unit=K.U64, store="f64")
+        return (o["y"][0] * dy).sum() + (o["last"][0] * dl).sum()
+
+    o = K.conv(**a, offsets=off, act=act, dy=dy, dlast=dl, unit=K.U64, store="f64")
+    directional(loss, a, {"x": o["dx"][0], "w": o["dw"][0], "bias": o["db"][0],
+                          "state": o["dstate"][0]}, rng)
+
+
+def test_norm_references_against_differences():
+    rng = np.random.default_rng(7)
+    s = rng.standard_normal
+    kw = dict(unit=K.U64, store="f64", stream="f64")
+    a = dict(x=s((4, 6)), w=s(6), res=s((4, 6)), scale=s(6))
+    dy, dr = s((4, 6)), s((4, 6))
+
+    def loss(a):
+        o = K.norm_in(**a, eps=1e-2, **kw)
+        return (o["y"][0] * dy).sum() + (o["r"][0] * dr).sum()
+
+    o = K.norm_in(**a, eps=1e-2, dy=dy, dr=dr, **kw)
+    directional(loss, a, {"x": o["dx"][0], "w": o["dw"][0], "res": o["dres"][0],
+                          "scale": o["dscale"][0]}, rng)
+    for order in ("gate_first", "norm_first"):
+        a = dict(x=s((4, 6)), w=s(6), gate=s((4, 6)), res=s((4, 6)), scale=s(6))
+
+        def loss(a):
+            return (K.norm_out(**a, order=order, eps=1e-2, **kw)["y"][0] * dy).sum()
+
+        o = K.norm_out(**a, order=order, eps=1e-2, dy=dy, **kw)
+        directional(loss, a, {"x": o["dx"][0], "w": o["dw"][0], "gate": o["dgate"][0], "res": dy,
+                              "scale": o["dscale"][0]}, rng)
+
+
+def test_a_planted_mistake_is_seen():
+    """The bounds are narrow enough that a wrong step shows: a coefficient off by 1e-4, a tap
+    taken one step late."""
+    rng = np.random.default_rng(8)
+    s = rng.standard_normal
+    a = dict(x=s((1, 40, 3)), dt=s((1, 40, 3)), A=-np.abs(s((3, 4))), B=s((1, 40, 1, 4)),
+             C=s((1, 40, 1, 4)))
+    good = K.scan(**a)
+    wrong = K.scan(**dict(a, A=a["A"] * (1 + 1e-4)))
+    assert (np.abs(wrong["y"][0] - good["y"][0]) > good["y"][1]).any()
+    x, w = s((1, 40, 3)), s((3, 3))
+    good = K.conv(x, w, None, None, None, "silu")
+    late = K.conv(x, np.roll(w, 1, 1), None, None, None, "silu")
+    assert (np.abs(late["y"][0] - good["y"][0]) > good["y"][1]).any()

@@ -1,0 +1,245 @@
+"""Selective scans on the GPU against the 64-bit reference and its error bounds."""
+import numpy as np
+import pytest
+import torch
+
+from preconditioned_cg_solver_amd import binding as B
+import block_util as K
+from block_gpu import DT, check, make, np64, offsets_of, unit_of
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+NAMES = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dbias", "dh0")
+
+
+def inputs(dtype, lead, d, N, groups=1, lengths=None, z=True, D=True, bias=True, h0=True,
+           strided=False, seed=0, rate=1.0):
+    r = make(seed, dtype)
+    off, n = offsets_of(lengths, lead)
+    x, dt = r(*lead, d, strided=strided), r(*lead, d, strided=strided)
+    both = r(*lead, 2 * groups * N + 8)
+    bs, cs = both[..., 4:4 + groups * N], both[..., 8 + groups * N:] if strided else \
+        both[..., 4 + groups * N:4 + 2 * groups * N]
+    bs, cs = (t.unflatten(-1, (groups, N)) for t in (bs, cs))
+    if not strided:
+        bs, cs = bs.contiguous(), cs.contiguous()
+    A = -rate * r.own(d, N).abs()
+    return dict(x=x, dt=dt, A=A, B=bs, C=cs, D=r.own(d) if D else None,
+                z=r(*lead, d, strided=strided) if z else None,
+                dt_bias=r.own(d) - 2 if bias else None, h0=r.own(n, d, N) if h0 else None,
+                offsets=off), r, n
+
+
+def run(dtype, lead, d, N, softplus=True, grads=True, **kw):
+    say("scan", dtype, lead, d, N, softplus, kw)
+    a, r, n = inputs(dtype, lead, d, N, **kw)
+    y, last, saved = B.sla_selscan_forward(**a, softplus=softplus, save=grads)
+    got = {"y": y, "last": last}
+    dy = dl = None
+    if grads:
+        dy, dl = r(*lead, d, strided=kw.get("strided", False)), r.own(n, d, N)
+        first = (a.pop("x"), a.pop("dt"), a.pop("A"), a.pop("B"), a.pop("C"))
+        got.update(zip(NAMES, B.sla_selscan_backward(*first, saved, dy, grad_last=dl, **a,
+                                                     softplus=softplus)))
+        a.update(zip(("x", "dt", "A", "B", "C"), first))
+    off = a.pop("offsets")
+    a["bias"] = a.pop("dt_bias")
+    want = K.scan(**{k: np64(v) for k, v in a.items()},
+                  offsets=None if off is None else np64(off).astype(int), softplus_=softplus,
+                  dy=np64(dy), dlast=np64(dl), unit=unit_of(dtype), store=dtype)
+    check(got, want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N", [1, 3, 4, 5, 8, 9, 16])
+def test_types_and_states(dtype, N):
+    run(dtype, (2, 37), 20, N)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 5, 15, 16, 17, 32, 33, 64, 100])
+@pytest.mark.parametrize("d", [1, 16, 70])
+def test_lengths_and_widths(steps, d):
+    run("bf16", (2, steps), d, 16)
+    run("f32", (1, steps), d, 6, z=False, D=False, bias=False, h0=False)
+
+
+@pytest.mark.parametrize("dtype", ["f64", "f32", "f16"])
+@pytest.mark.parametrize("N", [2, 16])
+def test_sequences_cut_into_chunks(dtype, N):
+    """Few channels and many steps: several chunks of a sequence, joined."""
+    run(dtype, (1, 700), 8, N)
+    run(dtype, (2, 333), 20, N, h0=False, rate=0.05)
+
+
+@pytest.mark.parametrize("lengths", [[0, 1, 2, 3, 0, 40, 19], [16, 16, 32], [1] * 20, [0, 0, 17],
+                                     [33, 0, 0], [300, 1, 0, 260, 47]])
+@pytest.mark.parametrize("dtype,N,d", [("bf16", 16, 20), ("f32", 4, 64), ("f64", 3, 5)])
+def test_packed(lengths, dtype, N, d):
+    run(dtype, (sum(lengths),), d, N, lengths=lengths)
+    run(dtype, (sum(lengths),), d, N, lengths=lengths, h0=False, z=False)
+
+
+@pytest.mark.parametrize("groups,d", [(2, 40), (4, 128), (3, 51), (8, 8)])
+def test_groups(groups, d):
+    run("bf16", (2, 35), d, 16, groups=groups)
+    run("f32", (60,), d, 5, groups=groups, lengths=[25, 0, 35])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_slices_of_wider_tensors(dtype):
+    run(dtype, (2, 33), 64, 16, strided=True)
+    run(dtype, (50,), 24, 7, lengths=[20, 30], strided=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f64"])
+def test_steps_without_softplus(dtype):
+    """Deltas of both signs: coefficients above 1 too."""
+    run(dtype, (2, 40), 33, 16, softplus=False, rate=0.3, bias=False)
+
+
+def test_many_channels_and_waves():
+    run("bf16", (1, 20), 1040, 16)
+    run("f32", (3, 18), 300, 8, groups=2)
+
+
+def test_no_steps():
+    a, r, n = inputs("f32", (2, 0), 5, 3)
+    y, last, saved = B.sla_selscan_forward(**a, save=True)
+    assert y.shape == (2, 0, 5) and torch.equal(last, a["h0"])
+    dl = r.own(2, 5, 3)
+    first = [a.pop(k) for k in ("x", "dt", "A", "B", "C")]
+    g = dict(zip(NAMES, B.sla_selscan_backward(*first, saved, first[0], grad_last=dl, **a)))
+    assert torch.equal(g["dh0"], dl)
+    assert not any(g[k].any() for k in ("dA", "dD", "dbias"))
+    a, _, _ = inputs("f32", (0, 4), 5, 3)
+    y, last, _ = B.sla_selscan_forward(**a)
+    assert y.shape == (0, 4, 5) and last.shape == (0, 5, 3)
+
+
+@pytest.mark.parametrize("steps", [1, 3, 20, 700])
+def test_state_updated_in_place(steps):
+    a, _, _ = inputs("bf16", (3, steps), 24, 16, seed=3)
+    y, last, _ = B.sla_selscan_forward(**a)
+    held = a["h0"]
+    y2, last2, _ = B.sla_selscan_forward(**a, h_last=held)
+    assert last2 is held and torch.equal(y, y2) and torch.equal(held, last)
+
+
+def test_steps_one_by_one_are_the_whole():
+    """To fp32 rounding: the kernels for few steps and for many sum over the states in
+    different orders."""
+    a, _, _ = inputs("f32", (2, 21), 36, 16, seed=4, h0=False)
+    whole, last, _ = B.sla_selscan_forward(**a)
+    st = torch.zeros(2, 36, 16, device="cuda")
+    parts = []
+    for t in range(21):
+        now = {k: v[:, t:t + 1] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+        now["h0"] = st
+        parts.append(B.sla_selscan_forward(**now, h_last=st)[0])
+    y = torch.cat(parts, 1)
+    assert torch.allclose(st, last, rtol=1e-6, atol=1e-6)
+    assert torch.allclose(y, whole, rtol=1e-5, atol=1e-5)
+
+
+def test_masked_steps_change_nothing():
+    """dt of -infinity (or the type's lowest value) is a delta of 0: the state passes through,
+    whatever B and C hold elsewhere, and a sequence of such steps keeps its state."""
+    a, _, _ = inputs("f32", (2, 90), 20, 16, seed=5)
+    for low in (float("-inf"), torch.finfo(torch.float32).min):
+        b = dict(a)
+        b["dt"] = a["dt"].clone()
+        b["dt"][:, 30:70] = low
+        b["dt"][1] = low
+        y, last, saved = B.sla_selscan_forward(**b, save=True)
+        assert torch.equal(last[1], a["h0"][1])
+        kept = {k: (torch.cat([v[:1, :30], v[:1, 70:]], 1) if k in ("x", "dt", "B", "C", "z") else v)
+                for k, v in a.items()}
+        kept["h0"] = a["h0"][:1].contiguous()
+        y2, last2, _ = B.sla_selscan_forward(**kept)
+        assert torch.allclose(last[:1], last2, rtol=1e-5, atol=1e-6)
+        assert torch.allclose(y[:1, 70:], y2[:, 30:], rtol=1e-4, atol=1e-5)
+        first = [b.pop(k) for k in ("x", "dt", "A", "B", "C")]
+        g = dict(zip(NAMES, B.sla_selscan_backward(*first, saved, torch.ones_like(y), **b)))
+        assert all(torch.isfinite(t).all() for t in g.values())
+        assert not g["ddt"][1].any()
+
+
+@pytest.mark.parametrize("N", [3, 16])
+def test_values_that_are_not_finite_stay_in_their_reach(N):
+    """An input that is not finite reaches its own channel from its step on, and no other
+    sequence; the states behind it are not finite."""
+    lengths = [20, 300, 30]
+    a, _, _ = inputs("f32", (350,), 20, N, lengths=lengths, seed=6)
+    y0, last0, _ = B.sla_selscan_forward(**a)
+    for v in (float("nan"), float("inf")):
+        b = dict(a)
+        b["x"] = a["x"].clone()
+        b["x"][40, 3] = v
+        y, last, _ = B.sla_selscan_forward(**b)
+        hit = torch.zeros_like(y, dtype=torch.bool)
+        hit[40:320, 3] = True
+        assert torch.equal(y[~hit], y0[~hit])
+        assert not torch.isfinite(y[40:320, 3]).any()
+        assert not torch.isfinite(last[1, 3]).any()
+        last[1, 3] = last0[1, 3]
+        assert torch.equal(last, last0)
+
+
+def test_strong_decay_and_no_decay():
+    """Coefficients that vanish, and rates of 0, which add up."""
+    a, _, _ = inputs("f32", (1, 600), 6, 4, seed=7, z=False)
+    a["A"][:2], a["A"][2:4] = -1e4, 0.0
+    y, last, saved = B.sla_selscan_forward(**a, save=True)
+    delta = torch.nn.functional.softplus(a["dt"].double() + a["dt_bias"].double())
+    dx = (delta * a["x"].double())[..., None] * a["B"].double()
+    assert torch.allclose(last[0, 2:4].double(), a["h0"][0, 2:4].double() + dx[0, :, 2:4].sum(0),
+                          rtol=1e-4, atol=1e-4)
+    assert torch.allclose(last[0, :2].double(), dx[0, -1, :2], rtol=1e-5, atol=1e-6)
+    first = [a.pop(k) for k in ("x", "dt", "A", "B", "C")]
+    g = B.sla_selscan_backward(*first, saved, torch.ones_like(y), **a)
+    assert all(t is None or torch.isfinite(t).all() for t in g)
+
+
+def test_two_runs_give_the_same_bits():
+    for kw in (dict(lead=(2, 900), d=24), dict(lead=(900,), d=24, lengths=[400, 3, 497])):
+        a, r, n = inputs("bf16", kw["lead"], kw["d"], 16, lengths=kw.get("lengths"), seed=8)
+        dy = r(*kw["lead"], kw["d"])
+        first = [a.pop(k) for k in ("x", "dt", "A", "B", "C")]
+        runs = []
+        for _ in range(2):
+            y, last, saved = B.sla_selscan_forward(*first, **a, save=True)
+            runs.append((y, last, saved, *B.sla_selscan_backward(*first, saved, dy, **a)))
+        assert all(torch.equal(p, q) for p, q in zip(*runs))
+
+
+def test_arbitrary_offsets_stay_within_the_arrays():
+    """Offsets that do not ascend give some result; what lies around the arrays is not
+    touched."""
+    off = torch.tensor([40, -3, 900, 12, 12, -70], device="cuda")
+    for steps in (50, 700):
+        a, r, _ = inputs("f32", (steps,), 20, 16, lengths=[steps // 5] * 5, seed=9)
+        a["offsets"] = off
+        room = torch.full((3, 5, 20, 16), 7.0, device="cuda")
+        y, last, saved = B.sla_selscan_forward(**a, save=True, h_last=room[1])
+        first = [a.pop(k) for k in ("x", "dt", "A", "B", "C")]
+        g = B.sla_selscan_backward(*first, saved, y, grad_last=a["h0"], **a)
+        torch.cuda.synchronize()
+        assert (room[0] == 7).all() and (room[2] == 7).all() and g[0].shape == y.shape
+
+
+def test_rows_past_32_bits():
+    """Steps that lie 2^30 elements apart: offsets of inputs past 2^31."""
+    wide = torch.zeros(5 << 30, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((1, 5, 32), (0, 1 << 30, 1))
+    a, r, _ = inputs("bf16", (1, 5), 32, 16, seed=10)
+    x.copy_(a["x"])
+    y0, last0, s0 = B.sla_selscan_forward(**a, save=True)
+    b = dict(a, x=x, z=x, dt=x)
+    c = dict(a, z=a["x"], dt=a["x"])
+    y, last, s = B.sla_selscan_forward(**b, save=True)
+    y1, last1, s1 = B.sla_selscan_forward(**c, save=True)
+    assert torch.equal(y, y1) and torch.equal(last, last1) and torch.equal(s, s1)
+    w = torch.randn(32, 4, device="cuda")
+    assert torch.equal(B.sla_conv_forward(x, w)[0], B.sla_conv_forward(a["x"], w)[0])
+    v = torch.ones(32, device="cuda")
+    assert torch.equal(B.sla_norm_in_forward(x, v)[0], B.sla_norm_in_forward(a["x"], v)[0])
