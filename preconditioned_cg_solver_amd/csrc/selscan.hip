@@ -285,57 +285,66 @@ __global__ __launch_bounds__(kWG) void scan_few(Args<T> p) {
 // not: in four factors, none of them 0, so that a state that is not finite
 // stays so; one that is 0 stays 0.
 template <typename C>
-__device__ __forceinline__ C carried(C h, C a, C sum) {
+__device__ __forceinline__ C factor(C a, C sum) {
   constexpr C kLow = sizeof(C) == 8 ? C(-1022) : C(-126);
   const C e = a == C(0) ? C(0) : a * sum * C(1.4426950408889634 / 4);
-  const C f = pow2(max(e, kLow));
+  return pow2(max(e, kLow));
+}
+template <typename C>
+__device__ __forceinline__ C carried(C h, C f) {
   return h == C(0) ? C(0) : h * f * f * f * f;
 }
 
 // Follows each state through the chunks, in place: what a chunk leaves from
 // nothing becomes what enters it.  A thread has one state of a sequence (packed: of
-// all); the loads of eight chunks are on their way together.
+// all); the loads of sixteen chunks are on their way together.
 template <typename T, bool BACKWARD>
-__global__ __launch_bounds__(kWG) void scan_join(Args<T> p) {
+__global__ __launch_bounds__(kLanes) void scan_join(Args<T> p) {
   using C = typename Compute<T>::type;
   const int64_t per = p.dim * p.states;
-  const int64_t k = (p.before + blockIdx.x) * kWG + threadIdx.x;
+  const int64_t k = (p.before + blockIdx.x) * kLanes + threadIdx.x;
   const int64_t seq = k / per, at = k % per;
   if (seq >= (p.offsets ? 1 : p.n_seq)) return;
   const int64_t channel = at / p.states;
   const C a = p.a[at];
   const C* start = BACKWARD ? p.grad_last : p.h0;
   C h = !p.offsets && start ? start[seq * per + at] : C(0);
-  constexpr int U = 8;
-  for (int i = 0; i < p.chunks; i += U) {
+  constexpr int U = 16;
+  const int64_t first = seq * p.chunks + (BACKWARD ? p.chunks - 1 : 0), step = BACKWARD ? -1 : 1;
+  C* ends = p.ends + first * per + at;
+  const C* from = ends;
+  const C* sums = p.deltas + first * p.dim + channel;
+  const int* cuts = p.cuts + first;
+  for (int left = p.chunks; left > 0; left -= U) {
     C end[U], sum[U];
-    bool cut[U];
-    int64_t row[U];
+    int cut[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = min(i + u, p.chunks - 1);
-      row[u] = seq * p.chunks + (BACKWARD ? p.chunks - 1 - j : j);
-      end[u] = p.ends[row[u] * per + at];
-      sum[u] = p.deltas[row[u] * p.dim + channel];
-      cut[u] = p.cuts[row[u]];
+      end[u] = *from;
+      sum[u] = *sums;
+      cut[u] = *cuts;
+      const int64_t hop = u + 1 < left ? step : 0;
+      from += hop * per, sums += hop * p.dim, cuts += hop;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u >= p.chunks) break;
-      p.ends[row[u] * per + at] = h;
-      h = cut[u] ? end[u] : carried(h, a, sum[u]) + end[u];
+      const C f = factor(a, sum[u]);
+      if (u < left) *ends = h;
+      ends += step * per;
+      h = cut[u] ? end[u] : carried(h, f) + end[u];
     }
   }
 }
 
-// Sequences without steps leave the state that they began with.
+// Sequences without steps leave the state that they began with: a workgroup takes
+// kWG elements of a state, of one sequence after the other.
 template <typename C>
 __global__ __launch_bounds__(kWG) void scan_empty(const int64_t* offsets, int64_t n_seq,
                                                   int64_t per, const C* from, C* to) {
-  for (int64_t s = blockIdx.x; s < n_seq; s += gridDim.x) {
+  const int64_t i = (int64_t)blockIdx.x * kWG + threadIdx.x;
+  for (int64_t s = blockIdx.y; s < n_seq; s += gridDim.y) {
     if (offsets && offsets[s + 1] > offsets[s]) continue;
-    for (int64_t i = threadIdx.x; i < per; i += kWG)
-      to[s * per + i] = from ? from[s * per + i] : C(0);
+    if (i < per) to[s * per + i] = from ? from[s * per + i] : C(0);
   }
 }
 
@@ -466,17 +475,17 @@ sla_status join(const Args<T>& p, const Plan& plan, bool backward, hipStream_t s
   if (plan.chunks < 2) return SLA_OK;
   Args<T> a = p;
   const int64_t n = (p.offsets ? 1 : p.n_seq) * p.dim * p.states;
-  return in_launches(a, (n + kWG - 1) / kWG, [&](dim3 grid) {
-    if (backward) scan_join<T, true><<<grid, kWG, 0, s>>>(a);
-    else scan_join<T, false><<<grid, kWG, 0, s>>>(a);
+  return in_launches(a, (n + kLanes - 1) / kLanes, [&](dim3 grid) {
+    if (backward) scan_join<T, true><<<grid, kLanes, 0, s>>>(a);
+    else scan_join<T, false><<<grid, kLanes, 0, s>>>(a);
   });
 }
 
 template <typename C>
 sla_status leave_empty(const sla_selscan_shape& q, const void* from, void* to, hipStream_t s) {
-  const unsigned grid = (unsigned)std::min<int64_t>(q.n_seq, 4096);
-  scan_empty<C><<<grid, kWG, 0, s>>>(q.d_offsets, q.n_seq, q.dim * q.n_state, (const C*)from,
-                                     (C*)to);
+  const int64_t per = q.dim * q.n_state;
+  const dim3 grid((unsigned)((per + kWG - 1) / kWG), (unsigned)std::min<int64_t>(q.n_seq, 256));
+  scan_empty<C><<<grid, kWG, 0, s>>>(q.d_offsets, q.n_seq, per, (const C*)from, (C*)to);
   SLA_HIP(hipGetLastError());
   return SLA_OK;
 }

@@ -33,6 +33,11 @@ namespace {
 // put them last, and keep it from taking so many ahead that the states leave the
 // registers.
 constexpr int kAhead = 2;
+// The last steps of a tile, whose coefficients there are registers for until the way back.
+template <typename C>
+constexpr int kept_steps() {
+  return sizeof(C) == 8 ? 1 : 4;
+}
 
 template <typename C>
 struct Drive {
@@ -161,8 +166,9 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
   if (threadIdx.x == 0 && w.block == 0) p.cuts[w.row] = cut;
 }
 
+// Two waves a SIMD; in fp64 one, with all of its registers.
 template <typename T, int NS, bool FAST>
-__global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
+__global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Args<T> p) {
   using C = typename Compute<T>::type;
   using R = Rows<C>;
   constexpr int TS = R::TS, EL = R::EL, N4 = 4 * NS;
@@ -298,11 +304,16 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
         return v;
       };
       // A step forward, from `before` to `now`, and back.
-      auto advance = [&](const Step& v, int i, const C (&before)[NS], C (&now)[NS]) {
+      auto coefficients = [&](const Step& v, C (&coef)[NS]) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) coef[j] = pow2(v.d.delta * a2[j]);
+      };
+      auto advance = [&](const Step& v, int i, const C (&coef)[NS], const C (&before)[NS],
+                         C (&now)[NS]) {
         C s = C(0);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          now[j] = pow2(v.d.delta * a2[j]) * before[j] + v.d.dx * v.b[j];
+          now[j] = coef[j] * before[j] + v.d.dx * v.b[j];
           const C m = v.c[j] * now[j];
           s += FAST || q * NS + j < p.states ? m : C(0);
         }
@@ -310,7 +321,8 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
         s += from_lane<kRor4>(s);
         sums[i][0][c] = s;
       };
-      auto retreat = [&](const Step& v, int i, const C (&before)[NS], const C (&now)[NS]) {
+      auto retreat = [&](const Step& v, int i, const C (&coef)[NS], const C (&before)[NS],
+                         const C (&now)[NS]) {
         C gb = C(0), qa = C(0), db[NS], dc[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -319,7 +331,7 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           db[j] = g * v.d.dx;
           const C m = g * v.b[j];
           gb += FAST || q * NS + j < p.states ? m : C(0);
-          mu[j] = pow2(v.d.delta * a2[j]) * g;
+          mu[j] = coef[j] * g;
           const C mh = mu[j] * before[j];
           const C ma = mh * a2[j];
           qa += FAST || q * NS + j < p.states ? ma : C(0);
@@ -353,8 +365,8 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
         }
       };
       if (n == TS && !starts && !ends) {
-        constexpr int G = kAhead;
-        C hs[TS][NS];
+        constexpr int G = kAhead, KEPT = kept_steps<C>();
+        C hs[TS][NS], kept[KEPT][NS];
         Step at[G], ahead[G];
 #pragma unroll
         for (int k = 0; k < G; ++k) ahead[k] = read(k);
@@ -367,8 +379,14 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int k = 0; k < G; ++k)
-            advance(at[k], i + k, i + k ? hs[i + k ? i + k - 1 : 0] : h0, hs[i + k]);
+          for (int k = 0; k < G; ++k) {
+            C coef[NS];
+            coefficients(at[k], coef);
+            advance(at[k], i + k, coef, i + k ? hs[i + k ? i + k - 1 : 0] : h0, hs[i + k]);
+            if (i + k >= TS - KEPT)
+#pragma unroll
+              for (int j = 0; j < NS; ++j) kept[i + k - (TS - KEPT)][j] = coef[j];
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -382,8 +400,15 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int k = 0; k < G; ++k)
-            retreat(at[k], i - k, i - k ? hs[i - k ? i - k - 1 : 0] : h0, hs[i - k]);
+          for (int k = 0; k < G; ++k) {
+            C coef[NS];
+            if (i - k >= TS - KEPT)
+#pragma unroll
+              for (int j = 0; j < NS; ++j) coef[j] = kept[i - k - (TS - KEPT)][j];
+            else
+              coefficients(at[k], coef);
+            retreat(at[k], i - k, coef, i - k ? hs[i - k ? i - k - 1 : 0] : h0, hs[i - k]);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
@@ -399,7 +424,10 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
           if (i > 0 && (starts >> i & 1))
             enter_states<NS, FAST>(before, p.h0, span_of(p, w, t0 + i).seq * p.dim + channel,
                                    p.states, q, live);
-          advance(read(i), i, before, now);
+          const Step v = read(i);
+          C coef[NS];
+          coefficients(v, coef);
+          advance(v, i, coef, before, now);
 #pragma unroll
           for (int j = 0; j < NS; ++j) hs[i + 1][j] = now[j];
         }
@@ -414,7 +442,10 @@ __global__ __launch_bounds__(kWG, 2) void scan_backward(Args<T> p) {
             enter_states<NS, FAST>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
           if (begins && i > 0)
             enter_states<NS, FAST>(before, p.h0, s * p.dim + channel, p.states, q, live);
-          retreat(read(i), i, before, now);
+          const Step v = read(i);
+          C coef[NS];
+          coefficients(v, coef);
+          retreat(v, i, coef, before, now);
           if (begins && p.grad_h0)
             put_states<NS, FAST>(mu, p.grad_h0, s * p.dim + channel, p.states, q, live);
         }
