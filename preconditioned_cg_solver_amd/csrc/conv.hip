@@ -133,29 +133,42 @@ __global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
 #pragma unroll
     for (int i = 0; i < U; ++i) in[i] = ahead[i];
     if (left > U) fetch(left - U);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (i >= left) break;
-      if (p.offsets && t + i == q.end) {
-        q = seq_at(p, r.dense, t + i);
-        look_back(t + i);
-        settle_past();
-      }
+    auto step = [&](const Pack<T, V>& x_in) {
+      C pre[V];
       Pack<T, V> o;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const C now = (C)in[i].v[v];
-        C pre = bias[v];
+        const C now = (C)x_in.v[v];
+        pre[v] = bias[v];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) pre += w[k][v] * past[k][v];
-        pre += w[K - 1][v] * now;
-        o.v[v] = (T)(p.silu ? silu(pre) : pre);
+        for (int k = 0; k < K - 1; ++k) pre[v] += w[k][v] * past[k][v];
+        pre[v] += w[K - 1][v] * now;
 #pragma unroll
         for (int k = 0; k + 1 < K - 1; ++k) past[k][v] = past[k + 1][v];
         past[K - 2][v] = now;
       }
+      if (p.silu)
+#pragma unroll
+        for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) o.v[v] = (T)pre[v];
       *(Pack<T, V>*)to = o;
       to += p.dim;
+    };
+    if (left >= U && (!p.offsets || t + U <= q.end)) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) step(in[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (i >= left) break;
+        if (p.offsets && t + i == q.end) {
+          q = seq_at(p, r.dense, t + i);
+          look_back(t + i);
+          settle_past();
+        }
+        step(in[i]);
+      }
     }
   }
   if (p.inlined && p.last && r.t1 == p.steps) {
@@ -292,6 +305,59 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
 #pragma unroll
       for (int i = 0; i < U; ++i) in[i] = in_ahead[i], up[i] = up_ahead[i];
       if (left > U) fetch(left - U);
+      // A step; what it completes is the gradient of the input K - 1 steps before.
+      auto step = [&](const Pack<T, V>& x_in, const Pack<T, V>& g_in, bool own) {
+        C pre[V], g[V], now[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          now[v] = (C)x_in.v[v], g[v] = (C)g_in.v[v], pre[v] = bias[v];
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) pre[v] += w[k][v] * past[k][v];
+          pre[v] += w[K - 1][v] * now[v];
+        }
+        if (p.silu)
+#pragma unroll
+          for (int v = 0; v < V; ++v) g[v] *= silu_slope(pre[v], sigmoid(pre[v]));
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int k = 0; k < K; ++k) sum[k][v] += w[k][v] * g[v];
+        if (own)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) dw[k][v] += g[v] * past[k][v];
+            dw[K - 1][v] += g[v] * now[v];
+            dw[K][v] += g[v];
+          }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int k = 0; k + 1 < K - 1; ++k) past[k][v] = past[k + 1][v];
+          past[K - 2][v] = now[v];
+        }
+      };
+      auto shift = [&] {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[k][v] = k + 1 < K ? sum[k + 1 < K ? k + 1 : k][v] : C(0);
+      };
+      if (t + U <= r.t1 && (!p.offsets || t + U <= q.end) && t - (K - 1) >= max(r.t0, q.begin)) {
+        // a group in the middle of the run and of a sequence
+        T* to = gx + (t - (K - 1)) * p.dim;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          step(in[i], up[i], true);
+          Pack<T, V> o;
+#pragma unroll
+          for (int v = 0; v < V; ++v) o.v[v] = (T)sum[0][v];
+          *(Pack<T, V>*)to = o;
+          to += p.dim;
+          shift();
+        }
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int64_t at = t + i;
@@ -310,32 +376,9 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
 #pragma unroll
             for (int v = 0; v < V; ++v) sum[k][v] = C(0);
         }
-        const bool own = at < r.t1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const C now = (C)in[i].v[v];
-          C pre = bias[v], g = (C)up[i].v[v];
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) pre += w[k][v] * past[k][v];
-          pre += w[K - 1][v] * now;
-          if (p.silu) {
-            g *= silu_slope(pre, sigmoid(pre));
-          }
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            sum[k][v] += w[k][v] * g;
-            if (own) dw[k][v] += g * (k < K - 1 ? past[k < K - 1 ? k : 0][v] : now);
-          }
-          if (own) dw[K][v] += g;
-#pragma unroll
-          for (int k = 0; k + 1 < K - 1; ++k) past[k][v] = past[k + 1][v];
-          past[K - 2][v] = now;
-        }
+        step(in[i], up[i], at < r.t1);
         emit(at - (K - 1), sum[0]);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int v = 0; v < V; ++v) sum[k][v] = k + 1 < K ? sum[k + 1 < K ? k + 1 : k][v] : C(0);
+        shift();
       }
     }
     if (!done && stop == q.end) finish();
