@@ -100,8 +100,9 @@ extern "C" {
 typedef enum {
     SLA_F64 = 0,
     SLA_F32 = 1,
-    SLA_BF16 = 2, /* recurrences and the AdamW step only: matrices are SLA_F64 or SLA_F32 */
-    SLA_F16 = 3,  /* recurrences only */
+    SLA_BF16 = 2, /* operators along sequences, norms and the AdamW step only: matrices are
+                   * SLA_F64 or SLA_F32 */
+    SLA_F16 = 3,  /* operators along sequences and norms only */
     SLA_DTYPE_RANGE_ = 0x7fffffff
 } sla_dtype;
 

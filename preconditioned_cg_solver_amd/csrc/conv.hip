@@ -451,7 +451,7 @@ sla_status check_shape(const sla_conv_shape* q) {
     set_error("a convolution has 2 to 4 taps");
     return SLA_ERR_UNSUPPORTED;
   }
-  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 28) || q->steps >= ((int64_t)1 << 40) ||
+  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 26) || q->steps >= ((int64_t)1 << 40) ||
       (__int128)(q->d_offsets ? 1 : q->n_seq) * (q->steps + 64) * (q->dim + 64) >=
           ((__int128)1 << 58) ||
       (__int128)q->n_seq * q->dim >= ((__int128)1 << 58)) {

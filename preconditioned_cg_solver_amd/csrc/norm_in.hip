@@ -25,7 +25,7 @@ sla_status check_shape(const sla_norm_shape* q) {
   if (q->stream != q->dtype && !(half && q->stream == SLA_F32))
     return refuse("the residual has x's dtype, or fp32 where that has 16 bits");
   if (!(q->eps >= 0.0) || std::isinf(q->eps)) return refuse("eps must be finite and not negative");
-  if (q->dim >= (1 << 30) || (__int128)q->rows * (q->dim + 1) >= ((__int128)1 << 58)) {
+  if (q->dim >= (1 << 26) || (__int128)q->rows * (q->dim + 1) >= ((__int128)1 << 58)) {
     set_error("sizes beyond what a call can index");
     return SLA_ERR_UNSUPPORTED;
   }

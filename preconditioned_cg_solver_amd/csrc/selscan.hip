@@ -370,7 +370,7 @@ sla_status check_shape(const sla_selscan_shape* q) {
     set_error("at most 16 states a channel");
     return SLA_ERR_UNSUPPORTED;
   }
-  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 26) || q->steps >= ((int64_t)1 << 40) ||
+  if (q->n_seq >= INT32_MAX || q->dim >= (1 << 23) || q->steps >= ((int64_t)1 << 40) ||
       (__int128)seqs * (q->steps + 16) * (q->dim + 64) * 16 >= ((__int128)1 << 59) ||
       (__int128)q->n_seq * q->dim * 16 >= ((__int128)1 << 59)) {
     set_error("sizes beyond what a call can index");
@@ -484,6 +484,7 @@ sla_status join(const Args<T>& p, const Plan& plan, bool backward, hipStream_t s
 template <typename C>
 sla_status leave_empty(const sla_selscan_shape& q, const void* from, void* to, hipStream_t s) {
   const int64_t per = q.dim * q.n_state;
+  if (!q.n_seq) return SLA_OK;
   const dim3 grid((unsigned)((per + kWG - 1) / kWG), (unsigned)std::min<int64_t>(q.n_seq, 256));
   scan_empty<C><<<grid, kWG, 0, s>>>(q.d_offsets, q.n_seq, per, (const C*)from, (C*)to);
   SLA_HIP(hipGetLastError());

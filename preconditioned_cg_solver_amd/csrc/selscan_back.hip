@@ -544,7 +544,7 @@ extern "C" sla_status sla_selscan_backward(const sla_selscan_shape* shape, const
   if ((st = check_in(q, in)) != SLA_OK) return st;
   if (!grads) return refuse("gradients are NULL");
   if (grad_seq < 0 || grad_step < 0) return refuse("negative stride");
-  if (empty(q)) return SLA_OK;
+  if (!q.dim) return SLA_OK;
   const sla_selscan_grads& o = *grads;
   if (!o.d_a) return refuse("a gradient is NULL");
   if (!no_steps(q)) {

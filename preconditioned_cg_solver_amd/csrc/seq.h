@@ -145,6 +145,6 @@ __device__ __forceinline__ double from_lane(double v) {
   return __hiloint2double(hi, lo);
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;             // within a quad
-constexpr int kRor4 = 0x124, kRor8 = 0x128, kRor12 = 0x12C;  // rotations of a row
+constexpr int kRor4 = 0x124, kRor8 = 0x128;  // rotations of a row
 
 }  // namespace sla

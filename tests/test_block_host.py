@@ -65,7 +65,7 @@ def norm_sizes(L, q):
     (dict(n_seq=-1), INVALID), (dict(steps=-1), INVALID), (dict(dim=-1), INVALID),
     (dict(dtype=9), INVALID), (dict(act=2), INVALID), (dict(width=1), UNSUPPORTED),
     (dict(width=5), UNSUPPORTED), (dict(steps=1 << 41), UNSUPPORTED),
-    (dict(dim=1 << 28), UNSUPPORTED), (dict(n_seq=1 << 30, steps=1 << 30), UNSUPPORTED)])
+    (dict(dim=1 << 26), UNSUPPORTED), (dict(n_seq=1 << 30, steps=1 << 30), UNSUPPORTED)])
 def test_conv_shapes_refused(L, kw, want):
     assert conv_sizes(L, conv_shape(**kw))[0] == want
     assert L.sla_last_error()
@@ -75,7 +75,7 @@ def test_conv_shapes_refused(L, kw, want):
     (dict(n_seq=-1), INVALID), (dict(steps=-1), INVALID), (dict(dim=-1), INVALID),
     (dict(dtype=9), INVALID), (dict(softplus=2), INVALID), (dict(groups=0), INVALID),
     (dict(groups=5), INVALID), (dict(n_state=0), INVALID), (dict(n_state=17), UNSUPPORTED),
-    (dict(steps=1 << 41), UNSUPPORTED), (dict(dim=1 << 26), UNSUPPORTED),
+    (dict(steps=1 << 41), UNSUPPORTED), (dict(dim=1 << 23), UNSUPPORTED),
     (dict(n_seq=1 << 30, steps=1 << 30), UNSUPPORTED)])
 def test_scan_shapes_refused(L, kw, want):
     assert scan_sizes(L, scan_shape(**kw))[0] == want
@@ -86,7 +86,7 @@ def test_scan_shapes_refused(L, kw, want):
     (dict(rows=-1), INVALID), (dict(dim=-1), INVALID), (dict(dtype=9), INVALID),
     (dict(stream=B.SLA_F16), INVALID), (dict(stream=B.SLA_F64), INVALID),
     (dict(dtype=B.SLA_F64), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
-    (dict(eps=float("inf")), INVALID), (dict(dim=1 << 30), UNSUPPORTED),
+    (dict(eps=float("inf")), INVALID), (dict(dim=1 << 26), UNSUPPORTED),
     (dict(rows=1 << 40, dim=1 << 29), UNSUPPORTED)])
 def test_norm_shapes_refused(L, kw, want):
     assert norm_sizes(L, norm_shape(**kw))[0] == want

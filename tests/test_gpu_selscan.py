@@ -114,6 +114,10 @@ def test_no_steps():
     a, _, _ = inputs("f32", (0, 4), 5, 3)
     y, last, _ = B.sla_selscan_forward(**a)
     assert y.shape == (0, 4, 5) and last.shape == (0, 5, 3)
+    y, last, saved = B.sla_selscan_forward(**a, save=True)
+    first = [a.pop(k) for k in ("x", "dt", "A", "B", "C")]
+    g = dict(zip(NAMES, B.sla_selscan_backward(*first, saved, first[0], **a)))
+    assert not any(g[k].any() for k in ("dA", "dD", "dbias"))  # sums of nothing
 
 
 @pytest.mark.parametrize("steps", [1, 3, 20, 700])
