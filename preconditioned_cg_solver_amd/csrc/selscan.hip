@@ -176,7 +176,6 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
         if constexpr (FULL)
           sums[i + ((q >> 1) | ((q & 1) << 1))][c] =
               fold_rows(fold_halves(s[0], s[1]), fold_halves(s[2], s[3]));
-        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       for (int i = 0; i < n; ++i) {
