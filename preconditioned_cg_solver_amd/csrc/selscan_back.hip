@@ -34,9 +34,9 @@ namespace {
 // registers.
 constexpr int kAhead = 2;
 // The last steps of a tile, whose coefficients there are registers for until the way back.
-template <typename C>
+template <typename T>
 constexpr int kept_steps() {
-  return sizeof(C) == 8 ? 1 : 4;
+  return sizeof(T) == 8 ? 1 : sizeof(T) == 4 ? 2 : 4;
 }
 
 template <typename C>
@@ -262,10 +262,13 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
         C delta[EL], slope[EL], ds[EL];
 #pragma unroll
         for (int e = 0; e < EL; ++e)
-          slope[e] = C(1), delta[e] = (C)ur.v[e] + s_bias[wave][cc + e], ds[e] = (C)gy.v[e];
+          delta[e] = (C)ur.v[e] + s_bias[wave][cc + e], ds[e] = (C)gy.v[e];
         if (p.softplus)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) delta[e] = softplus(delta[e], slope[e]);
+          for (int e = 0; e < EL; ++e) {
+            delta[e] = softplus(delta[e], slope[e]);
+            slopes[r][cc + e] = slope[e];
+          }
         if (gated)
 #pragma unroll
           for (int e = 0; e < EL; ++e) {
@@ -277,7 +280,6 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
           for (int e = 0; e < EL; ++e) {
             drive[r][cc + e] = {delta[e], delta[e] * (C)x.v[e]};
             dss[r][cc + e] = ds[e];
-            slopes[r][cc + e] = slope[e];
           }
       }
       keep_shared<C, NS>(bs, br);
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
         }
       };
       if (n == TS && !starts && !ends) {
-        constexpr int G = kAhead, KEPT = kept_steps<C>();
+        constexpr int G = kAhead, KEPT = kept_steps<T>();
         C hs[TS][NS], kept[KEPT][NS];
         Step at[G], ahead[G];
 #pragma unroll
@@ -453,26 +455,38 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
       wave_sync();
 
       if (r < n) {
-        C gx[EL];
+        C gx[EL], gb[EL], du[EL], dsv[EL], xv[EL];
         Pack<T, EL> ox, ou, oz{};
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-          const C xv = (C)x.v[e], gb = sums[r][1][cc + e], ds = dss[r][cc + e];
-          const C du = (sums[r][2][cc + e] * C(0.69314718055994531) + xv * gb) * slopes[r][cc + e];
-          ou.v[e] = (T)du;
-          dbias[e] += du;
-          gx[e] = drive[r][cc + e].delta * gb;
-          if (p.d) gx[e] += s_d[wave][cc + e] * ds;
-          ddd[e] += ds * xv;
-          ox.v[e] = (T)gx[e];
+          xv[e] = (C)x.v[e], gb[e] = sums[r][1][cc + e], dsv[e] = dss[r][cc + e];
+          du[e] = sums[r][2][cc + e] * C(0.69314718055994531) + xv[e] * gb[e];
+          gx[e] = drive[r][cc + e].delta * gb[e];
+          ddd[e] += dsv[e] * xv[e];
         }
-        if (gated)
+        if (p.softplus)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            C s = sums[r][0][cc + e];
-            if (p.d) s += s_d[wave][cc + e] * (C)x.v[e];
-            oz.v[e] = (T)((C)gy.v[e] * s * silu_slope((C)z.v[e], zsig[e]));
-          }
+          for (int e = 0; e < EL; ++e) du[e] *= slopes[r][cc + e];
+        C skip[EL];
+        if (p.d)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) skip[e] = s_d[wave][cc + e], gx[e] += skip[e] * dsv[e];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          dbias[e] += du[e];
+          ou.v[e] = (T)du[e], ox.v[e] = (T)gx[e];
+        }
+        if (gated) {
+          C total[EL];
+#pragma unroll
+          for (int e = 0; e < EL; ++e) total[e] = sums[r][0][cc + e];
+          if (p.d)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) total[e] += skip[e] * xv[e];
+#pragma unroll
+          for (int e = 0; e < EL; ++e)
+            oz.v[e] = (T)((C)gy.v[e] * total[e] * silu_slope((C)z.v[e], zsig[e]));
+        }
         store_some<FAST, EL>(p.grad_x + to, ox, some);
         store_some<FAST, EL>(p.grad_dt + to, ou, some);
         if (gated) store_some<FAST, EL>(p.grad_z + to, oz, some);
