@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   };
   int left = (int)(w.t1 - w.t0);  // steps
   fetch(min(left, TS));
-  Span now = p.offsets ? span_of(p, w, w.t0) : Span{};
+  Span now = p.offsets ? waited_for(span_of(p, w, w.t0)) : Span{};
 
   for (int64_t t0 = w.t0; left > 0; t0 += TS, left -= TS) {
     const int n = min(left, TS);
@@ -115,10 +115,11 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
     if constexpr (FULL) keep_shared<C, NS>(cs, cr);
     if (left > TS) fetch(min(left - TS, TS));
     unsigned starts, ends;
-    edges_of<TS>(p, w, now, t0, n, starts, ends);
+    int64_t mine;
+    edges_of<TS, false>(p, w, now, t0, n, starts, ends, mine);
     if (!p.offsets) starts = 0;  // h holds what enters
     auto begin = [&](int i) {
-      const int64_t s = span_of(p, w, t0 + i).seq;
+      const int64_t s = from_lane_of(mine, i);
       enter_states<NS, FAST>(h, p.h0, s * p.dim + channel, p.states, q, live);
       cut = true;
     };
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
           s = fold_halves(s, s);
           sums[i][c] = fold_rows(s, s);
           if (ends >> i & 1) {
-            const int64_t at = span_of(p, w, t0 + i).seq;
+            const int64_t at = from_lane_of(mine, i);
             put_states<NS, FAST>(h, p.h_last, at * p.dim + channel, p.states, q, live);
           }
         }
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
     total += sum;
     wave_sync();
     if constexpr (FULL) {
-      if (r < n) {
+      if (r < n && t0 + r >= w.lo && t0 + r < w.hi) {
         C v[EL];
         Pack<T, EL> o;
 #pragma unroll

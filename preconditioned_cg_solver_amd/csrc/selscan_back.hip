@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
     us.move(), gs.move(), zs.move(), ct.move();
   };
   fetch((int)(w.t1 - last));
-  Span now = p.offsets ? span_of(p, w, last) : Span{};
+  Span now = p.offsets ? waited_for(span_of(p, w, last)) : Span{};
   for (int64_t t0 = last; t0 >= w.t0; t0 -= TS) {
     const int n = (int)min((int64_t)TS, w.t1 - t0);
     C delta[EL], ds[EL], slope;
@@ -106,12 +106,15 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
     if (gated)
 #pragma unroll
       for (int e = 0; e < EL; ++e) ds[e] *= silu((C)zr.v[e]);
+    const unsigned inside = inside_of(w, t0, TS);
+    const bool is = inside >> r & 1;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) pull[r][cc + e] = {delta[e], ds[e]};
-    keep_shared<C, NS>(cs, cr);
+    for (int e = 0; e < EL; ++e) pull[r][cc + e] = {is ? delta[e] : C(0), is ? ds[e] : C(0)};
+    keep_shared<C, NS>(cs, cr, inside);
     if (t0 > w.t0) fetch(TS);
     unsigned starts, ends;
-    edges_of<TS>(p, w, now, t0, n, starts, ends);
+    int64_t mine;
+    edges_of<TS, true>(p, w, now, t0, n, starts, ends, mine);
     wave_sync();
     C sum = C(0);
     struct Step {
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kWG) void scan_back_local(Args<T> p) {
     } else {
       for (int i = n - 1; i >= 0; --i) {
         if (ends >> i & 1) {
-          const int64_t s = span_of(p, w, t0 + i).seq;
+          const int64_t s = from_lane_of(mine, i);
           enter_states<NS, FAST>(mu, p.grad_last, s * p.dim + channel, p.states, q, live);
           cut = true;
         }
@@ -250,13 +253,16 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
     for (int i = lane; i < TS * 2 * N4; i += kLanes)
       (&s_bc[0][wave][0][0][0])[i] = (&s_bc[1][wave][0][0][0])[i] = C(0);
   }
-  Span now = p.offsets ? span_of(p, w, last) : Span{};
+  Span now = p.offsets ? waited_for(span_of(p, w, last)) : Span{};
   int turn = 0;
 
   for (int64_t t0 = last; t0 >= w.t0; t0 -= TS, turn ^= 1) {
     const int n = (int)min((int64_t)TS, w.t1 - t0);
+    // Rows of no sequence count as zeros, whatever they hold, and have gradients of zero.
+    const unsigned inside = inside_of(w, t0, TS);
     if (!idle) {
       const Pack<T, EL> x = xr, z = zr, gy = gr;
+      const bool is = inside >> r & 1;
       C zsig[EL];
       {
         C delta[EL], slope[EL], ds[EL];
@@ -278,19 +284,20 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
         if (!FAST || some > 0)  // else they stay 0, as what does not exist adds nothing to sums
 #pragma unroll
           for (int e = 0; e < EL; ++e) {
-            drive[r][cc + e] = {delta[e], delta[e] * (C)x.v[e]};
-            dss[r][cc + e] = ds[e];
+            drive[r][cc + e] = {is ? delta[e] : C(0), is ? delta[e] * (C)x.v[e] : C(0)};
+            dss[r][cc + e] = is ? ds[e] : C(0);
           }
       }
-      keep_shared<C, NS>(bs, br);
-      keep_shared<C, NS>(cs, cr);
+      keep_shared<C, NS>(bs, br, inside);
+      keep_shared<C, NS>(cs, cr, inside);
       C h0[NS];
 #pragma unroll
-      for (int j = 0; j < NS; ++j) h0[j] = enter[j];
+      for (int j = 0; j < NS; ++j) h0[j] = inside & 1 ? enter[j] : C(0);
       settle(h0);
       if (t0 > w.t0) fetch(TS);
       unsigned starts, ends;
-      edges_of<TS>(p, w, now, t0, n, starts, ends);
+      int64_t mine;
+      edges_of<TS, true>(p, w, now, t0, n, starts, ends, mine);
       wave_sync();
 
       struct Step {
@@ -424,8 +431,8 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
 #pragma unroll
           for (int j = 0; j < NS; ++j) before[j] = hs[i][j];
           if (i > 0 && (starts >> i & 1))
-            enter_states<NS, FAST>(before, p.h0, span_of(p, w, t0 + i).seq * p.dim + channel,
-                                   p.states, q, live);
+            enter_states<NS, FAST>(before, p.h0, from_lane_of(mine, i) * p.dim + channel, p.states,
+                                   q, live);
           const Step v = read(i);
           C coef[NS];
           coefficients(v, coef);
@@ -436,7 +443,7 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
 #pragma unroll 1
         for (int i = n - 1; i >= 0; --i) {
           const bool begins = starts >> i & 1, stops = ends >> i & 1;
-          const int64_t s = begins || stops ? span_of(p, w, t0 + i).seq : 0;
+          const int64_t s = from_lane_of(mine, i);
           C before[NS], now[NS];
 #pragma unroll
           for (int j = 0; j < NS; ++j) before[j] = hs[i][j], now[j] = hs[i + 1][j];
@@ -459,7 +466,7 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
         Pack<T, EL> ox, ou, oz{};
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-          xv[e] = (C)x.v[e], gb[e] = sums[r][1][cc + e], dsv[e] = dss[r][cc + e];
+          xv[e] = is ? (C)x.v[e] : C(0), gb[e] = sums[r][1][cc + e], dsv[e] = dss[r][cc + e];
           du[e] = sums[r][2][cc + e] * C(0.69314718055994531) + xv[e] * gb[e];
           gx[e] = drive[r][cc + e].delta * gb[e];
           ddd[e] += dsv[e] * xv[e];
@@ -467,6 +474,8 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
         if (p.softplus)
 #pragma unroll
           for (int e = 0; e < EL; ++e) du[e] *= slopes[r][cc + e];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) du[e] = is ? du[e] : C(0);
         C skip[EL];
         if (p.d)
 #pragma unroll
@@ -485,7 +494,7 @@ __global__ __launch_bounds__(kWG, sizeof(T) == 8 ? 1 : 2) void scan_backward(Arg
             for (int e = 0; e < EL; ++e) total[e] += skip[e] * xv[e];
 #pragma unroll
           for (int e = 0; e < EL; ++e)
-            oz.v[e] = (T)((C)gy.v[e] * total[e] * silu_slope((C)z.v[e], zsig[e]));
+            oz.v[e] = is ? (T)((C)gy.v[e] * total[e] * silu_slope((C)z.v[e], zsig[e])) : T(0);
         }
         store_some<FAST, EL>(p.grad_x + to, ox, some);
         store_some<FAST, EL>(p.grad_dt + to, ou, some);
