@@ -592,7 +592,10 @@ sla_status sla_adamw_set_state(sla_adamw_t opt, const float *d_m, const float *d
  * captured in a HIP graph.  Two calls on different streams need workspaces of
  * their own.  Sums are made in a fixed order: two runs give the same bits.
  * Outputs must not overlap inputs or each other, but where said otherwise.
- * Whatever the offsets of packed sequences hold, no access leaves the arrays.
+ * Packed rows before the first offset or behind the last (a batch that is padded) are of
+ * no sequence: whatever they hold, the forward calls leave their outputs as they
+ * were, and their gradients are zeros.  Whatever the offsets hold, no access leaves
+ * the arrays.
  */
 
 /*

@@ -51,9 +51,21 @@ __device__ __forceinline__ Seq seq_at(const ConvArgs<T>& p, int64_t dense, int64
   return {s, p.offsets[s], p.offsets[s + 1]};
 }
 
-// A thread's run of steps.
+// The same for a step behind sequence q: mostly one of the next few.
+template <typename T>
+__device__ __forceinline__ Seq seq_after(const ConvArgs<T>& p, const Seq& q, int64_t t) {
+  int64_t s = q.s;
+  for (int i = 0; i < 4; ++i) {
+    if (s + 1 >= p.n_seq || p.offsets[s + 1] > t) return {s, p.offsets[s], p.offsets[s + 1]};
+    ++s;
+  }
+  return seq_at(p, 0, t);
+}
+
+// A thread's run of steps, from `from` to `to`; t0 <= t < t1 of them are of sequences (packed
+// rows before the first and behind the last are of none).
 struct Run {
-  int64_t dense, t0, t1, at, col;
+  int64_t dense, t0, t1, at, col, from, to, hi;
   bool some;
 };
 template <int V, typename T>
@@ -65,8 +77,12 @@ __device__ __forceinline__ Run run_of(const ConvArgs<T>& p) {
   r.col = ((k % p.groups * p.side + wave % p.side) * kLanes + (threadIdx.x & 63)) * V;
   r.some = run < p.all && r.col < p.dim;
   r.dense = p.offsets ? 0 : run / p.runs;
-  r.t0 = (run - r.dense * p.runs) * p.run;
-  r.t1 = min(r.t0 + p.run, p.steps);
+  r.from = (run - r.dense * p.runs) * p.run;
+  r.to = min(r.from + p.run, p.steps);
+  const int64_t lo = p.offsets ? min(max(p.offsets[0], (int64_t)0), p.steps) : 0;
+  r.hi = p.offsets ? min(max(p.offsets[p.n_seq], lo), p.steps) : p.steps;
+  r.t0 = max(r.from, lo);
+  r.t1 = min(r.to, r.hi);
   r.at = p.offsets ? 0 : r.dense * p.steps;
   return r;
 }
@@ -90,7 +106,7 @@ __global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
   using C = typename Compute<T>::type;
   constexpr int U = 8;
   const Run r = run_of<V>(p);
-  if (!r.some) return;
+  if (!r.some || r.t0 >= r.t1) return;
   C w[K][V], bias[V], past[K - 1][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -163,7 +179,7 @@ __global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
       for (int i = 0; i < U; ++i) {
         if (i >= left) break;
         if (p.offsets && t + i == q.end) {
-          q = seq_at(p, r.dense, t + i);
+          q = seq_after(p, q, t + i);
           look_back(t + i);
           settle_past();
         }
@@ -223,7 +239,7 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
   for (int k = 0; k <= K; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = C(0);
-  if (r.some) {
+  if (r.some && r.t0 < r.t1) {
     C w[K][V], bias[V], past[K - 1][V], sum[K][V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -280,7 +296,7 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
         emit(q.end - (K - 1) + j, sum[j]);
       }
     };
-    const int64_t stop = min(r.t1 + K - 1, p.steps);
+    const int64_t stop = min(r.t1 + K - 1, r.hi);
     Pack<T, V> in[U], up[U], in_ahead[U], up_ahead[U];
     const T *from = x + r.t0 * p.x_step, *gfrom = gy ? gy + r.t0 * p.gy_step : nullptr;
     auto fetch = [&](int left) {
@@ -368,7 +384,7 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
             done = true;
             break;
           }
-          q = seq_at(p, r.dense, at);
+          q = seq_after(p, q, at);
           look_back(at);
           settle_past();
 #pragma unroll
@@ -382,6 +398,10 @@ __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
       }
     }
     if (!done && stop == q.end) finish();
+  }
+  if (p.offsets && r.some) {  // rows of no sequence have gradients of zero
+    for (int64_t t = r.from; t < r.to; ++t)
+      if (t < r.t0 || t >= r.t1) *(Pack<T, V>*)(p.grad_x + t * p.dim + r.col) = Pack<T, V>{};
   }
   // over the workgroup's runs, and one row of parts for it
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;

@@ -45,7 +45,8 @@ def test_lengths_and_widths(steps, d):
     run("f32", (1, steps), d, 3, state=False)
 
 
-@pytest.mark.parametrize("lengths", [[0, 1, 2, 3, 0, 40, 9], [5], [1] * 12, [0, 0, 17], [33, 0, 0]])
+@pytest.mark.parametrize("lengths", [[0, 1, 2, 3, 0, 40, 9], [5], [1] * 12, [0, 0, 17], [33, 0, 0],
+                                     [3] + [0] * 9 + [20]])
 @pytest.mark.parametrize("d", [3, 256])
 @pytest.mark.parametrize("k", [2, 4])
 def test_packed(lengths, d, k):
@@ -119,6 +120,34 @@ def test_values_that_are_not_finite_stay_in_their_reach():
             assert (y[hit] == 0).all()
         else:
             assert not torch.isfinite(y[hit]).any()
+
+
+@pytest.mark.parametrize("before,behind", [(0, 40), (5, 0), (17, 133)])
+@pytest.mark.parametrize("d", [3, 512])
+def test_padded_rows_are_of_no_sequence(before, behind, d):
+    """Rows before the first and behind the last sequence hold NaN: the results are those without
+    them, the weights' gradients too, and their own gradients are zeros."""
+    r = make(11, "bf16")
+    lengths = [30, 0, 2, 100, 1]
+    n = sum(lengths)
+    off, _ = offsets_of(lengths, (n,))
+    x, w, b, st = r(n, d), r.own(d, 4), r.own(d), r(5, 3, d)
+    dy, dl = r(n, d), r(5, 3, d)
+
+    def pad(t):
+        return torch.cat([t.new_full((before, d), float("nan")), t,
+                          t.new_full((behind, d), float("nan"))])
+
+    y, last = B.sla_conv_forward(x, w, bias=b, state=st, offsets=off)
+    g = B.sla_conv_backward(x, w, dy, bias=b, state=st, grad_last=dl, offsets=off)
+    py, plast = B.sla_conv_forward(pad(x), w, bias=b, state=st, offsets=off + before)
+    pg = B.sla_conv_backward(pad(x), w, pad(dy), bias=b, state=st, grad_last=dl,
+                             offsets=off + before)
+    assert torch.equal(py[before:before + n], y) and torch.equal(plast, last)
+    assert torch.equal(pg[0][before:before + n], g[0]) and torch.equal(pg[3], g[3])
+    assert not pg[0][:before].any() and not pg[0][before + n:].any()
+    assert torch.allclose(pg[1], g[1], rtol=1e-4, atol=1e-4)  # other runs, other order
+    assert torch.allclose(pg[2], g[2], rtol=1e-4, atol=1e-4)
 
 
 def test_arbitrary_offsets_leave_the_neighbours_alone():

@@ -72,7 +72,8 @@ def test_sequences_cut_into_chunks(dtype, N):
 
 
 @pytest.mark.parametrize("lengths", [[0, 1, 2, 3, 0, 40, 19], [16, 16, 32], [1] * 20, [0, 0, 17],
-                                     [33, 0, 0], [300, 1, 0, 260, 47]])
+                                     [33, 0, 0], [300, 1, 0, 260, 47],
+                                     [3] + [0] * 70 + [20], [1, 0] * 90 + [5]])
 @pytest.mark.parametrize("dtype,N,d", [("bf16", 16, 20), ("f32", 4, 64), ("f64", 3, 5)])
 def test_packed(lengths, dtype, N, d):
     run(dtype, (sum(lengths),), d, N, lengths=lengths)
@@ -214,6 +215,40 @@ def test_two_runs_give_the_same_bits():
             y, last, saved = B.sla_selscan_forward(*first, **a, save=True)
             runs.append((y, last, saved, *B.sla_selscan_backward(*first, saved, dy, **a)))
         assert all(torch.equal(p, q) for p, q in zip(*runs))
+
+
+@pytest.mark.parametrize("before,behind", [(0, 40), (5, 0), (17, 33), (0, 300), (200, 1)])
+@pytest.mark.parametrize("lengths", [[30, 0, 5, 100], [700], [1, 0, 0, 16]])
+def test_padded_rows_are_of_no_sequence(before, behind, lengths):
+    """Rows before the first and behind the last sequence hold NaN: the results are those without
+    them, the parameters' gradients too, and their own gradients are zeros."""
+    n = sum(lengths)
+    a, r, _ = inputs("f32", (n,), 20, 16, lengths=lengths, seed=12)
+    dy, dl = r(n, 20), r.own(len(lengths), 20, 16)
+
+    def pad(t):
+        return torch.cat([t.new_full((before, *t.shape[1:]), float("nan")), t,
+                          t.new_full((behind, *t.shape[1:]), float("nan"))])
+
+    b = {k: pad(v) if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    b["offsets"] = a["offsets"] + before
+    keep = slice(before, before + n)
+    outs = []
+    for q, g in ((a, dy), (b, pad(dy))):
+        y, last, saved = B.sla_selscan_forward(**q, save=True)
+        first = [q.pop(k) for k in ("x", "dt", "A", "B", "C")]
+        outs.append((y, last, dict(zip(NAMES, B.sla_selscan_backward(*first, saved, g, grad_last=dl,
+                                                                     **q)))))
+    (y, last, g), (py, plast, pg) = outs
+    # chunks and tiles lie elsewhere: equal to fp32 rounding
+    close = dict(rtol=1e-4, atol=1e-4)
+    assert torch.allclose(py[keep], y, **close) and torch.allclose(plast, last, **close)
+    for k in NAMES:
+        if g[k].shape[0] == n:
+            assert torch.allclose(pg[k][keep], g[k], **close), k
+            assert not pg[k][:before].any() and not pg[k][before + n:].any(), k
+        else:
+            assert torch.allclose(pg[k], g[k], rtol=1e-4, atol=1e-3), k
 
 
 def test_arbitrary_offsets_stay_within_the_arrays():
