@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kWG) void conv_last(ConvArgs<T> p) {
 template <typename T, int K, int V, bool STREAM>
 __global__ __launch_bounds__(kWG) void conv_backward(ConvArgs<T> p) {
   using C = typename Compute<T>::type;
-  constexpr int U = 4;
+  constexpr int U = V == 1 ? 8 : 4;
   __shared__ C red[kWaves - 1][kLanes * V];
   const Run r = run_of<V>(p);
   C dw[K + 1][V];  // the bias's last
@@ -500,10 +500,13 @@ Cut cut_of(const sla_conv_shape& q, int v, bool backward) {
   const int64_t seqs = q.d_offsets ? 1 : q.n_seq;
   // Waves that fill the device a few times over, of runs that look back seldom.  8 x 2048 x
   // 2048 bf16, us, by the waves that are wanted: forward 2048 28.7, 4096 26.9, 8192 28.9;
-  // backward 1024 98, 2048 67, 4096 72, 8192 83.
+  // backward 1024 69, 2048 54, 4096 61, 8192 75.  Longer runs make fewer parts of the weights'
+  // gradients, shorter ones hide more of memory's latency: backward with runs of 64, 128
+  // and 256 steps 8 x 4096 x 4096 bf16 200, 180, 165, 50003 x 768 fp32 103, 116, 112.
   const int64_t want = std::max<int64_t>(1, (backward ? 2048 : 4096) / (c.blocks * seqs));
   const int64_t run = (q.steps + want - 1) / want;
-  c.run = (int)std::min<int64_t>(std::max<int64_t>((run + 7) / 8 * 8, 8), backward ? 128 : 64);
+  const int64_t most = backward && v >= 4 ? 256 : 64;
+  c.run = (int)std::min(std::max<int64_t>((run + 7) / 8 * 8, 8), most);
   c.runs = (q.steps + c.run - 1) / c.run;
   c.all = c.runs * seqs;
   // Waves stand side by side until they reach 512 bytes of a row (backward 1024), so that
