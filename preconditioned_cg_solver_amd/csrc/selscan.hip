@@ -5,7 +5,9 @@
 // fused sums, so with 16 states it is bound by arithmetic, not bytes.  A lane keeps
 // its states in registers through all steps; what depends on the channel alone
 // (softplus, the gate) is worked out once per element in another sharing of the
-// tile among the lanes, and handed over through LDS of the wave.
+// tile among the lanes, and handed over through LDS of the wave.  A tile takes 486 vector
+// instructions; 8 x 2048 x 2048 x 16 states bf16, a wave a SIMD, 214 us with the vector unit
+// at work 60% of them, 16 x 2048 x 2048 332.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -35,7 +37,8 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
   __shared__ C s_sum[FULL ? kWavesOf : 1][TS][kChannels];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place w = place_of<T, kWavesOf>(p);
-  if (w.some <= 0 || (!FULL && w.part == p.chunks - 1)) return;  // what the last leaves is not asked
+  // what the last chunk leaves is not asked
+  if (w.some <= 0 || (!FULL && w.part == p.chunks - 1)) return;
   auto& drive = s_drive[wave];
   auto& bs = s_b[wave];
   auto& cs = s_c[FULL ? wave : 0];
@@ -222,9 +225,10 @@ __global__ __launch_bounds__(kWG) void scan_forward(Args<T> p) {
 }
 
 // Sequences of a few steps, a serving step above all: 4 lanes take a channel from the
-// first step to the last, its states among them, without LDS.  16 x 4096 x 16 states bf16,
-// one step: 3.4 us for 8.9 in tiles.
-constexpr int kFew = 4;
+// first step to the last, its states among them, without LDS.  n x steps x 4096 x 16
+// states bf16, here and in tiles, us: 16 x 1 4.8 and 8.6, 16 x 4 7.1 and 9.9, 16 x 8 10.1 and
+// 11.4, 16 x 16 15.9 and 14.3; 64 x 1 10.5 and 22.6, 64 x 8 25.3 and 29.7, 64 x 16 45.7 and 38.5.
+constexpr int kFew = 8;
 template <typename T, int NS, bool FAST>
 __global__ __launch_bounds__(kWG) void scan_few(Args<T> p) {
   using C = typename Compute<T>::type;
