@@ -598,6 +598,12 @@ sla_status sla_adamw_set_state(sla_adamw_t opt, const float *d_m, const float *d
  * the arrays.
  */
 
+/* Zeros in the rows of a dense (steps, dim) d_y that are of no sequence, for outputs whose
+ * memory was not set before.  SLA_ERR_INVALID_ARG on NULL arrays, negative sizes or an
+ * unknown dtype, SLA_ERR_UNSUPPORTED on sizes beyond what a call can index. */
+sla_status sla_rows_clear(const int64_t *d_offsets, int64_t n_seq, int64_t steps, int64_t dim,
+                          sla_dtype dtype, void *d_y, void *stream);
+
 /*
  * Causal convolution along a sequence, per channel, with 2 to 4 taps:
  *   pre_t = bias + sum_{k < width} weight[k] x_{t - width + 1 + k},

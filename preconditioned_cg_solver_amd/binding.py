@@ -165,6 +165,7 @@ def _declare(L):
         "sla_adamw_get_state": ([vp, vp, vp, vp], st),
         "sla_adamw_set_state": ([vp, vp, vp, vp], st),
         "sla_conv_sizes": ([vp, ctypes.POINTER(sz)], st),
+        "sla_rows_clear": ([vp, i64, i64, i64, ctypes.c_int, vp, vp], st),
         "sla_conv_forward": ([vp, vp, i64, i64, vp, vp, vp, vp, vp, vp], st),
         "sla_conv_backward": ([vp, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp,
                                sz, vp], st),
@@ -1113,6 +1114,26 @@ def _conv_sizes(q: ConvShape) -> int:
     return work.value
 
 
+def _clear_rows(q, y, raw):
+    _check(lib().sla_rows_clear(q.d_offsets, q.n_seq, q.steps, q.dim, q.dtype, _raw(y), raw))
+
+
+def sla_rows_clear(y: torch.Tensor, offsets: torch.Tensor, stream=None) -> None:
+    """Zeros in the rows of a packed, dense y (steps, channels) that are of no sequence:
+    before the first offset and behind the last."""
+    if offsets is None:
+        raise ValueError("offsets must be given")
+    n, t, d = _sequences(y, offsets)
+    if not y.is_contiguous():
+        raise ValueError("y must be dense")
+    dev = _device_of((("y", y), ("offsets", offsets)))
+    raw, ctx, used = _enter(dev, stream)
+    _check(lib().sla_rows_clear(offsets.data_ptr(), n, t, d, _DTYPES[y.dtype], _raw(y), raw))
+    if used is not None:
+        _record(used, y, offsets)
+    _written(y)
+
+
 def sla_conv_sizes(x, weight, offsets=None, act: str = "silu") -> int:
     """Bytes of the backward pass's workspace."""
     return _conv_sizes(_conv_shape(x, weight, offsets, act))
@@ -1128,7 +1149,8 @@ def sla_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     x as in sla_linrec_forward, strided or packed; weight (channels, taps) and bias
     (channels) float32 (float64 for float64).  state (sequences, taps - 1, channels), of
     x's dtype: the inputs before each sequence, oldest first (None: zeros); last, of the same
-    form, receives what follows needs, and may be state itself.  `stream` as in
+    form, receives what follows needs, and may be state itself.  Packed rows before the first
+    offset or behind the last count as nothing and give zeros.  `stream` as in
     sla_linrec_forward.  Returns (y, last)."""
     q = _conv_shape(x, weight, offsets, act)
     pt = _param_dtype(x)
@@ -1145,6 +1167,8 @@ def sla_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
         if last is None:
             last = torch.empty(held, dtype=x.dtype, device=dev)
             pl = _raw(last)
+    if offsets is not None:
+        _clear_rows(q, y, raw)
     _check(lib().sla_conv_forward(ctypes.byref(q), *px, pw, pb, ps, _raw(y), pl, raw))
     if used is not None:
         _record(used, x, weight, bias, state, offsets, given)
@@ -1250,7 +1274,8 @@ def sla_selscan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
     x's dtype, at most 16 states, channels in equal groups of neighbours; A (channels,
     states), D and dt_bias (channels) and the states h0, h_last (sequences, channels,
     states) float32 (float64 for float64).  h_last may be given to be overwritten, for dense
-    sequences h0 itself.  `stream` as in sla_linrec_forward.  Returns (y, h_last, saved);
+    sequences h0 itself.  Packed rows before the first offset or behind the last count as
+    nothing and give zeros.  `stream` as in sla_linrec_forward.  Returns (y, h_last, saved);
     `saved` (None unless save) is what the backward pass needs."""
     a = _Selscan(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
     pl = _dense(h_last, "h_last", a.held, a.pt)
@@ -1266,6 +1291,8 @@ def sla_selscan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
             pl = _raw(h_last)
         saved = torch.empty(n_saved // a.pt.itemsize, dtype=a.pt, device=dev) if save else None
         work = _scratch(n_work, dev)
+    if offsets is not None:
+        _clear_rows(a.q, y, raw)
     _check(lib().sla_selscan_forward(ctypes.byref(a.q), ctypes.byref(a.given), _raw(y), pl,
                                      _raw(saved), _raw(work), n_work, raw))
     if used is not None:

@@ -199,6 +199,18 @@ __global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
   }
 }
 
+// Zeros in the rows before the first sequence and behind the last: a call without such
+// rows reads two offsets.
+template <typename W>
+__global__ __launch_bounds__(kWG) void clear_rows(const int64_t* offsets, int64_t n_seq,
+                                                  int64_t steps, int64_t dim, W* y) {
+  const int64_t lo = min(max(offsets[0], (int64_t)0), steps);
+  const int64_t hi = min(max(offsets[n_seq], lo), steps);
+  const int64_t all = (lo + steps - hi) * dim;
+  for (int64_t i = (int64_t)blockIdx.x * kWG + threadIdx.x; i < all; i += (int64_t)gridDim.x * kWG)
+    y[i < lo * dim ? i : i + (hi - lo) * dim] = W(0);
+}
+
 // The last states of all sequences; backward (BACK) the gradients of the states of
 // those without steps, which are the last states'.
 template <typename T, int K, int V, bool BACK>
@@ -601,6 +613,31 @@ sla_status sla_conv_sizes(const sla_conv_shape* shape, size_t* work_bytes) {
   if (st != SLA_OK) return st;
   if (!work_bytes) return refuse("NULL result");
   *work_bytes = work_bytes_of(*shape);
+  return SLA_OK;
+}
+
+sla_status sla_rows_clear(const int64_t* d_offsets, int64_t n_seq, int64_t steps, int64_t dim,
+                          sla_dtype dtype, void* d_y, void* stream) {
+  if (n_seq < 0 || steps < 0 || dim < 0) return refuse("negative size");
+  if (dtype != SLA_F64 && dtype != SLA_F32 && dtype != SLA_BF16 && dtype != SLA_F16)
+    return refuse("unknown dtype");
+  if ((__int128)steps * dim >= ((__int128)1 << 59)) {
+    set_error("sizes beyond what a call can index");
+    return SLA_ERR_UNSUPPORTED;
+  }
+  if (steps == 0 || dim == 0) return SLA_OK;
+  if (!d_offsets || !d_y) return refuse("offsets or y is NULL");
+  TraceRange tr("sla_rows_clear");
+  const hipStream_t s = (hipStream_t)stream;
+  const unsigned grid = (unsigned)std::min<int64_t>((steps * dim + kWG - 1) / kWG, 1024);
+  const auto clear = [&](auto word) {
+    using W = decltype(word);
+    clear_rows<W><<<grid, kWG, 0, s>>>(d_offsets, n_seq, steps, dim, (W*)d_y);
+  };
+  if (dtype == SLA_F64) clear(uint64_t());
+  else if (dtype == SLA_F32) clear(uint32_t());
+  else clear(uint16_t());
+  SLA_HIP(hipGetLastError());
   return SLA_OK;
 }
 

@@ -382,3 +382,21 @@ def test_a_planted_mistake_is_seen():
     good = K.conv(x, w, None, None, None, "silu")
     late = K.conv(x, np.roll(w, 1, 1), None, None, None, "silu")
     assert (np.abs(late["y"][0] - good["y"][0]) > good["y"][1]).any()
+
+
+def test_refusals_of_clearing_rows():
+    L, some = B.lib(), ctypes.c_void_p(64)
+    assert L.sla_rows_clear(some, -1, 4, 4, 0, some, None) == INVALID
+    assert L.sla_rows_clear(some, 1, -4, 4, 0, some, None) == INVALID
+    assert L.sla_rows_clear(some, 1, 4, -4, 0, some, None) == INVALID
+    assert L.sla_rows_clear(some, 1, 4, 4, 99, some, None) == INVALID
+    assert L.sla_rows_clear(None, 1, 4, 4, 0, some, None) == INVALID
+    assert L.sla_rows_clear(some, 1, 4, 4, 0, None, None) == INVALID
+    assert L.sla_rows_clear(some, 1, 1 << 40, 1 << 30, 0, some, None) == UNSUPPORTED
+    assert L.sla_rows_clear(some, 1, 0, 4, 0, some, None) == OK  # nothing to clear
+    y = torch.zeros(4, 3)
+    for bad in (lambda: B.sla_rows_clear(y, None), lambda: B.sla_rows_clear(y.T, torch.zeros(2).long()),
+                lambda: B.sla_rows_clear(y.long(), torch.zeros(2).long()),
+                lambda: B.sla_rows_clear(y, torch.zeros(2).long())):  # not on the GPU
+        with pytest.raises((ValueError, TypeError)):
+            bad()

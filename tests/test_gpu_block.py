@@ -321,3 +321,32 @@ def test_the_blocks_gradients_through_a_readout():
             up[name], down[name] = t + h * v, t - h * v
             diff = float((loss(up) - loss(down)) / (2 * h))
         assert abs(diff - float((g * v).sum())) <= 1e-5 * (1 + abs(diff)), name
+
+
+@pytest.mark.parametrize("dtype", [torch.float64, torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("marks", [[0, 70], [9, 9], [0, 31, 31, 61], [12, 40, 70], [70, 70], [7]])
+def test_outputs_of_padded_rows_are_zeros(dtype, marks):
+    """Memory that held NaN is handed out again: rows of no sequence are zeros all the same,
+    so that what follows may sum over them."""
+    wide = torch.float64 if dtype == torch.float64 else torch.float32
+    gen = torch.Generator().manual_seed(4)
+
+    def r(*s, t=dtype):
+        return torch.randn(*s, generator=gen, dtype=torch.float64).to(t).cuda()
+
+    x, dt, b = r(70, 23), r(70, 23), r(70, 1, 16)
+    w, A = r(23, 4, t=wide), -r(23, 16, t=wide).abs()
+    off = torch.tensor(marks, device="cuda")
+    outside = torch.ones(70, dtype=torch.bool)
+    outside[marks[0]:marks[-1]] = False
+    for f in (lambda: B.sla_conv_forward(x, w, offsets=off),
+              lambda: B.sla_selscan_forward(x, dt, A, b, b, offsets=off)):
+        dirty = [torch.full((70, 23), float("nan"), dtype=dtype, device="cuda") for _ in range(8)]
+        del dirty
+        y = f()[0].cpu()
+        assert torch.isfinite(y).all() and not y[outside].any()
+    # in C: those rows and no others
+    y = torch.full((70, 23), float("nan"), dtype=dtype, device="cuda")
+    B.sla_rows_clear(y, off)
+    y = y.cpu()
+    assert not y[outside].any() and torch.isnan(y[~outside]).all()
