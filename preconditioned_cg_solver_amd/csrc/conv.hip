@@ -699,8 +699,11 @@ sla_status sla_conv_backward(const sla_conv_shape* shape, const void* d_x, int64
   if (q.dim == 0) return SLA_OK;
   if (!d_grad_weight) return refuse("the weight's gradient is NULL");
   const bool work = !empty(q) && q.steps;
-  if (work && (!d_x || !d_weight || !d_grad_x)) return refuse("x, weight or grad_x is NULL");
-  if (work)
+  // packed rows without a sequence, whose gradients are zeros
+  const bool none = q.d_offsets && !q.n_seq && q.steps;
+  if (work && (!d_x || !d_weight)) return refuse("x or weight is NULL");
+  if ((work || none) && !d_grad_x) return refuse("grad_x is NULL");
+  if (work || none)
     for (const void* a : {d_x, d_state, d_grad_y, d_grad_last})
       if (a && (a == d_grad_x || a == d_grad_state))
         return refuse("a gradient must not be an input");
@@ -710,6 +713,9 @@ sla_status sla_conv_backward(const sla_conv_shape* shape, const void* d_x, int64
   if (need && (!d_work || work_bytes < need)) return refuse("workspace too small");
   if ((uintptr_t)d_work & 255) return refuse("the workspace must be 256-byte aligned");
   TraceRange tr("sla_conv_backward");
+  if (none && (st = sla_rows_clear(q.d_offsets, 0, q.steps, q.dim, q.dtype, d_grad_x, stream)) !=
+                  SLA_OK)
+    return st;
   return with_types(q, [&](auto t, auto taps) -> sla_status {
     using T = decltype(t);
     using C = typename Compute<T>::type;

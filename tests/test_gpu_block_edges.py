@@ -1,0 +1,41 @@
+"""Edges of a sequence block's operators on the GPU: batches of rows without a sequence, and
+values that are not finite beside rows of no sequence."""
+import pytest
+import torch
+
+from preconditioned_cg_solver_amd import autograd as AG
+from preconditioned_cg_solver_amd import binding as B
+from block_gpu import DT, make
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+SCAN = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dbias", "dh0")
+
+
+def soil(*shapes, dtype):
+    """Memory that is handed out again soon holds NaN."""
+    held = [torch.full(s, float("nan"), dtype=dtype, device="cuda") for s in shapes for _ in range(6)]
+    del held
+
+
+def none_of(mark):
+    return torch.tensor([mark], dtype=torch.int64, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d", [23, 512])
+@pytest.mark.parametrize("mark", [0, 7, 70])
+def test_conv_gradients_without_a_sequence(dtype, d, mark):
+    """Offsets of one entry: all rows are of no sequence, and their gradients are zeros."""
+    say("conv, no sequence", dtype, d, mark)
+    r, off = make(0, dtype), none_of(mark)
+    x, w, b, dy = r(70, d), r.own(d, 4), r.own(d), r(70, d)
+    soil((70, d), dtype=DT[dtype])
+    dx, dw, db, _ = B.sla_conv_backward(x, w, dy, bias=b, offsets=off)
+    assert not dx.any() and not dw.any() and not db.any()
+    x.requires_grad_(), w.requires_grad_()
+    y, last = AG.causal_conv(x, w, b, offsets=off)
+    assert not y.any() and last.shape == (0, 3, d)
+    soil((70, d), dtype=DT[dtype])
+    dx, dw = torch.autograd.grad(y.sum(), [x, w])
+    assert not dx.any() and not dw.any()
