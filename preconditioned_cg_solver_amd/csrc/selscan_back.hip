@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <utility>
 
 #include "rowsum.h"
 #include "selscan.h"
@@ -572,8 +573,10 @@ extern "C" sla_status sla_selscan_backward(const sla_selscan_shape* shape, const
   if (!q.dim) return SLA_OK;
   const sla_selscan_grads& o = *grads;
   if (!o.d_a) return refuse("a gradient is NULL");
-  if (!no_steps(q)) {
-    if (!d_saved || !d_grad_y) return refuse("the saved states or grad_y is NULL");
+  // packed rows without a sequence, whose gradients are zeros
+  const bool none = q.d_offsets && !q.n_seq && q.steps;
+  if (!no_steps(q) || none) {
+    if (!none && (!d_saved || !d_grad_y)) return refuse("the saved states or grad_y is NULL");
     if (!o.d_x || !o.d_dt || !o.d_b || !o.d_c || (in->d_z && !o.d_z))
       return refuse("a gradient is NULL");
     const void* outs[] = {o.d_x, o.d_dt, in->d_z ? o.d_z : nullptr, o.d_b, o.d_c};
@@ -588,6 +591,13 @@ extern "C" sla_status sla_selscan_backward(const sla_selscan_shape* shape, const
   if ((st = check_work(w.bytes, d_work, work_bytes)) != SLA_OK) return st;
   TraceRange tr("sla_selscan_backward");
   const hipStream_t s = (hipStream_t)stream;
+  if (none) {
+    const int64_t shared = q.groups * q.n_state;
+    for (auto [to, width] : {std::pair{o.d_x, q.dim}, {o.d_dt, q.dim},
+                             {in->d_z ? o.d_z : nullptr, q.dim}, {o.d_b, shared}, {o.d_c, shared}})
+      if (to && (st = sla_rows_clear(q.d_offsets, 0, q.steps, width, q.dtype, to, stream)) != SLA_OK)
+        return st;
+  }
   void* const h0 = in->d_h0 ? o.d_h0 : nullptr;
   if (h0 && (q.d_offsets || q.steps == 0)) {
     st = q.dtype == SLA_F64 ? leave_empty<double>(q, d_grad_last, h0, s)

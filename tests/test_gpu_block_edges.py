@@ -39,3 +39,27 @@ def test_conv_gradients_without_a_sequence(dtype, d, mark):
     soil((70, d), dtype=DT[dtype])
     dx, dw = torch.autograd.grad(y.sum(), [x, w])
     assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d,N,groups", [(24, 16, 1), (23, 3, 1), (24, 4, 3)])
+@pytest.mark.parametrize("mark", [0, 7, 70])
+def test_scan_gradients_without_a_sequence(dtype, d, N, groups, mark):
+    """Offsets of one entry: all rows are of no sequence, and their gradients are zeros."""
+    say("scan, no sequence", dtype, d, N, groups, mark)
+    r, off = make(1, dtype), none_of(mark)
+    x, dt, z, dy = r(70, d), r(70, d), r(70, d), r(70, d)
+    b, c = r(70, groups, N), r(70, groups, N)
+    A, D, bias = -r.own(d, N).abs(), r.own(d), r.own(d)
+    own = dict(D=D, z=z, dt_bias=bias, offsets=off)
+    _, _, saved = B.sla_selscan_forward(x, dt, A, b, c, **own, save=True)
+    soil((70, d), (70, groups, N), dtype=DT[dtype])
+    grads = B.sla_selscan_backward(x, dt, A, b, c, saved, dy, **own)
+    for name, g in zip(SCAN[:-1], grads):
+        assert not g.any(), name
+    leaves = [t.requires_grad_() for t in (x, dt, A, b, c, D, z, bias)]
+    y, last = AG.selective_scan(x, dt, A, b, c, D=D, z=z, dt_bias=bias, offsets=off)
+    assert not y.any() and last.shape == (0, d, N)
+    soil((70, d), (70, groups, N), dtype=DT[dtype])
+    for name, g in zip(SCAN[:-1], torch.autograd.grad(y.sum(), leaves)):
+        assert not g.any(), name
