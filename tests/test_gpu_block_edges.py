@@ -63,3 +63,46 @@ def test_scan_gradients_without_a_sequence(dtype, d, N, groups, mark):
     soil((70, d), (70, groups, N), dtype=DT[dtype])
     for name, g in zip(SCAN[:-1], torch.autograd.grad(y.sum(), leaves)):
         assert not g.any(), name
+
+
+@pytest.mark.parametrize("before,behind", [(37, 50), (5, 3), (200, 130)])
+@pytest.mark.parametrize("d,N", [(24, 16), (23, 3)])
+@pytest.mark.parametrize("what", ["gradient", "state", "rate"])
+def test_padded_rows_beside_what_is_not_finite(what, d, N, before, behind):
+    """An infinite gradient at the first row of the first sequence, an infinite state at the last
+    of the last, a rate of -infinity: rows before and behind, which hold NaN, have gradients of
+    zero, and the other results are those without such rows."""
+    say("scan, not finite beside padding", what, d, N, before, behind)
+    r = make(2, "f32")
+    n, off = 50, torch.tensor([0, 20, 50], device="cuda")
+    a = dict(x=r(n, d), dt=r(n, d), B=r(n, 1, N), C=r(n, 1, N), z=r(n, d))
+    own = dict(D=r.own(d), dt_bias=r.own(d) - 2, h0=r.own(2, d, N))
+    A, dy, dl = -r.own(d, N).abs(), r(n, d), r.own(2, d, N)
+    if what == "gradient":
+        dy[0, 3] = float("inf")
+    elif what == "state":
+        a["x"][-1, 5] = float("inf")
+    else:
+        A[7, 2] = float("-inf")
+
+    def pad(t):
+        return torch.cat([t.new_full((before, *t.shape[1:]), float("nan")), t,
+                          t.new_full((behind, *t.shape[1:]), float("nan"))])
+
+    def grads(a, off, dy):
+        first = (a["x"], a["dt"], A, a["B"], a["C"])
+        y, last, saved = B.sla_selscan_forward(*first, z=a["z"], **own, offsets=off, save=True)
+        g = B.sla_selscan_backward(*first, saved, dy, grad_last=dl, z=a["z"], **own, offsets=off)
+        return {"y": y, "last": last, **dict(zip(SCAN, g))}
+
+    plain = grads(a, off, dy)
+    padded = grads({k: pad(v) for k, v in a.items()}, off + before, pad(dy))
+    for k, g in plain.items():
+        p = padded[k]
+        if g.shape[0] == n:
+            rest = torch.cat([p[:before], p[before + n:]])
+            assert (rest == 0).all(), k  # NaN is not 0
+            p = p[before:before + n]
+        # tiles and chunks lie elsewhere: equal to fp32 rounding, and as finite
+        assert torch.equal(torch.isfinite(p), torch.isfinite(g)), k
+        assert torch.allclose(p, g, rtol=1e-4, atol=1e-3, equal_nan=True), k
