@@ -304,16 +304,15 @@ bool packs(const void* p, int64_t row, size_t bytes, int v, bool one);
 struct Way {
   int v, w, np;
 };
-template <typename T>
-Way way_of(int64_t dim, bool wide) {
-  constexpr int V = 16 / (int)sizeof(T);
+// v: elements of a pack.
+inline Way way_of(int v, int64_t dim, bool wide) {
   if (wide) {
-    if (dim <= 64 * V) return {V, 1, 1};
-    if (dim <= 256 * V) return {V, 4, 1};
-    if (dim <= 512 * V) return {V, 8, 1};
-    if (dim <= 1024 * V) return {V, 16, 1};
-    if (dim <= 2048 * V) return {V, 16, 2};
-    return {V, 16, 0};
+    if (dim <= 64 * v) return {v, 1, 1};
+    if (dim <= 256 * v) return {v, 4, 1};
+    if (dim <= 512 * v) return {v, 8, 1};
+    if (dim <= 1024 * v) return {v, 16, 1};
+    if (dim <= 2048 * v) return {v, 16, 2};
+    return {v, 16, 0};
   }
   if (dim <= 1024) return {1, 4, 4};
   if (dim <= 4096) return {1, 16, 4};
@@ -323,6 +322,9 @@ Way way_of(int64_t dim, bool wide) {
 inline int64_t groups_of(const Way& w, int64_t rows) {
   const int64_t teams = w.w == 1 ? 4 : 1;
   return std::min<int64_t>((rows + teams - 1) / teams, w.w == 16 ? kMostGroups / 2 : kMostGroups);
+}
+inline int64_t teams_of(const Way& w, int64_t rows) {
+  return groups_of(w, rows) * (w.w == 1 ? 4 : 1);
 }
 
 template <typename T, typename R, bool IN, bool BACK>
@@ -377,8 +379,8 @@ sla_status run_back(const sla_norm_shape& q, Args<T, R>& p, bool wide, void* wor
   using C = typename Compute<T>::type;
   RowSums<C> r{};
   if (q.rows) {
-    const Way way = way_of<T>(q.dim, wide);
-    r.rows = groups_of(way, q.rows) * (way.w == 1 ? 4 : 1);
+    const Way way = way_of(16 / (int)sizeof(T), q.dim, wide);
+    r.rows = teams_of(way, q.rows);
     p.part_weight = (C*)work;
     p.part_scale = scale ? p.part_weight + r.rows * q.dim : nullptr;
     const sla_status st = run<T, R, IN, true>(p, way, s);

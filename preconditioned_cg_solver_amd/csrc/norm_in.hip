@@ -34,9 +34,11 @@ sla_status check_shape(const sla_norm_shape* q) {
 
 size_t work_bytes_of(const sla_norm_shape& q) {
   if (!q.rows || !q.dim) return 0;
-  // teams of one wave are four to a workgroup
-  const size_t teams = (size_t)std::min<int64_t>(q.rows + 3, 4 * kMostGroups);
-  return align_up(teams * 2 * q.dim * (q.dtype == SLA_F64 ? 8 : 4));
+  // whether a row is read in packs or not
+  const int v = 16 / (int)dtype_bytes(q.dtype);
+  const int64_t teams = std::max(teams_of(way_of(v, q.dim, true), q.rows),
+                                 teams_of(way_of(v, q.dim, false), q.rows));
+  return align_up((size_t)teams * 2 * q.dim * (q.dtype == SLA_F64 ? 8 : 4));
 }
 
 bool packs(const void* p, int64_t row, size_t bytes, int v, bool one) {
@@ -91,7 +93,7 @@ sla_status sla_norm_in_forward(const sla_norm_shape* shape, const void* d_x, int
     const bool wide = q.dim % V == 0 && packs(d_x, x_row, sizeof(T), V, one) &&
                       packs(d_residual, residual_row, sizeof(R), V, one) &&
                       packs(d_y, 0, sizeof(T), V, one) && packs(d_r, 0, sizeof(R), V, one);
-    return run<T, R, true, false>(p, way_of<T>(q.dim, wide), (hipStream_t)stream);
+    return run<T, R, true, false>(p, way_of(V, q.dim, wide), (hipStream_t)stream);
   });
 }
 

@@ -57,7 +57,7 @@ sla_status sla_norm_out_forward(const sla_norm_shape* shape, sla_norm_order orde
                       packs(d_gate, gate_row, sizeof(T), V, one) &&
                       packs(d_residual, residual_row, sizeof(R), V, one) &&
                       packs(d_out, 0, sizeof(R), V, one);
-    return run<T, R, false, false>(p, way_of<T>(q.dim, wide), (hipStream_t)stream);
+    return run<T, R, false, false>(p, way_of(V, q.dim, wide), (hipStream_t)stream);
   });
 }
 
