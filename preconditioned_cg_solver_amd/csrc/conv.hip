@@ -80,8 +80,8 @@ __device__ __forceinline__ Run run_of(const ConvArgs<T>& p) {
   r.dense = p.offsets ? 0 : run / p.runs;
   r.from = (run - r.dense * p.runs) * p.run;
   r.to = min(r.from + p.run, p.steps);
-  const int64_t lo = p.offsets ? min(max(p.offsets[0], (int64_t)0), p.steps) : 0;
-  r.hi = p.offsets ? min(max(p.offsets[p.n_seq], lo), p.steps) : p.steps;
+  const int64_t lo = p.offsets ? row_at(p.offsets[0], 0, p.steps) : 0;
+  r.hi = p.offsets ? row_at(p.offsets[p.n_seq], lo, p.steps) : p.steps;
   r.t0 = max(r.from, lo);
   r.t1 = min(r.to, r.hi);
   r.at = p.offsets ? 0 : r.dense * p.steps;
@@ -96,8 +96,7 @@ __device__ __forceinline__ Pack<T, V> input_at(const ConvArgs<T>& p, const T* x,
   if (t >= q.begin) {
     if (t >= 0) r = *(const Pack<T, V>*)(x + t * p.x_step);
   } else if (p.state) {
-    const int64_t j = min(max(t - q.begin + K - 1, (int64_t)0), (int64_t)(K - 2));
-    r = *(const Pack<T, V>*)(p.state + (q.s * (K - 1) + j) * p.dim + col);
+    r = *(const Pack<T, V>*)(p.state + (q.s * (K - 1) + state_at(t, q.begin, K)) * p.dim + col);
   }
   return r;
 }
@@ -204,8 +203,7 @@ __global__ __launch_bounds__(kWG) void conv_forward(ConvArgs<T> p) {
 template <typename W>
 __global__ __launch_bounds__(kWG) void clear_rows(const int64_t* offsets, int64_t n_seq,
                                                   int64_t steps, int64_t dim, W* y) {
-  const int64_t lo = min(max(offsets[0], (int64_t)0), steps);
-  const int64_t hi = min(max(offsets[n_seq], lo), steps);
+  const int64_t lo = row_at(offsets[0], 0, steps), hi = row_at(offsets[n_seq], lo, steps);
   const int64_t all = (lo + steps - hi) * dim;
   for (int64_t i = (int64_t)blockIdx.x * kWG + threadIdx.x; i < all; i += (int64_t)gridDim.x * kWG)
     y[i < lo * dim ? i : i + (hi - lo) * dim] = W(0);
@@ -220,8 +218,8 @@ __global__ __launch_bounds__(kWG) void conv_last(ConvArgs<T> p) {
   Seq q{k / per, 0, p.steps};
   const int64_t col = k % per * V;
   if (p.offsets) {
-    q.begin = min(max(p.offsets[q.s], (int64_t)0), p.steps);
-    q.end = min(max(p.offsets[q.s + 1], q.begin), p.steps);
+    q.begin = row_at(p.offsets[q.s], 0, p.steps);
+    q.end = row_at(p.offsets[q.s + 1], q.begin, p.steps);
   }
   const T* const x = p.x + (p.offsets ? 0 : q.s * p.x_seq) + col;
   Pack<T, V> o[K - 1];

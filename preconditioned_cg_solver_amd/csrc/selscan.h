@@ -83,8 +83,8 @@ __device__ __forceinline__ Place place_of(const Args<T>& p) {
   w.t0 = w.part * p.chunk;
   w.t1 = min(w.t0 + p.chunk, p.steps);
   w.at = p.offsets ? 0 : w.seq * p.steps;
-  w.lo = p.offsets ? min(max(p.offsets[0], (int64_t)0), p.steps) : 0;
-  w.hi = p.offsets ? min(max(p.offsets[p.n_seq], w.lo), p.steps) : p.steps;
+  w.lo = p.offsets ? row_at(p.offsets[0], 0, p.steps) : 0;
+  w.hi = p.offsets ? row_at(p.offsets[p.n_seq], w.lo, p.steps) : p.steps;
   return w;
 }
 

@@ -1,25 +1,14 @@
-// Parts shared by the operators along sequences: where packed sequences begin,
-// the activations and their slopes, and sums over lanes.
+// Parts shared by the operators along sequences: the activations and their slopes, and
+// sums over lanes.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include "elem.h"
 #include "internal.h"
+#include "offsets.h"
 
 namespace sla {
-
-// The sequence of step t: the last one that begins at t or before (the first if
-// none does), so a valid index whatever the offsets hold.
-__device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t n, int64_t t) {
-  int64_t lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (offsets[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // Orders a wave's LDS accesses before and after it: its lanes exchange data
 // without a barrier, for LDS serves a wave's accesses in their order.
