@@ -1,11 +1,12 @@
-"""Edges of a sequence block's operators on the GPU: batches of rows without a sequence, and
-values that are not finite beside rows of no sequence."""
+"""Edges of a sequence block's operators on the GPU: batches of rows without a sequence, values that
+are not finite beside rows of no sequence, and scans long or wide enough not to be cut."""
 import pytest
 import torch
 
 from preconditioned_cg_solver_amd import autograd as AG
 from preconditioned_cg_solver_amd import binding as B
-from block_gpu import DT, make
+import block_util as K
+from block_gpu import DT, check, make, np64, offsets_of, unit_of
 from gpu_util import say
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +107,64 @@ def test_padded_rows_beside_what_is_not_finite(what, d, N, before, behind):
         # tiles and chunks lie elsewhere: equal to fp32 rounding, and as finite
         assert torch.equal(torch.isfinite(p), torch.isfinite(g)), k
         assert torch.allclose(p, g, rtol=1e-4, atol=1e-3, equal_nan=True), k
+
+
+def scan_part(a, off, dy, dl, store, pick):
+    """The reference of some channels, or sequences, of a call."""
+    q = {k: v if v is None else np64(pick(k, v)) for k, v in {**a, "dy": dy, "dlast": dl}.items()}
+    return K.scan(**q, offsets=off, unit=unit_of(store), store=store)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 192), ("f32", 190), ("f64", 192)])
+def test_long_scans_that_are_not_cut(dtype, d):
+    """Enough sequences that each is one chunk in both directions (12 waves of channels each), of
+    17 tiles and a part of one: three of them against the reference, the others without gradients so
+    that the sums over all are sums over the three."""
+    say("scan, long and uncut", dtype, d)
+    r, n, steps, N = make(3, dtype), 128, 277, 16
+    a = dict(x=r(n, steps, d), dt=r(n, steps, d), A=-r.own(d, N).abs(), B=r(n, steps, 1, N),
+             C=r(n, steps, 1, N), D=r.own(d), z=r(n, steps, d), bias=r.own(d) - 2, h0=r.own(n, d, N))
+    dy, dl = r(n, steps, d), r.own(n, d, N)
+    some = [0, 77, 127]
+    others = [s for s in range(n) if s not in some]
+    dy[others], dl[others] = 0, 0
+    kw = dict(D=a["D"], z=a["z"], dt_bias=a["bias"], h0=a["h0"])
+    first = (a["x"], a["dt"], a["A"], a["B"], a["C"])
+    assert B.sla_selscan_sizes(*first, **kw)[1] == 0  # nothing to join
+    y, last, saved = B.sla_selscan_forward(*first, **kw, save=True)
+    got = dict(zip(SCAN, B.sla_selscan_backward(*first, saved, dy, grad_last=dl, **kw)))
+    got.update(y=y, last=last)
+    whole = ("A", "D", "bias")
+    want = scan_part(a, None, dy, dl, dtype, lambda k, v: v if k in whole else v[some])
+    check({k: v if k[1:] in whole else v[some] for k, v in got.items()}, want)
+    for k in ("dx", "ddt", "dB", "dC", "dz", "dh0"):
+        assert not got[k][others].any(), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wide_packed_scans_that_are_not_cut(dtype):
+    """Enough channels that packed sequences are one chunk: the first and the last of 64 groups
+    against the reference."""
+    say("scan, wide, packed and uncut", dtype)
+    r, d, G, N, lengths = make(4, dtype), 24576, 64, 16, [40, 0, 3, 107]
+    steps, per = sum(lengths), d // G
+    off, n = offsets_of(lengths, (steps,))
+    a = dict(x=r(steps, d), dt=r(steps, d), A=-r.own(d, N).abs(), B=r(steps, G, N),
+             C=r(steps, G, N), D=r.own(d), z=r(steps, d), bias=r.own(d) - 2, h0=r.own(n, d, N))
+    dy, dl = r(steps, d), r.own(n, d, N)
+    kw = dict(D=a["D"], z=a["z"], dt_bias=a["bias"], h0=a["h0"], offsets=off)
+    first = (a["x"], a["dt"], a["A"], a["B"], a["C"])
+    assert B.sla_selscan_sizes(*first, **kw)[1] == 0  # nothing to join
+    y, last, saved = B.sla_selscan_forward(*first, **kw, save=True)
+    got = dict(zip(SCAN, B.sla_selscan_backward(*first, saved, dy, grad_last=dl, **kw)))
+    got.update(y=y, last=last)
+    for g in (0, G - 1):
+        c = slice(g * per, (g + 1) * per)
+
+        def pick(k, v):
+            if k in ("A", "D", "bias", "dA", "dD", "dbias"):
+                return v[c]
+            return v[:, g:g + 1] if k in ("B", "C", "dB", "dC") else v[:, c]
+
+        want = scan_part(a, np64(off).astype(int), dy, dl, dtype, pick)
+        check({k: pick(k, v) for k, v in got.items()}, want)
