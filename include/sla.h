@@ -594,8 +594,10 @@ sla_status sla_adamw_set_state(sla_adamw_t opt, const float *d_m, const float *d
  * Outputs must not overlap inputs or each other, but where said otherwise.
  * Packed rows before the first offset or behind the last (a batch that is padded) are of
  * no sequence: whatever they hold, the forward calls leave their outputs as they
- * were, and their gradients are zeros.  Whatever the offsets hold, no access leaves
- * the arrays.
+ * were, and their gradients are zeros; of a packed batch without sequences these are all
+ * rows.  Whatever the offsets hold, no access leaves the arrays.
+ * A backward call reads the inputs that the forward call had: where an output may
+ * take the place of an input, a backward pass that wants the old one needs a copy.
  */
 
 /* Zeros in the rows of a dense (steps, dim) d_y that are of no sequence, for outputs whose
@@ -712,7 +714,9 @@ sla_status sla_selscan_backward(const sla_selscan_shape *shape, const sla_selsca
  * with rms(v) = sqrt(mean(v^2) + eps) and silu(v) = v / (1 + exp(-v)).  residual (then 0),
  * scale (then 1) and gate (then no factor) may be NULL.  x, y and gate have `dtype`;
  * residual, r and out have `stream`, which is `dtype` or, for 16 bits, SLA_F32.  weight
- * and scale are (dim).  The norm of r is taken before r is rounded.  Rows of x, residual and
+ * and scale are (dim).  The norm of r is taken before r is rounded.  The squares are summed
+ * in fp32 (fp64 for SLA_F64) as they are: a row whose sum leaves that range has an infinite rms.
+ * Rows of x, residual and
  * gate lie x_row, .. elements apart (>= 0); all other arrays are dense.  d_rstd
  * receives 1 / rms of each row, which the backward pass starts from (NULL: none will
  * follow).
@@ -731,7 +735,7 @@ typedef struct {
 sla_status sla_norm_sizes(const sla_norm_shape *shape, size_t *work_bytes);
 
 /* Without residual and scale, r is x: then d_r has to be NULL.  d_r may be d_residual
- * where that is dense, updated in place. */
+ * where that is dense, updated in place (for inference: the backward call reads the residual). */
 sla_status sla_norm_in_forward(const sla_norm_shape *shape, const void *d_x, int64_t x_row,
                                const void *d_residual, int64_t residual_row, const void *d_scale,
                                const void *d_weight, void *d_y, void *d_r, void *d_rstd,

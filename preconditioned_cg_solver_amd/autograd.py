@@ -140,7 +140,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, offset
                    softplus: bool = True):
     """(y, last states) of the scan that binding.sla_selscan_forward describes,
     differentiable in all tensors but the offsets; besides them it saves a state every
-    16 steps (8 in float64)."""
+    16 steps (8 in float64) if any of them requires a gradient, under torch.no_grad too:
+    binding.sla_selscan_forward keeps none unless asked, and takes few steps faster so."""
     return SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, h0, offsets, softplus)
 
 

@@ -658,6 +658,9 @@ sla_status sla_conv_forward(const sla_conv_shape* shape, const void* d_x, int64_
     ConvArgs<T> p = args_of<T>(q, d_x, x_seq_stride, x_step_stride, d_weight, d_bias, d_state);
     p.y = (T*)d_y, p.last = (T*)d_last;
     const size_t b = sizeof(T);
+    // Packs where they leave no lane without channels.  8 x 8192 steps bf16, us, in packs and by
+    // elements: 64 channels 12.2 and 7.5 (backward 31.1 and 18.3), 128 13.5 and 10.4 (32.8 and
+    // 24.8), 192 14.4 and 14.8 (33.6 and 30.3), 252 15.7 and 16.3 (34.5 and 34.3).
     const bool wide =
         q.dim % M == 0 && q.dim >= kLanes * M &&
         packs(d_x, x_seq_stride, x_step_stride, b, M, q.d_offsets || q.n_seq == 1, q.steps == 1) &&

@@ -1,5 +1,5 @@
-// Storage types of the recurrences and of the AdamW step, and the type each
-// is computed in: fp64 for fp64, fp32 for everything else.
+// Storage types of the operators along sequences, of the norms and of the AdamW step,
+// and the type each is computed in: fp64 for fp64, fp32 for everything else.
 #pragma once
 
 #include <hip/hip_runtime.h>

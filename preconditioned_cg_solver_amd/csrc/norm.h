@@ -7,6 +7,13 @@
 // read again (from the caches) where they are needed a second time.  16384 x 2048 bf16 before a
 // block, fp32 stream, 70 and 107 us (5.8 and 5.7 TB/s); 16384 x 4096 bf16 after, 76 and 133
 // (5.3 and 5.0).
+//
+// Far from that, in us, forward + backward, before a block and after it.  Wide rows, whose sums
+// and next row do not fit the registers (two packs a lane of 16 waves spill 100 to 176 beside the 128
+// that there are; rows read again have their sums in memory): 4096 x 16384 bf16 84 + 397 and 101 +
+// 667 (bytes at 5.95 TB/s: 90 + 113 each), 4096 x 16384 fp32 248 + 464 and 241 + 586, 4000 x 8191 bf16
+// 75 + 183 and 113 + 288.  Narrow rows, which leave lanes without elements: 100000 x 64 bf16 25 +
+// 52 and 39 + 80 (bytes: 9 + 11 each), 100000 x 33 bf16 89 + 101 and 120 + 136.
 #pragma once
 
 #include <algorithm>

@@ -3,8 +3,8 @@
 // A wave takes 16 channels of a chunk of steps, tile by tile.  A lane has one
 // channel and NS of its states, so the states of a channel lie in 4 lanes; the
 // products that sum over them are folded between those lanes.
-// Nothing is shared between waves but the caches: a wave exchanges data through
-// LDS of its own, without barriers.
+// A wave exchanges data through LDS of its own, without barriers; but for one thing, the
+// sums over channels of the backward pass, nothing is shared between waves but the caches.
 #pragma once
 
 #include <type_traits>
@@ -16,9 +16,9 @@ namespace selscan {
 
 constexpr int kChannels = 16;  // of a wave
 constexpr int kLanes = 64;
-// Steps of a tile: the backward pass holds NS states and coefficients of each
-// of them in registers (16 steps of 4 states: 128 registers in fp32).  A state
-// is saved at every tile.
+// Steps of a tile: the backward pass holds NS states of each of them in registers (16
+// steps of 4 states: 64 registers in fp32), and the coefficients of the last few.  A
+// state is saved at every tile.
 template <typename C>
 constexpr int tile_steps() {
   return sizeof(C) == 8 ? 8 : 16;

@@ -6,7 +6,7 @@
 // its states in registers through all steps; what depends on the channel alone
 // (softplus, the gate) is worked out once per element in another sharing of the
 // tile among the lanes, and handed over through LDS of the wave.  A tile takes 486 vector
-// instructions; 8 x 2048 x 2048 x 16 states bf16, a wave a SIMD, 214 us with the vector unit
+// instructions; 8 x 2048 x 2048 x 16 states bf16, a wave a SIMD, 212 us with the vector unit
 // at work 60% of them, 16 x 2048 x 2048 332.
 #include <hip/hip_runtime.h>
 

@@ -6,12 +6,14 @@
 // (q = g a h_{t-1} = mu_t h_{t-1} needs no division and no difference.)
 //
 // A wave works a tile's states out again from the one saved at its start, keeps
-// them and the coefficients in registers, and comes back.  Sums over a channel's
-// states and over channels are folded between lanes; those over the waves of a
-// workgroup go through LDS, and those over workgroups through a workspace, so that
-// every sum is made in one order.  Bound by arithmetic: a tile takes 1647 vector
-// instructions; 8 x 2048 x 2048 x 16 states bf16, cut to two waves a SIMD, 496 us with the
-// vector unit at work 86% of them, after a first pass of 108.
+// them in registers, with the coefficients of the last steps (the others' are worked
+// out twice), and comes back.  Sums over a channel's states and over channels are folded
+// between lanes; those over the waves of a workgroup go through LDS, with one barrier a
+// tile, and those over workgroups through a workspace, so that every sum is made in one
+// order.  Bound by arithmetic: a tile takes 1634 vector instructions; 8 x 2048 x 2048 x 16
+// states bf16, cut to two waves a SIMD, 490 us with the vector unit at work 86% of them, after
+// a first pass of 106.  fp64 states leave the registers (304 bytes a lane, a wave a SIMD):
+// 8 x 2048 x 1024 x 16 states 1395 us whole, fp32 361.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
