@@ -12,8 +12,8 @@
 // tile, and those over workgroups through a workspace, so that every sum is made in one
 // order.  Bound by arithmetic: a tile takes 1634 vector instructions; 8 x 2048 x 2048 x 16
 // states bf16, cut to two waves a SIMD, 490 us with the vector unit at work 86% of them, after
-// a first pass of 106.  fp64 states leave the registers (304 bytes a lane, a wave a SIMD):
-// 8 x 2048 x 1024 x 16 states 1395 us whole, fp32 361.
+// a first pass of 106.  fp64, a wave a SIMD: 8 x 2048 x 1024 x 16 states 1395 us the whole
+// call, fp32 361.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
